@@ -1,6 +1,7 @@
 """Cases of the operators around the MoE layer: the root-mean-square norm of the
-residual stream (with its addition, the sandwich form and an E4M3 output) and
-the balance loss of the router, with their gradients.
+residual stream (with its addition, the sandwich form and an E4M3 output), the
+balance loss of the router, both with their gradients, and the gradients of
+the layer itself.
 
 ``run`` computes a case in its plain form (elementary torch operations in
 32 bits), or with ``own`` set through the package's entry points.  ``exact``
@@ -36,6 +37,13 @@ def balance_case(name, direction, N, E, K, score, segments, add):
     return dict(case, name=name) if name else case
 
 
+def layer_case(name, N, d, E, K, h, shared, add):
+    """Backward pass of the layer: shared: hidden width of the shared expert (0:
+    none); add: the logits have a gradient of their own already (a balance loss)."""
+    case = {"op": "layer", "N": N, "d": d, "E": E, "K": K, "h": h, "shared": shared, "add": add}
+    return dict(case, name=name) if name else case
+
+
 def listed():
     return [
         # one sequence being decoded: the norm in front of an E4M3 layer, latency alone
@@ -44,24 +52,24 @@ def listed():
         norm_case("norm decode", "fwd", 64, 2560, "f32", True, True, "bf16"),
         # an odd width that no vector load fits, a ragged row count, no residual
         norm_case("norm odd", "fwd", 3001, 777, "none", False, False, "f32"),
-        # the prefill batch in front of the E4M3 layer, bf16 residual stream
-        norm_case("norm prefill", "fwd", 16384, 2560, "bf16", True, True, "bf16"),
-        # the largest batch, fp32 residual stream
-        norm_case("norm large", "fwd", 65536, 2560, "f32", False, True, "f32"),
-        # one short microbatch of the narrower layer
-        norm_case("norm grad small", "bwd", 300, 2048, "bf16", False, False, "bf16"),
+        # the largest batch in front of the E4M3 layer, fp32 residual stream
+        norm_case("norm large", "fwd", 65536, 2560, "f32", True, True, "f32"),
         # odd width, sandwich form, all four gradients
         norm_case("norm grad odd", "bwd", 1025, 1001, "bf16", True, False, "f32"),
         # a training microbatch of the wide layer, fp32 residual stream, sandwich form
         norm_case("norm grad large", "bwd", 16384, 2560, "f32", True, False, "f32"),
-        # a small batch of the narrow layer, one segment: latency
+        # a small batch of the narrow layer, one segment, for logging: latency
         balance_case("balance small", "fwd", 256, 128, 8, "sigmoid", 0, False),
-        # loads and loss of the prefill batch in packed sequences, for logging
-        balance_case("balance packed", "fwd", 16384, 384, 6, "sigmoid_norm", 37, False),
         # odd sizes, softmax scores, short and empty sequences, padding between them
         balance_case("balance odd step", "step", 1237, 100, 5, "softmax", 9, False),
         # the largest training batch, gradient added to the router's own
         balance_case("balance step", "step", 65536, 384, 6, "sigmoid_norm", 16, True),
+        # a short microbatch, odd token count, of a small layer without a shared expert
+        layer_case("layer grad small", 333, 320, 20, 4, 160, 0, False),
+        # a microbatch of the narrower layer
+        layer_case("layer grad narrow", 4096, 2048, 128, 8, 768, 768, False),
+        # a training microbatch of the wide layer, balance loss on
+        layer_case("layer grad wide", 16384, 2560, 384, 6, 512, 512, True),
     ]
 
 
@@ -69,19 +77,35 @@ def log_int(rng, lo, hi):
     return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
 
 
-def draw(rng):
-    if rng.random() < 0.6:
-        direction = rng.choice(["fwd", "fwd", "bwd"])
-        quant = direction == "fwd" and rng.random() < 0.6
-        d = 128 * log_int(rng, 1, 64) if quant else log_int(rng, 64, 8192)
-        most = 65536 * 2560 if direction == "fwd" else 16384 * 2560
-        rows = log_int(rng, 1, min(65536, most // d))
-        return norm_case(None, direction, rows, d, rng.choice(["none", "bf16", "f32"]),
-                         rng.random() < 0.5, quant, rng.choice(["bf16", "f32"]))
-    E = log_int(rng, 9, 384)
-    return balance_case(None, rng.choice(["fwd", "step"]), log_int(rng, 1, 65536), E,
-                        rng.randint(1, 8), rng.choice(["sigmoid", "sigmoid_norm", "softmax"]),
+def draw_norm(rng):
+    direction = rng.choice(["fwd", "fwd", "bwd"])
+    quant = direction == "fwd" and rng.random() < 0.6
+    d = 128 * log_int(rng, 1, 64) if quant else log_int(rng, 64, 8192)
+    most = 65536 * 2560 if direction == "fwd" else 16384 * 2560
+    rows = log_int(rng, 1, min(65536, most // d))
+    return norm_case(None, direction, rows, d, rng.choice(["none", "bf16", "f32"]),
+                     rng.random() < 0.5, quant, rng.choice(["bf16", "f32"]))
+
+
+def draw_balance(rng):
+    return balance_case(None, rng.choice(["fwd", "step"]), log_int(rng, 1, 65536),
+                        log_int(rng, 9, 384), rng.randint(1, 8),
+                        rng.choice(["sigmoid", "sigmoid_norm", "softmax"]),
                         rng.choice([0, log_int(rng, 1, 64)]), rng.random() < 0.5)
+
+
+def draw_layer(rng):
+    d, h, E = 64 * log_int(rng, 1, 40), 32 * log_int(rng, 1, 24), log_int(rng, 9, 384)
+    if d * h * E > 2560 * 512 * 384:
+        h = 32
+    K = rng.randint(1, 8)
+    most = 16384 * 6 * 2560 * 512 // (K * d * h)
+    return layer_case(None, log_int(rng, 1, min(16384, most)), d, E, K, h,
+                      rng.choice([0, h, 32 * log_int(rng, 1, 16)]), rng.random() < 0.5)
+
+
+def draw(rng):
+    return rng.choice([draw_norm, draw_balance, draw_layer])(rng)
 
 
 # ---------------------------------------------------------------- inputs
@@ -142,8 +166,34 @@ def prepare_balance(case, seed):
     return s
 
 
+def prepare_layer(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rand(std, *shape):
+        return torch.empty(*shape, dtype=torch.bfloat16, device="cuda").normal_(0.0, std, generator=g)
+
+    N, d, E, K, h, hs = (case[k] for k in ("N", "d", "E", "K", "h", "shared"))
+    s = {"case": case, "x": rand(1.0, N, d), "dy": rand(1e-3, N, d),
+         "w_router": rand(1.5 / math.sqrt(d), E, d), "w_gate": rand(1.0 / math.sqrt(d), E, h, d),
+         "w_up": rand(1.0 / math.sqrt(d), E, h, d), "w_down": rand(1.0 / math.sqrt(h), E, d, h)}
+    s["ws_gate"] = rand(1.0 / math.sqrt(d), 1, hs, d) if hs else None
+    s["ws_up"] = rand(1.0 / math.sqrt(d), 1, hs, d) if hs else None
+    s["ws_down"] = rand(1.0 / math.sqrt(hs), 1, d, hs) if hs else None
+    # what the forward pass left: logits, and the experts that a bias chose which
+    # keeps the loads near each other, as the quantile update does
+    popular = 0.8 * torch.randn(E, generator=g, device="cuda")
+    s["logits"] = s["x"].float() @ s["w_router"].float().t() + popular
+    off = 0.15 * torch.randn(E, generator=g, device="cuda")
+    s["ids"] = torch.topk(s["logits"] - popular + off, K, dim=1).indices.int()
+    s["grad"] = 1e-3 * torch.randn(N, E, generator=g, device="cuda") if case["add"] else None
+    return s
+
+
+PREPARE = {"norm": prepare_norm, "balance": prepare_balance, "layer": prepare_layer}
+
+
 def prepare(case, seed):
-    return prepare_norm(case, seed) if case["op"] == "norm" else prepare_balance(case, seed)
+    return PREPARE[case["op"]](case, seed)
 
 
 # ---------------------------------------------------------------- plain forms
@@ -231,6 +281,62 @@ def plain_balance(s):
     return out
 
 
+def plain_experts_grad(x, dy, scale, w_gate, w_up, w_down):
+    """Gradients of scale * (silu(x Wg^T) * (x Wu^T)) Wd^T for every expert's rows
+    [E, rows, d]: of x, of the scale and of the three weights."""
+    wg, wu, wd = w_gate.float(), w_up.float(), w_down.float()
+    gate, up = torch.bmm(x, wg.mT.contiguous()), torch.bmm(x, wu.mT.contiguous())
+    sig = 1.0 / (1.0 + torch.exp(-gate))
+    hidden = gate * sig * up
+    back = torch.bmm(dy, wd)
+    dscale = (back * hidden).sum(-1)
+    back = back * scale.unsqueeze(-1)
+    dup = back * gate * sig
+    dgate = back * up * sig * (1.0 + gate * (1.0 - sig))
+    dx = torch.bmm(dgate, wg) + torch.bmm(dup, wu)
+    grads = [torch.bmm(dgate.mT.contiguous(), x), torch.bmm(dup.mT.contiguous(), x),
+             torch.bmm(dy.mT.contiguous(), hidden * scale.unsqueeze(-1))]
+    return dx, dscale, [t.bfloat16() for t in grads]
+
+
+def plain_layer_grad(s):
+    case = s["case"]
+    N, d, E, K = case["N"], case["d"], case["E"], case["K"]
+    x, dy = s["x"].float(), s["dy"].float()
+    ids = s["ids"].long()
+    z = torch.gather(s["logits"], 1, ids)
+    score = 1.0 / (1.0 + torch.exp(-z))
+    # the pairs of every expert side by side, padded to the longest expert's
+    flat = ids.reshape(-1)
+    loads = torch.bincount(flat, minlength=E)
+    most = int(loads.max())
+    order = torch.argsort(flat, stable=True)
+    rank = torch.arange(N * K, device="cuda") - (loads.cumsum(0) - loads)[flat[order]]
+    slot = torch.empty_like(order)
+    slot[order] = flat[order] * most + rank
+    token = torch.arange(N, device="cuda").repeat_interleave(K)
+    xp, dyp = x.new_zeros(E * most, d), x.new_zeros(E * most, d)
+    sp = x.new_zeros(E * most)
+    xp[slot], dyp[slot], sp[slot] = x[token], dy[token], score.reshape(-1)
+    dxp, dscore, grads = plain_experts_grad(xp.view(E, most, d), dyp.view(E, most, d),
+                                            sp.view(E, most), s["w_gate"], s["w_up"], s["w_down"])
+    dx = dxp.view(E * most, d)[slot].view(N, K, d).sum(1)
+    dscore = dscore.view(-1)[slot].view(N, K)
+    dz = torch.zeros_like(s["logits"]) if s["grad"] is None else s["grad"].clone()
+    dz.scatter_add_(1, ids, dscore * score * (1.0 / (1.0 + torch.exp(z))))
+    out = dict(zip(("w_gate", "w_up", "w_down"), grads))
+    if case["shared"]:
+        one = torch.ones(1, N, device="cuda")
+        dxs, _, grads = plain_experts_grad(x.unsqueeze(0), dy.unsqueeze(0), one, s["ws_gate"],
+                                           s["ws_up"], s["ws_down"])
+        dx = dx + dxs[0]
+        out.update(zip(("ws_gate", "ws_up", "ws_down"), grads))
+    out["dx"] = (dx + dz @ s["w_router"].float()).bfloat16()
+    out["w_router"] = (dz.t() @ x).bfloat16()
+    out["dlogits"] = dz
+    return out
+
+
 # ---------------------------------------------------------------- the package's operators
 def own_norm(s):
     import sigmoid_top_routing_router_amd as M
@@ -272,10 +378,21 @@ def own_balance(s):
     return out
 
 
+def own_layer_grad(s):
+    import sigmoid_top_routing_router_amd as M
+    names = ["w_router", "w_gate", "w_up", "w_down"]
+    names += ["ws_gate", "ws_up", "ws_down"] if s["case"]["shared"] else []
+    dx, dlogits, grads = M.backward(s["dy"], s["x"], M.ExpertWeights(**{n: s[n] for n in names}),
+                                    s["logits"], s["ids"], grad_logits=s["grad"])
+    return {"dx": dx, "dlogits": dlogits, **{n: getattr(grads, n) for n in names}}
+
+
 def run(state):
     case = state["case"]
     if case["op"] == "balance":
         return own_balance(state) if own else plain_balance(state)
+    if case["op"] == "layer":
+        return own_layer_grad(state) if own else plain_layer_grad(state)
     if case["direction"] == "bwd":
         return own_norm_grad(state) if own else plain_norm_grad(state)
     return own_norm(state) if own else plain_norm(state)
@@ -297,6 +414,15 @@ def work(case):
         moved = n * (2 + (stream or 2) + 2 + 2 * stream + (2 if case["post"] else 0))
         moved += weights + (2 if case["post"] else 1) * d * 4
         return {"bytes": moved, "flops": n * (28 if case["post"] else 14)}
+    if case["op"] == "layer":
+        N, d, E, K, h, hs = (case[k] for k in ("N", "d", "E", "K", "h", "shared"))
+        # x, dy and dx; the weights of the experts that are used, and every weight's gradient;
+        # the hidden products of the forward pass are formed again: eight products of each pair
+        used = E * (1.0 - (1.0 - K / E) ** N)
+        moved = 3 * N * d * 2 + N * E * 4 * (2 if case["add"] else 1) + 2 * N * K * 4 + 4 * E * d
+        moved += 6 * d * h * (used + E) + 12 * d * hs
+        flops = 16 * d * (N * K * h + N * hs) + 4 * N * E * d
+        return {"bytes": moved, "flops": flops}
     N, E, K, G = case["N"], case["E"], case["K"], max(case["segments"], 1)
     moved = N * E * 4 + N * K * 4 + G * E * 8 + G * 8
     flops = N * E * 6
@@ -379,6 +505,48 @@ def exact_balance(s, case):
     return out
 
 
+def swiglu(x, w_gate, w_up, w_down):
+    return (torch.nn.functional.silu(x @ w_gate.t()) * (x @ w_up.t())) @ w_down.t()
+
+
+def exact_layer(s, case):
+    """Automatic differentiation of <dy, y>, expert by expert."""
+    x, dy = s["x"].double(), s["dy"].double()
+    dx = torch.zeros_like(x)
+    dlogits = torch.zeros_like(s["logits"], dtype=torch.float64) if s["grad"] is None else s["grad"].double()
+    out = {n: torch.zeros(s[n].shape, dtype=torch.float32, device="cuda") for n in ("w_gate", "w_up", "w_down")}
+
+    def pull(rows, z, weights):
+        """Adds this expert's part to dx; its weights' gradients and the logits'."""
+        xe = x[rows].requires_grad_(True)
+        ws = [w.double().requires_grad_(True) for w in weights]
+        score = torch.sigmoid(z).unsqueeze(1) if z is not None else 1.0
+        y = torch.sum(dy[rows] * score * swiglu(xe, *ws))
+        grads = torch.autograd.grad(y, [xe, *ws] + ([z] if z is not None else []))
+        dx.index_add_(0, rows, grads[0])
+        return grads[1:4], grads[4] if z is not None else None
+
+    for e in range(case["E"]):
+        rows = (s["ids"] == e).any(1).nonzero().squeeze(1)
+        if rows.numel():
+            z = s["logits"][rows, e].double().requires_grad_(True)
+            grads, dz = pull(rows, z, (s["w_gate"][e], s["w_up"][e], s["w_down"][e]))
+            dlogits[rows, e] += dz
+            for n, g in zip(("w_gate", "w_up", "w_down"), grads):
+                out[n][e] = g
+    if case["shared"]:
+        grads, _ = pull(torch.arange(case["N"], device="cuda"), None,
+                        (s["ws_gate"][0], s["ws_up"][0], s["ws_down"][0]))
+        for n, g in zip(("ws_gate", "ws_up", "ws_down"), grads):
+            out[n] = g.unsqueeze(0)
+    out["dx"] = dx + dlogits @ s["w_router"].double()
+    out["w_router"] = dlogits.t() @ x
+    out["dlogits"] = dlogits
+    return out
+
+
+EXACT = {"norm": exact_norm, "balance": exact_balance, "layer": exact_layer}
+
+
 def exact(case, seed):
-    s = prepare(case, seed)
-    return exact_norm(s, case) if case["op"] == "norm" else exact_balance(s, case)
+    return EXACT[case["op"]](prepare(case, seed), case)
