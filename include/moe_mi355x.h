@@ -386,6 +386,21 @@ moe_status_t moe_forward_fp8(const moe_problem_t* p, const moe_fp8_weights_t* w,
                              void* stream);
 
 /*
+ * moe_forward_fp8_quantized - moe_forward_fp8 with x given as E4M3 codes
+ * already: x_codes [N,d] (16-byte aligned) and x_scales [N,d/128], as
+ * moe_rms_norm or moe_fp8_quantize_rows writes them.  The experts multiply
+ * these codes and the call quantises nothing; the router reads x (bf16), so x
+ * is still required (with logits_in it is not read).  With the codes that
+ * moe_fp8_quantize_rows gives for x, the result is moe_forward_fp8's, bit for
+ * bit.  Workspace, other arguments and errors as moe_forward_fp8.
+ */
+moe_status_t moe_forward_fp8_quantized(const moe_problem_t* p, const moe_fp8_weights_t* w,
+                                       const uint16_t* x, const uint8_t* x_codes,
+                                       const float* x_scales, const float* beta_in, uint16_t* y,
+                                       moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/*
  * moe_forward_noalloc - moe_forward for callers that cannot allocate device
  * memory: code under HIP graph capture, tight serving loops, harnesses that
  * forbid allocation.  The same layer as moe_forward (same kernels, bit-equal
@@ -406,6 +421,135 @@ moe_status_t moe_forward_fp8(const moe_problem_t* p, const moe_fp8_weights_t* w,
 moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
                                  const uint16_t* x, const float* beta_in, uint16_t* y,
                                  moe_aux_t* aux, void* stream);
+
+/*
+ * Root-mean-square norm of the residual stream around the layer ([K1D]: every
+ * sublayer is normalised before and after, then added to the stream).
+ *
+ * moe_rms_norm - for each of n rows of d columns, in fp32:
+ *   u = x                              without post_weight,
+ *   u = x * rsqrt(mean(x^2) + eps) * post_weight   with it (sandwich form);
+ *   r = residual + u                   (residual NULL: r = u);
+ *   y = r * rsqrt(mean(r^2) + eps) * weight.
+ * y leaves in bf16 and / or as E4M3 codes with one fp32 scale per 1 x 128
+ * group, by the rule of moe_fp8_quantize_rows applied to the fp32 y (not to
+ * its bf16 rounding): the x and the codes that moe_forward_fp8_quantized
+ * takes.  r is rounded once, to the stream's type; y is formed from the
+ * unrounded r.
+ *
+ *  x            [n,d] bf16 bits.
+ *  residual     [n,d] or NULL: bf16 bits, or fp32 with MOE_NORM_STREAM_F32.
+ *  post_weight  [d] or NULL; weight [d]: bf16 bits, or fp32 with
+ *               MOE_NORM_WEIGHT_F32.
+ *  y            [n,d] bf16 out or NULL.
+ *  residual_out [n,d] out or NULL, in the stream's type; it may be residual
+ *               itself.
+ *  codes        [n,d] out or NULL, scales [n,d/128] out (both or neither):
+ *               d % 128 == 0 and every buffer except scales 16-byte aligned.
+ * At least one output.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
+ * row of zeros with eps = 0 has no norm).  bf16 buffers 2-byte, fp32 buffers
+ * 4-byte aligned; 16-byte aligned buffers and d % 8 == 0 take the fast path.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
+ *
+ * moe_rms_norm_backward - gradients of the same function at the stored r:
+ * with a = rsqrt(mean(r^2) + eps), g = r a, h = grad_y * weight,
+ *   dr = grad_residual + a (h - g mean(h g)),
+ *   grad_residual_out = dr, grad_weight = sum over rows of grad_y * g;
+ * without post_weight grad_x = dr; with it, b = rsqrt(mean(x^2) + eps),
+ * m = x b, k = dr * post_weight:
+ *   grad_x = b (k - m mean(k m)), grad_post_weight = sum over rows of dr * m.
+ * The row sums run in fp32 in a fixed order.
+ *
+ *  grad_y       [n,d] bf16 bits.
+ *  r            [n,d] in the stream's type: residual_out of the forward call
+ *               (or its x, where there was neither residual nor post_weight).
+ *  x            [n,d] bf16 bits, with post_weight only (else NULL).
+ *  grad_residual [n,d] in the stream's type, or NULL (zero).
+ *  grad_x       [n,d] bf16 out or NULL.
+ *  grad_residual_out [n,d] out or NULL, in the stream's type.
+ *  grad_weight, grad_post_weight [d] fp32 out or NULL (the latter with
+ *               post_weight only).  n = 0 gives zeros.
+ *  workspace    moe_rms_norm_backward_workspace_bytes(n, d) bytes, 256-byte
+ *               aligned; 0 from the query means n or d out of range.
+ * No output may alias an input.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, WORKSPACE_TOO_SMALL, HIP.
+ */
+#define MOE_NORM_STREAM_F32 0x1u  /* residual, residual_out, r and their gradients are fp32 */
+#define MOE_NORM_WEIGHT_F32 0x2u  /* weight and post_weight are fp32 */
+moe_status_t moe_rms_norm(const uint16_t* x, const void* residual, const void* post_weight,
+                          const void* weight, int64_t n, int32_t d, float eps, uint32_t flags,
+                          uint16_t* y, void* residual_out, uint8_t* codes, float* scales,
+                          void* stream);
+size_t moe_rms_norm_backward_workspace_bytes(int64_t n, int32_t d);
+moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const uint16_t* x,
+                                   const void* grad_residual, const void* weight,
+                                   const void* post_weight, int64_t n, int32_t d, float eps,
+                                   uint32_t flags, uint16_t* grad_x, void* grad_residual_out,
+                                   float* grad_weight, float* grad_post_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Balance loss of the router (the auxiliary loss that [KPT] §7 and §8 set the
+ * quantile bias and the load-error injection against), over the segments of a
+ * batch: its sequences, packed or padded, or the whole batch.
+ *
+ * moe_balance_loss - with c_ge the loads of segment g (ids of its rows equal
+ * to e; ids outside [0,E) are not counted), f_ge = E c_ge / sum_e c_ge (0
+ * when the segment has no loads) and P_ge the mean over its rows of p_te:
+ *   loss = coef / n_seg * sum_g sum_e f_ge P_ge,
+ *   p = sigma(z)                     MOE_SCORE_SIGMOID (the layer's scores),
+ *   p = sigma(z) / sum_e sigma(z)    MOE_SCORE_SIGMOID_NORM,
+ *   p = softmax(z)                   MOE_SCORE_SOFTMAX.
+ * An empty segment contributes 0 and still counts in n_seg.
+ *
+ *  logits       [N,E] fp32; rows outside every segment are not used, whatever
+ *               they hold.
+ *  topk_ids     [N,K] int32, or NULL when counts_in is given (K is then not
+ *               used, but checked).
+ *  counts_in    [n_seg,E] int32 or NULL: loads to use for f instead of the
+ *               batch's own (for instance summed over several GPUs).
+ *  seg_begin, seg_end  [n_seg] int32 in device memory, or both NULL (n_seg =
+ *               1: the whole batch): segment g holds the rows seg_begin[g] ..
+ *               seg_end[g] - 1.  0 <= begin_0 <= end_0 <= begin_1 <= ... <= N;
+ *               for packed sequences pass the offsets and the offsets + 1.
+ *               Bounds are clamped to [0, N]; arrays that are not ascending
+ *               give unspecified values and no access out of range.
+ *  loss         [1] fp32 out (formed in fp64 from fp32 partial sums).
+ *  counts_out   [n_seg,E] int32 out or NULL: the batch's own loads (written
+ *               only when topk_ids is given).
+ *  mean_scores  [n_seg,E] fp32 out or NULL: P.
+ *  workspace    moe_balance_workspace_bytes(N, E, n_seg), 256-byte aligned; 0
+ *               from the query means a size out of range.
+ * 1 <= n_seg <= 2^20.  Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE,
+ * WORKSPACE_TOO_SMALL, HIP.
+ *
+ * moe_balance_loss_backward - grad_logits_out = grad_logits + grad_loss *
+ * d loss / d logits, f held constant.  Rows outside every segment get
+ * grad_logits (or 0) alone.
+ *
+ *  counts       [n_seg,E] int32: the loads that the forward call used
+ *               (counts_in, or its counts_out).
+ *  grad_loss    [1] fp32 in device memory, or NULL (1).
+ *  grad_logits  [N,E] fp32 or NULL (zero); grad_logits_out may be the same
+ *               buffer.  It must not be logits.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
+ */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SIGMOID_NORM 1
+#define MOE_SCORE_SOFTMAX 2
+size_t moe_balance_workspace_bytes(int64_t N, int32_t E, int32_t n_seg);
+moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids,
+                              const int32_t* counts_in, const int32_t* seg_begin,
+                              const int32_t* seg_end, int64_t N, int32_t E, int32_t K,
+                              int32_t n_seg, int32_t score, float coef, float* loss,
+                              int32_t* counts_out, float* mean_scores, void* workspace,
+                              size_t workspace_bytes, void* stream);
+moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* counts,
+                                       const int32_t* seg_begin, const int32_t* seg_end,
+                                       int64_t N, int32_t E, int32_t n_seg, int32_t score,
+                                       float coef, const float* grad_loss,
+                                       const float* grad_logits, float* grad_logits_out,
+                                       void* stream);
 
 /*
  * Stage timing (a profiling aid).  moe_stage_timing(1): every moe_forward

@@ -23,7 +23,8 @@ __all__ = ["route", "eqb_bias", "eqb_workspace_bytes", "EqbState", "eqb_bias_par
            "forward_workspace_bytes", "fp8_quantize_blocks", "fp8_quantize_rows",
            "Fp8ExpertWeights", "quantize_experts", "forward_fp8", "forward_fp8_workspace_bytes",
            "ExpertWeights", "MoeError", "load_library", "stage_timing", "stage_times",
-           "forward_noalloc", "pack_gateup", "pack_gateup_weights"]
+           "forward_noalloc", "pack_gateup", "pack_gateup_weights", "rms_norm",
+           "rms_norm_backward", "balance_loss", "balance_loss_backward"]
 
 AUX_FIELDS = [f for f, _ in MoeAux._fields_]
 
@@ -69,6 +70,24 @@ def _on(stream):
     kernels on that stream are done."""
     torch = _torch()
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _on_device(t, stream):
+    """_on(stream) with the device of t as the current one, for the calls that
+    take tensors of another device than the current."""
+    torch = _torch()
+    if t.device.index == torch.cuda.current_device():
+        return _on(stream)
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(t.device))
+    ctx.enter_context(_on(stream))
+    return ctx
+
+
+def _one_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
 def _bf16():
@@ -391,7 +410,8 @@ def _aux_tensors(aux, N, E, K, device):
 
 
 def _run_forward(fp8, x, wstruct, N, d, E, K, h, n_shared, h_shared, beta_in, recompute_bias,
-                 key_bits, logit_offset, logits_in, aux, workspace, out, stream, extra_flags=0):
+                 key_bits, logit_offset, logits_in, aux, workspace, out, stream, extra_flags=0,
+                 x_quant=None):
     torch = _torch()
     lib = _lib.load()
     beta_in = _dev(beta_in, "beta_in", torch.float32, (E,))
@@ -411,7 +431,10 @@ def _run_forward(fp8, x, wstruct, N, d, E, K, h, n_shared, h_shared, beta_in, re
         _dev(y, "out", _bf16(), (N, d))
         aux_t = _aux_tensors(aux, N, E, K, x.device)
         a = MoeAux(*[_ptr(aux_t.get(f)) for f in AUX_FIELDS]) if aux_t else None
-        _lib.check(fwd(C.byref(p), C.byref(wstruct), _ptr(x), _ptr(beta_in), _ptr(y),
+        given = () if x_quant is None else (_ptr(x_quant[0]), _ptr(x_quant[1]))
+        if given:
+            fwd = lib.moe_forward_fp8_quantized
+        _lib.check(fwd(C.byref(p), C.byref(wstruct), _ptr(x), *given, _ptr(beta_in), _ptr(y),
                        C.byref(a) if a is not None else None, _ptr(workspace),
                        workspace.numel() * workspace.element_size(), _stream(stream)))
     return (y, aux_t) if aux else y
@@ -491,13 +514,19 @@ def forward_noalloc(x, weights: ExpertWeights, K: int, beta_in=None,
 def forward_fp8(x, weights: Fp8ExpertWeights, K: int, beta_in=None,
                 recompute_bias: bool = False, key_bits: int = 16, logit_offset=None,
                 logits_in=None, aux=(), workspace=None, out=None, stream=None,
-                route_fused: bool = False):
+                route_fused: bool = False, x_quant=None):
     """MoE layer forward with E4M3 experts (moe_forward_fp8).  x: [N, d] bf16;
-    weights from ``quantize_experts`` or given codes and scales."""
+    weights from ``quantize_experts`` or given codes and scales.  ``x_quant``:
+    the (codes, scales) of x from ``rms_norm(..., quantize=True)`` or
+    ``fp8_quantize_rows``; the call then quantises nothing
+    (moe_forward_fp8_quantized)."""
     torch = _torch()
     x = _dev(x, "x", _bf16())
     N, d = x.shape
     u8, f32 = torch.uint8, torch.float32
+    if x_quant is not None:
+        _dev(x_quant[0], "x_quant codes", u8, (N, d))
+        _dev(x_quant[1], "x_quant scales", f32, (N, d // 128))
     wg = _dev(weights.w_gate, "w_gate", u8)
     if weights.packed:
         if wg.dim() != 4 or wg.shape[1] * 128 != d or wg.shape[3] != 128:
@@ -527,7 +556,208 @@ def forward_fp8(x, weights: Fp8ExpertWeights, K: int, beta_in=None,
     flags = (MOE_PACKED_GATEUP if weights.packed else 0) | \
         (MOE_ROUTE_FUSED if route_fused else 0)
     return _run_forward(True, x, w, N, d, E, K, h, n_shared, hs, beta_in, recompute_bias,
-                        key_bits, logit_offset, logits_in, aux, workspace, out, stream, flags)
+                        key_bits, logit_offset, logits_in, aux, workspace, out, stream, flags,
+                        x_quant)
+
+
+def _norm_weights(weight, post_weight, d):
+    torch = _torch()
+    weight = _dev(weight, "weight", (*_bf16(), torch.float32), (d,))
+    post_weight = _dev(post_weight, "post_weight", weight.dtype, (d,))
+    return weight, post_weight, _lib.MOE_NORM_WEIGHT_F32 if weight.dtype == torch.float32 else 0
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, post_weight=None,
+             quantize: bool = False, norm_out: bool = True, inplace: bool = False, stream=None):
+    """Root-mean-square norm of the residual stream (moe_rms_norm):
+    r = residual + x (``post_weight``: the normed x times it is added instead,
+    the sandwich form), y = r / rms(r) * weight.  x: [n, d] bf16; residual bf16
+    or fp32; weights bf16 or fp32, both of one type.
+
+    Returns (y, residual_out, quant): y [n, d] bf16 (None without
+    ``norm_out``); residual_out = r in the type of residual (bf16 without one),
+    or None where r is x itself; quant = (codes uint8 [n, d], fp32 scales
+    [n, d/128]) with ``quantize``, else None.  With ``inplace`` r overwrites
+    residual."""
+    torch = _torch()
+    lib = _lib.load()
+    x = _dev(x, "x", _bf16())
+    if x.dim() != 2:
+        raise ValueError("x must be [n, d]")
+    n, d = x.shape
+    weight, post_weight, flags = _norm_weights(weight, post_weight, d)
+    residual = _dev(residual, "residual", (*_bf16(), torch.float32), (n, d))
+    _one_device(x, weight=weight, post_weight=post_weight, residual=residual)
+    if inplace and residual is None:
+        raise ValueError("inplace needs residual")
+    if residual is not None and residual.dtype == torch.float32:
+        flags |= _lib.MOE_NORM_STREAM_F32
+    with _on_device(x, stream):
+        dev = x.device
+        y = torch.empty((n, d), dtype=torch.bfloat16, device=dev) if norm_out else None
+        r = None
+        if inplace:
+            r = residual
+        elif residual is not None:
+            r = torch.empty_like(residual)
+        elif post_weight is not None:
+            r = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+        codes = scales = None
+        if quantize:
+            codes = torch.empty((n, d), dtype=torch.uint8, device=dev)
+            scales = torch.empty((n, d // 128), dtype=torch.float32, device=dev)
+        _lib.check(lib.moe_rms_norm(_ptr(x), _ptr(residual), _ptr(post_weight), _ptr(weight), n,
+                                    d, eps, flags, _ptr(y), _ptr(r), _ptr(codes), _ptr(scales),
+                                    _stream(stream)))
+    return y, r, (codes, scales) if quantize else None
+
+
+def rms_norm_backward(grad_y, r, weight, eps: float = 1e-6, grad_residual=None, x=None,
+                      post_weight=None, weight_grads: bool = True, workspace=None, stream=None):
+    """Gradients of rms_norm (moe_rms_norm_backward).  grad_y: [n, d] bf16; r:
+    the residual_out of the forward call, or its x where that was None;
+    grad_residual: gradient that reaches r from elsewhere, in r's type; x and
+    post_weight: both, for the sandwich form.
+
+    Returns (grad_x bf16, grad_residual in r's type, grad_weight fp32 [d],
+    grad_post_weight fp32 [d] or None); without post_weight and with a bf16 r
+    the first two are one tensor.  Without ``weight_grads`` the last two are
+    None."""
+    torch = _torch()
+    lib = _lib.load()
+    grad_y = _dev(grad_y, "grad_y", _bf16())
+    if grad_y.dim() != 2:
+        raise ValueError("grad_y must be [n, d]")
+    n, d = grad_y.shape
+    weight, post_weight, flags = _norm_weights(weight, post_weight, d)
+    r = _dev(r, "r", (*_bf16(), torch.float32), (n, d))
+    grad_residual = _dev(grad_residual, "grad_residual", r.dtype, (n, d))
+    x = _dev(x, "x", _bf16(), (n, d))
+    if (x is None) != (post_weight is None):
+        raise ValueError("x belongs to post_weight: both or neither")
+    _one_device(grad_y, weight=weight, post_weight=post_weight, r=r, grad_residual=grad_residual,
+                x=x, workspace=workspace)
+    f32 = r.dtype == torch.float32
+    if f32:
+        flags |= _lib.MOE_NORM_STREAM_F32
+    with _on_device(grad_y, stream):
+        dev = grad_y.device
+        dres = torch.empty((n, d), dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
+        shared = post_weight is None and not f32
+        dx = None if shared else torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+        dw = torch.empty((d,), dtype=torch.float32, device=dev) if weight_grads else None
+        dp = torch.empty((d,), dtype=torch.float32, device=dev) \
+            if weight_grads and post_weight is not None else None
+        if workspace is None:
+            need = int(lib.moe_rms_norm_backward_workspace_bytes(n, d))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _lib.check(lib.moe_rms_norm_backward(
+            _ptr(grad_y), _ptr(r), _ptr(x), _ptr(grad_residual), _ptr(weight), _ptr(post_weight),
+            n, d, eps, flags, _ptr(dx), _ptr(dres), _ptr(dw), _ptr(dp), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dres if shared else dx, dres, dw, dp
+
+
+def _segments(segments, first):
+    """(begin, end, n_seg) of the segments argument of the balance loss."""
+    torch = _torch()
+    if segments is None:
+        return None, None, 1
+    if isinstance(segments, torch.Tensor):
+        cu = _dev(segments, "segments", torch.int32)
+        if cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError("segments must be [n_seg + 1] offsets or (begin, end)")
+        begin, end = cu[:-1], cu[1:]
+    else:
+        begin, end = segments
+        begin = _dev(begin, "segments begin", torch.int32)
+        end = _dev(end, "segments end", torch.int32, (begin.numel(),))
+    _one_device(first, segments=begin, segments_end=end)
+    return begin, end, begin.numel()
+
+
+def _score(score):
+    if score not in _lib.SCORES:
+        raise ValueError(f"score must be one of {sorted(_lib.SCORES)}, got {score!r}")
+    return _lib.SCORES[score]
+
+
+def balance_loss(logits, topk_ids=None, coef: float = 1e-2, score: str = "sigmoid_norm",
+                 segments=None, counts=None, workspace=None, stream=None):
+    """Balance loss of the router (moe_balance_loss): coef times the mean over
+    the segments of sum_e f_e P_e, with f_e = E c_e / sum c over the segment's
+    loads and P_e the mean score of its rows (``score``: "sigmoid",
+    "sigmoid_norm" or "softmax" of the logits).  ``segments``: int32 offsets
+    [n_seg + 1] of packed sequences, or (begin, end) int32 [n_seg] each, for
+    padded ones; None: the batch is one segment.  ``counts``: int32 [n_seg, E]
+    loads to use in place of the batch's own.
+
+    Returns (loss fp32 [1], counts int32 [n_seg, E] of the batch's own
+    topk_ids (the given ones without topk_ids), mean scores fp32
+    [n_seg, E])."""
+    torch = _torch()
+    lib = _lib.load()
+    logits = _dev(logits, "logits", torch.float32)
+    N, E = logits.shape
+    topk_ids = _dev(topk_ids, "topk_ids", torch.int32)
+    K = 1
+    if topk_ids is not None:
+        if topk_ids.dim() != 2 or topk_ids.shape[0] != N:
+            raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, expected ({N}, K)")
+        K = topk_ids.shape[1]
+    begin, end, n_seg = _segments(segments, logits)
+    counts = _dev(counts, "counts", torch.int32, (n_seg, E))
+    if topk_ids is None and counts is None:
+        raise ValueError("topk_ids or counts is required")
+    _one_device(logits, topk_ids=topk_ids, counts=counts, workspace=workspace)
+    which = _score(score)
+    with _on_device(logits, stream):
+        dev = logits.device
+        loss = torch.empty((1,), dtype=torch.float32, device=dev)
+        mean = torch.empty((n_seg, E), dtype=torch.float32, device=dev)
+        own = None
+        if topk_ids is not None:
+            own = torch.empty((n_seg, E), dtype=torch.int32, device=dev)
+        if workspace is None:
+            need = int(lib.moe_balance_workspace_bytes(N, E, n_seg))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _lib.check(lib.moe_balance_loss(
+            _ptr(logits), _ptr(topk_ids), _ptr(counts), _ptr(begin), _ptr(end), N, E, K, n_seg,
+            which, coef, _ptr(loss), _ptr(own), _ptr(mean), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
+    return loss, counts if own is None else own, mean
+
+
+def balance_loss_backward(logits, counts, coef: float = 1e-2, score: str = "sigmoid_norm",
+                          segments=None, grad_loss=None, grad_logits=None, inplace: bool = False,
+                          stream=None):
+    """Gradient of balance_loss with respect to the logits
+    (moe_balance_loss_backward), the loads held constant: grad_logits (None:
+    zero) + grad_loss (fp32 [1] on the device, None: 1) * d loss / d logits,
+    fp32 [N, E].  ``counts``: the loads that the loss was formed with.  With
+    ``inplace`` the gradient is added into grad_logits itself."""
+    torch = _torch()
+    lib = _lib.load()
+    logits = _dev(logits, "logits", torch.float32)
+    N, E = logits.shape
+    begin, end, n_seg = _segments(segments, logits)
+    counts = _dev(counts, "counts", torch.int32, (n_seg, E))
+    if counts is None:
+        raise ValueError("counts is required")
+    grad_loss = _dev(grad_loss, "grad_loss", torch.float32)
+    if grad_loss is not None and grad_loss.numel() != 1:
+        raise ValueError("grad_loss must hold one value")
+    grad_logits = _dev(grad_logits, "grad_logits", torch.float32, (N, E))
+    if inplace and grad_logits is None:
+        raise ValueError("inplace needs grad_logits")
+    _one_device(logits, counts=counts, grad_loss=grad_loss, grad_logits=grad_logits)
+    which = _score(score)
+    with _on_device(logits, stream):
+        out = grad_logits if inplace else torch.empty_like(logits)
+        _lib.check(lib.moe_balance_loss_backward(
+            _ptr(logits), _ptr(counts), _ptr(begin), _ptr(end), N, E, n_seg, which, coef,
+            _ptr(grad_loss), _ptr(grad_logits), _ptr(out), _stream(stream)))
+    return out
 
 
 def stage_timing(enable=True):

@@ -17,6 +17,9 @@ MOE_RECOMPUTE_BIAS = 0x1
 MOE_KEY32 = 0x2
 MOE_PACKED_GATEUP = 0x4
 MOE_ROUTE_FUSED = 0x8
+MOE_NORM_STREAM_F32 = 0x1
+MOE_NORM_WEIGHT_F32 = 0x2
+SCORES = {"sigmoid": 0, "sigmoid_norm": 1, "softmax": 2}  # MOE_SCORE_*
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
                 3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_HIP"}
@@ -27,7 +30,9 @@ EXPORTED = ["moe_route", "moe_eqb_workspace_bytes", "moe_eqb_bias", "moe_eqb_sta
             "moe_forward_workspace_bytes", "moe_forward", "moe_pack_gateup_weights",
             "moe_fp8_quantize_blocks",
             "moe_fp8_quantize_rows", "moe_forward_fp8_workspace_bytes", "moe_forward_fp8",
-            "moe_forward_noalloc",
+            "moe_forward_noalloc", "moe_forward_fp8_quantized",
+            "moe_rms_norm", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
+            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
             "moe_status_string",
             "moe_last_error_message", "moe_abi_version", "moe_stage_timing",
             "moe_stage_times", "moe_stage_name"]
@@ -131,6 +136,26 @@ def load(path: str = LIB_PATH):
     lib.moe_forward_noalloc.argtypes = [C.POINTER(MoeProblem), C.POINTER(MoeWeights), vp, vp, vp,
                                         C.POINTER(MoeAux), vp]
     lib.moe_forward_noalloc.restype = C.c_int
+    lib.moe_forward_fp8_quantized.argtypes = [C.POINTER(MoeProblem), C.POINTER(MoeFp8Weights), vp,
+                                              vp, vp, vp, vp, C.POINTER(MoeAux), vp, C.c_size_t,
+                                              vp]
+    lib.moe_forward_fp8_quantized.restype = C.c_int
+    f32, u32 = C.c_float, C.c_uint32
+    lib.moe_rms_norm.argtypes = [vp, vp, vp, vp, i64, i32, f32, u32, vp, vp, vp, vp, vp]
+    lib.moe_rms_norm.restype = C.c_int
+    lib.moe_rms_norm_backward_workspace_bytes.argtypes = [i64, i32]
+    lib.moe_rms_norm_backward_workspace_bytes.restype = C.c_size_t
+    lib.moe_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, f32, u32, vp, vp, vp,
+                                          vp, vp, C.c_size_t, vp]
+    lib.moe_rms_norm_backward.restype = C.c_int
+    lib.moe_balance_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.moe_balance_workspace_bytes.restype = C.c_size_t
+    lib.moe_balance_loss.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, vp, vp, vp,
+                                     vp, C.c_size_t, vp]
+    lib.moe_balance_loss.restype = C.c_int
+    lib.moe_balance_loss_backward.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, f32, vp, vp, vp,
+                                              vp]
+    lib.moe_balance_loss_backward.restype = C.c_int
     lib.moe_status_string.argtypes = [C.c_int]
     lib.moe_status_string.restype = C.c_char_p
     lib.moe_last_error_message.argtypes = []

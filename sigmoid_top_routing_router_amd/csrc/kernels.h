@@ -166,6 +166,49 @@ hipError_t launch_lei(const float* Z, const int32_t* ids, const float* G, int64_
                       int K, float lam, float tau, float* Gout, float* dZ, float* inj_out,
                       int32_t* counts, float* inj, hipStream_t stream);
 
+// ---------------------------------------------------------------- norm
+// Root-mean-square norm of n rows of d columns (1 <= d <= kNormMaxD):
+// r = residual + (post_w ? post_w * x / rms(x) : x), y = w * r / rms(r); any of
+// y, r_out (of the residual's type) and codes / scales may be NULL.  codes
+// need d % 128 == 0 and every pointer 16-byte aligned.
+constexpr int kNormMaxD = 8192;
+hipError_t launch_rms_norm(const uint16_t* x, const void* residual, const void* post_w,
+                           const void* w, int64_t n, int d, float eps, bool stream_f32,
+                           bool weight_f32, uint16_t* y, void* r_out, uint8_t* codes,
+                           float* scales, hipStream_t stream);
+// Its backward pass over the rows r that were normalised (x: the input of the
+// first norm, with post_w only); dres NULL: zero.  part holds
+// rms_norm_grad_blocks(n, d) * (post_w ? 2 : 1) * d floats.
+int rms_norm_grad_blocks(int64_t n, int d);
+hipError_t launch_rms_norm_grad(const uint16_t* dy, const void* r, const uint16_t* x,
+                                const void* dres, const void* w, const void* post_w, int64_t n,
+                                int d, float eps, bool stream_f32, bool weight_f32, uint16_t* dx,
+                                void* dr_out, float* dw, float* dw_post, float* part,
+                                hipStream_t stream);
+
+// ---------------------------------------------------------------- balance loss
+// Workspace: partial rows of score sums and loads [balance_slots(N, G)][E],
+// the segments' terms [G][ceil(E / 64)][2], and a counter.
+struct BalanceWork {
+  float* sums;
+  uint32_t* loads;
+  double* terms;
+  uint32_t* ticket;
+};
+int64_t balance_slots(int64_t N, int G);
+// begin / end NULL: one segment, the whole batch.  ids NULL: counts_in is
+// required.  score: 0 sigmoid, 1 normalised sigmoid, 2 softmax.
+hipError_t launch_balance_loss(const float* Z, const int32_t* ids, const int32_t* counts_in,
+                               const int32_t* begin, const int32_t* end, int64_t N, int E, int K,
+                               int G, int score, float coef, const BalanceWork& w, float* loss,
+                               int32_t* counts_out, float* mean_out, hipStream_t stream);
+// grad_out = grad_in (NULL: zero; may be grad_out) + the gradient of the loss
+// times grad_loss[0] (NULL: 1).
+hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int32_t* begin,
+                               const int32_t* end, int64_t N, int E, int G, int score, float coef,
+                               const float* grad_loss, const float* grad_in, float* grad_out,
+                               hipStream_t stream);
+
 // ---------------------------------------------------------------- FP8
 // Rows of X [N,C] bf16 (C % 128 == 0) -> E4M3 codes Q [N,C] and one fp32
 // scale per 1 x 128 group, S [N, C/128].

@@ -226,6 +226,10 @@ struct Experts {
   const uint16_t* w_router = nullptr;
   const moe_weights_t* b = nullptr;
   const moe_fp8_weights_t* q = nullptr;
+  // E4M3 experts with x given as codes and 1 x 128 scales (else x is
+  // quantised here)
+  const uint8_t* x_codes = nullptr;
+  const float* x_scales = nullptr;
 };
 
 // ---- stage timing: S+1 boundary events per recorded call
@@ -381,8 +385,10 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
   // little arithmetic: its routed GEMMs stream the weights straight into
   // registers, and its dense products are split over many small blocks.
   const bool small = N <= moe::kSmallBatch;
-  if (ex.fp8)
+  if (ex.fp8 && !ex.x_codes)
     MOE_TRY_HIP(moe::launch_quant_rows(x, N, d, l.xq, l.xs, st), "moe_forward: quantise x");
+  const uint8_t* xq = ex.x_codes ? ex.x_codes : l.xq;
+  const float* xs = ex.x_codes ? ex.x_scales : l.xs;
   SideJoin sj;
   const bool folded = shared_folded(*p);
   SideStream* side = (shared && !folded && !ex.in_order) ? side_stream() : nullptr;
@@ -421,7 +427,7 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
       Z = zout;
     }
     if (shared_here && ex.fp8)
-      MOE_TRY_HIP(moe::launch_shared_gateup_dense_small(l.xq, l.xs, N, d, q->ws_gate, q->ss_gate,
+      MOE_TRY_HIP(moe::launch_shared_gateup_dense_small(xq, xs, N, d, q->ws_gate, q->ss_gate,
                                                         q->ws_up, q->ss_up, hs, true, l.Hsq,
                                                         l.Hss, l.part, st),
                   "moe_forward: shared gate/up");
@@ -436,7 +442,7 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
       MOE_TRY_HIP(hipMemcpyAsync(A.logits, Z, (size_t)N * E * 4, hipMemcpyDeviceToDevice, st),
                   "moe_forward: logits copy");
     if (shared_here && ex.fp8)
-      MOE_TRY_HIP(moe::launch_gateup_fp8(l.xq, l.xs, N, nullptr, 1, nullptr, nullptr, 0, N,
+      MOE_TRY_HIP(moe::launch_gateup_fp8(xq, xs, N, nullptr, 1, nullptr, nullptr, 0, N,
                                          q->ws_gate, q->ss_gate, q->ws_up, q->ss_up, d, hs,
                                          l.Hsq, l.Hss, st),
                   "moe_forward: shared gate/up");
@@ -447,7 +453,7 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
   } else {
     float* zout = A.logits ? A.logits : l.Z;
     if (shared_here && ex.fp8)
-      MOE_TRY_HIP(moe::launch_router_shared_gateup_fp8(x, l.xq, l.xs, N, d, ex.w_router,
+      MOE_TRY_HIP(moe::launch_router_shared_gateup_fp8(x, xq, xs, N, d, ex.w_router,
                                                        p->logit_offset, E, zout, q->ws_gate,
                                                        q->ss_gate, q->ws_up, q->ss_up, hs,
                                                        l.Hsq, l.Hss, st, sel),
@@ -473,7 +479,7 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
     if (small) {
       // the split-K kernels of a small batch, with partial sums of their own
       if (ex.fp8)
-        MOE_TRY_HIP(moe::launch_shared_gateup_dense_small(l.xq, l.xs, N, d, q->ws_gate,
+        MOE_TRY_HIP(moe::launch_shared_gateup_dense_small(xq, xs, N, d, q->ws_gate,
                                                           q->ss_gate, q->ws_up, q->ss_up, hs,
                                                           true, l.Hsq, l.Hss, l.part_side, s2),
                     "moe_forward: shared gate/up");
@@ -488,7 +494,7 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
                       ex.fp8 ? q->ss_down : nullptr, hs, ex.fp8, l.sh, l.part_side, s2),
                   "moe_forward: shared down");
     } else if (ex.fp8) {
-      MOE_TRY_HIP(moe::launch_gateup_fp8(l.xq, l.xs, N, nullptr, 1, nullptr, nullptr, 0, N,
+      MOE_TRY_HIP(moe::launch_gateup_fp8(xq, xs, N, nullptr, 1, nullptr, nullptr, 0, N,
                                          q->ws_gate, q->ss_gate, q->ws_up, q->ss_up, d, hs,
                                          l.Hsq, l.Hss, s2),
                   "moe_forward: shared gate/up");
@@ -578,12 +584,12 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
   }
   const moe::SharedFold* sf = folded ? &fold : nullptr;
   if (ex.fp8 && small)
-    MOE_TRY_HIP(moe::launch_gateup_fp8_small(l.xq, l.xs, N, pw.sorted_src, K, pw.tiles,
+    MOE_TRY_HIP(moe::launch_gateup_fp8_small(xq, xs, N, pw.sorted_src, K, pw.tiles,
                                              pw.n_tiles, l.max_tiles, 0, q->w_gate, q->s_gate,
                                              q->w_up, q->s_up, d, h, l.Hq, l.Hqs, st, packed, sf),
                 "moe_forward: gate/up");
   else if (ex.fp8)
-    MOE_TRY_HIP(moe::launch_gateup_fp8(l.xq, l.xs, N, pw.sorted_src, K, pw.tiles, pw.n_tiles,
+    MOE_TRY_HIP(moe::launch_gateup_fp8(xq, xs, N, pw.sorted_src, K, pw.tiles, pw.n_tiles,
                                        l.max_tiles, 0, q->w_gate, q->s_gate, q->w_up, q->s_up, d,
                                        h, l.Hq, l.Hqs, st, packed),
                 "moe_forward: gate/up");
@@ -950,10 +956,10 @@ moe_status_t moe::set_error(moe_status_t s, const char* msg) { return fail(s, "%
 
 extern "C" {
 
-moe_status_t moe_forward_fp8(const moe_problem_t* p, const moe_fp8_weights_t* w,
-                             const uint16_t* x, const float* beta_in, uint16_t* y,
-                             moe_aux_t* aux, void* workspace, size_t workspace_bytes,
-                             void* stream) {
+static moe_status_t forward_fp8(const moe_problem_t* p, const moe_fp8_weights_t* w,
+                                const uint16_t* x, const uint8_t* x_codes, const float* x_scales,
+                                const float* beta_in, uint16_t* y, moe_aux_t* aux,
+                                void* workspace, size_t workspace_bytes, void* stream) {
   moe_status_t s = check_problem_fp8(p);
   if (s != MOE_OK) return s;
   if (!w || !x || !y) return fail(MOE_ERR_INVALID_ARGUMENT, "weights, x and y are required");
@@ -972,7 +978,30 @@ moe_status_t moe_forward_fp8(const moe_problem_t* p, const moe_fp8_weights_t* w,
   ex.fp8 = true;
   ex.w_router = w->w_router;
   ex.q = w;
+  ex.x_codes = x_codes;
+  ex.x_scales = x_scales;
   return forward_impl(p, ex, x, beta_in, y, aux, workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_forward_fp8(const moe_problem_t* p, const moe_fp8_weights_t* w,
+                             const uint16_t* x, const float* beta_in, uint16_t* y,
+                             moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  return forward_fp8(p, w, x, nullptr, nullptr, beta_in, y, aux, workspace, workspace_bytes,
+                     stream);
+}
+
+moe_status_t moe_forward_fp8_quantized(const moe_problem_t* p, const moe_fp8_weights_t* w,
+                                       const uint16_t* x, const uint8_t* x_codes,
+                                       const float* x_scales, const float* beta_in, uint16_t* y,
+                                       moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  if (!x_codes || !x_scales)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "x_codes and x_scales are required");
+  if (!aligned(x_codes, 16) || !aligned(x_scales, 4))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "x_codes must be 16-byte and x_scales 4-byte aligned");
+  return forward_fp8(p, w, x, x_codes, x_scales, beta_in, y, aux, workspace, workspace_bytes,
+                     stream);
 }
 
 moe_status_t moe_fp8_quantize_blocks(const uint16_t* w, int64_t count, int32_t rows,

@@ -1,0 +1,539 @@
+// Root-mean-square norm of the residual stream, with its addition, the
+// sandwich form and an E4M3 output, and its backward pass.
+//
+// "Kolibri 1 im Detail" (block description): every sublayer is normalised
+// before and after, then added to the residual stream.  One pass over a row:
+//   u = x                              or x * rsqrt(mean(x^2) + eps) * w_post
+//   r = residual + u
+//   y = r * rsqrt(mean(r^2) + eps) * w
+// y leaves in bf16 and / or, per 1 x 128 group, as s = amax / 448 and the
+// E4M3 code of y / s; the codes are formed from the fp32 y (one rounding, not
+// two).  Backward, with a = rsqrt(mean(r^2) + eps), n = r a, h = dy w:
+//   dr = dres + a (h - n mean(h n)),  dw = sum_t dy n,  dresidual = dr,
+// and through the sandwich norm of x (b = rsqrt(mean(x^2) + eps), m = x b,
+// k = dr w_post): dx = b (k - m mean(k m)), dw_post = sum_t dr m.  The two
+// reciprocal roots are formed again from r and x, which are read anyway, so
+// the forward pass keeps nothing for it.
+//
+// All statistics, sums and the row itself are fp32; a row is read once and
+// kept in registers.  TPR threads own a row (a wave or a block of 256), each
+// NV pieces of VEC consecutive columns: VEC = 8 (16-byte loads of bf16) when
+// the width is a multiple of 8 and every pointer 16-byte aligned, else VEC = 1.
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2_t v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ uint16_t one_bf16(float a) {
+  return __builtin_bit_cast(uint16_t, (__bf16)a);
+}
+
+// VEC consecutive values of a bf16 or fp32 row at column c.
+template <int VEC>
+__device__ __forceinline__ void load_bf16(const uint16_t* p, float* v) {
+  if constexpr (VEC == 8) {
+    const u32x4_t t = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(t[i] << 16);
+      v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
+    }
+  } else {
+    v[0] = bf16_bits_to_f32(*p);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float* p, float* v) {
+  if constexpr (VEC == 8) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p);
+    const f32x4_t b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+    v[0] = *p;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_any(const void* base, int64_t at, bool f32, float* v) {
+  if (f32) load_f32<VEC>(reinterpret_cast<const float*>(base) + at, v);
+  else load_bf16<VEC>(reinterpret_cast<const uint16_t*>(base) + at, v);
+}
+template <int VEC>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const float* v) {
+  if constexpr (VEC == 8) {
+    const u32x4_t t = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                       pack_bf16(v[6], v[7])};
+    *reinterpret_cast<u32x4_t*>(p) = t;
+  } else {
+    *p = one_bf16(v[0]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_f32(float* p, const float* v) {
+  if constexpr (VEC == 8) {
+    const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    *reinterpret_cast<f32x4_t*>(p) = a;
+    *reinterpret_cast<f32x4_t*>(p + 4) = b;
+  } else {
+    *p = v[0];
+  }
+}
+
+// Sum over the wave: DPP inside each 16-lane row, then the four rows.
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += __uint_as_float(dpp_u32<kDppQuadSwap1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppQuadSwap2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppRowHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppRowMirror>(__float_as_uint(v)));
+  const uint32_t u = __float_as_uint(v);
+  return (__uint_as_float(readlane_u32(u, 0)) + __uint_as_float(readlane_u32(u, 16))) +
+         (__uint_as_float(readlane_u32(u, 32)) + __uint_as_float(readlane_u32(u, 48)));
+}
+
+// Sums of NS values over the TPR threads of a row.  `part` holds NS floats per
+// wave of the block; it is not written again before the next barrier.
+template <int TPR, int NS>
+__device__ __forceinline__ void row_sums(float (&v)[NS], float* part) {
+#pragma unroll
+  for (int i = 0; i < NS; ++i) v[i] = wave_sum_f32(v[i]);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) part[(threadIdx.x >> 6) * NS + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += part[w * NS + i];
+      v[i] = s;
+    }
+  }
+}
+
+constexpr float kE4M3Max = 448.0f;
+
+struct NormArgs {
+  const uint16_t* x;
+  const void* residual;
+  const void* post_w;
+  const void* w;
+  int64_t n;
+  int d;
+  float eps;
+  bool stream_f32, weight_f32;
+  uint16_t* y;
+  void* r_out;
+  uint8_t* codes;
+  float* scales;
+};
+
+template <int TPR, int NV, int VEC, bool POST>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
+  constexpr int BT = TPR < 256 ? 256 : TPR;
+  __shared__ float part[2][BT / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (BT / TPR) + threadIdx.x / TPR;
+  // a wave past the last row leaves whole (TPR = 64: no barrier below)
+  if (row >= a.n) return;
+  const int d = a.d;
+  const int64_t base = row * d;
+  const float inv_d = 1.0f / (float)d;
+  float v[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + t) * VEC;
+    if (c < d) {
+      load_bf16<VEC>(a.x + base + c, v[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j][i] = 0.0f;
+    }
+  }
+  if constexpr (POST) {
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) ss[0] += v[j][i] * v[j][i];
+    row_sums<TPR>(ss, part[0]);
+    const float b = rsqrtf(ss[0] * inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      if (c < d) {
+        float w[VEC];
+        load_any<VEC>(a.post_w, c, a.weight_f32, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * b * w[i];
+      }
+    }
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      if (c < d) {
+        float q[VEC];
+        load_any<VEC>(a.residual, base + c, a.stream_f32, q);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j][i] += q[i];
+      }
+    }
+  }
+  if (a.r_out) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      if (c < d) {
+        if (a.stream_f32) store_f32<VEC>(reinterpret_cast<float*>(a.r_out) + base + c, v[j]);
+        else store_bf16<VEC>(reinterpret_cast<uint16_t*>(a.r_out) + base + c, v[j]);
+      }
+    }
+  }
+  float ss[1] = {0.0f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) ss[0] += v[j][i] * v[j][i];
+  row_sums<TPR>(ss, part[1]);
+  const float s = rsqrtf(ss[0] * inv_d + a.eps);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + t) * VEC;
+    if (c < d) {
+      float w[VEC];
+      load_any<VEC>(a.w, c, a.weight_f32, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * s * w[i];
+      if (a.y) store_bf16<VEC>(a.y + base + c, v[j]);
+    }
+    if constexpr (VEC == 8) {
+      // 16 neighbouring lanes hold one 1 x 128 group (d % 128 == 0 here), all
+      // of them inside the row or none
+      if (a.codes) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
+        m = row16_max_f32(m);
+        const float sc = m / kE4M3Max;
+        u32x2_t q = {0u, 0u};
+        if (m != 0.0f) {
+          float z[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            z[i] = fminf(fmaxf(v[j][i] / sc, -kE4M3Max), kE4M3Max);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            int pk = __builtin_amdgcn_cvt_pk_fp8_f32(z[4 * k], z[4 * k + 1], 0, false);
+            pk = __builtin_amdgcn_cvt_pk_fp8_f32(z[4 * k + 2], z[4 * k + 3], pk, true);
+            q[k] = (uint32_t)pk;
+          }
+        }
+        if (c < d) {
+          *reinterpret_cast<u32x2_t*>(a.codes + base + c) = q;
+          if ((threadIdx.x & 15) == 0) a.scales[(base + c) >> 7] = (m != 0.0f) ? sc : 0.0f;
+        }
+      }
+    }
+  }
+}
+
+struct NormGradArgs {
+  const uint16_t* dy;
+  const void* r;
+  const uint16_t* x;
+  const void* dres;
+  const void* w;
+  const void* post_w;
+  int64_t n;
+  int d;
+  float eps;
+  bool stream_f32, weight_f32;
+  uint16_t* dx;
+  void* dr_out;
+  float* part_w;     // [blocks][d] partial sums of dw, then (POST) of dw_post
+};
+
+// Grid-stride over the rows; a thread keeps the sums of its own columns over
+// the block's rows, and every block leaves one partial row of them (its
+// rows' groups added in order through LDS), so the result does not depend on
+// the order in which blocks run.
+template <int TPR, int NV, int VEC, bool POST>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int BT = TPR < 256 ? 256 : TPR;
+  constexpr int RPB = BT / TPR;
+  __shared__ float part[2][2][3 * (BT / 64)];
+  const int t = threadIdx.x % TPR;
+  const int sub = threadIdx.x / TPR;
+  const int d = a.d;
+  const float inv_d = 1.0f / (float)d;
+  float dw[NV][VEC], dp[POST ? NV : 1][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      dw[j][i] = 0.0f;
+      if (POST) dp[j][i] = 0.0f;
+    }
+  int flip = 0;
+  // a block of one row at a time (RPB = 1) has one loop count, for the barriers
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.n;
+       row += (int64_t)gridDim.x * RPB, flip ^= 1) {
+    const int64_t base = row * d;
+    float r[NV][VEC], g[NV][VEC];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      if (c < d) {
+        load_any<VEC>(a.r, base + c, a.stream_f32, r[j]);
+        load_bf16<VEC>(a.dy + base + c, g[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r[j][i] = g[j][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      float w[VEC];
+      if (c < d) {
+        load_any<VEC>(a.w, c, a.weight_f32, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        s[0] += r[j][i] * r[j][i];
+        s[1] += g[j][i] * w[i] * r[j][i];
+      }
+    }
+    row_sums<TPR>(s, part[flip][0]);
+    const float ra = rsqrtf(s[0] * inv_d + a.eps);
+    const float k1 = ra * ra * ra * s[1] * inv_d;  // a n mean(h n) = r k1
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      if (c < d) {
+        float w[VEC], q[VEC];
+        load_any<VEC>(a.w, c, a.weight_f32, w);
+        if (a.dres) {
+          load_any<VEC>(a.dres, base + c, a.stream_f32, q);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) q[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          dw[j][i] += g[j][i] * (r[j][i] * ra);
+          r[j][i] = q[i] + (ra * (g[j][i] * w[i]) - r[j][i] * k1);  // dr from here on
+        }
+        if (a.dr_out) {
+          if (a.stream_f32) store_f32<VEC>(reinterpret_cast<float*>(a.dr_out) + base + c, r[j]);
+          else store_bf16<VEC>(reinterpret_cast<uint16_t*>(a.dr_out) + base + c, r[j]);
+        }
+        if (!POST && a.dx) store_bf16<VEC>(a.dx + base + c, r[j]);
+      }
+    }
+    if constexpr (POST) {
+      float xs[NV][VEC];
+      float p[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * VEC;
+        if (c < d) {
+          float w[VEC];
+          load_bf16<VEC>(a.x + base + c, xs[j]);
+          load_any<VEC>(a.post_w, c, a.weight_f32, w);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            p[0] += xs[j][i] * xs[j][i];
+            p[1] += r[j][i] * w[i] * xs[j][i];
+          }
+        }
+      }
+      row_sums<TPR>(p, part[flip][1]);
+      const float rb = rsqrtf(p[0] * inv_d + a.eps);
+      const float k2 = rb * rb * rb * p[1] * inv_d;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * VEC;
+        if (c < d) {
+          float w[VEC], o[VEC];
+          load_any<VEC>(a.post_w, c, a.weight_f32, w);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            dp[j][i] += r[j][i] * (xs[j][i] * rb);
+            o[i] = rb * (r[j][i] * w[i]) - xs[j][i] * k2;
+          }
+          if (a.dx) store_bf16<VEC>(a.dx + base + c, o);
+        }
+      }
+    }
+  }
+  // the block's partial row
+  float* out = a.part_w + (int64_t)blockIdx.x * (POST ? 2 : 1) * d;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      if (c < d) {
+        store_f32<VEC>(out + c, dw[j]);
+        if (POST) store_f32<VEC>(out + d + c, dp[j]);
+      }
+    }
+  } else {
+    // four waves of one block: added in order, one column set at a time
+    __shared__ float red[RPB][TPR * VEC];
+#pragma unroll
+    for (int q = 0; q < (POST ? 2 : 1); ++q) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) red[sub][t * VEC + i] = q ? dp[POST ? j : 0][i] : dw[j][i];
+        __syncthreads();
+        for (int k = threadIdx.x; k < TPR * VEC; k += BT) {
+          const int c = j * TPR * VEC + k;
+          if (c < d) out[q * d + c] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
+        }
+      }
+    }
+  }
+}
+
+// Sums the partial rows [rows][cols] in a fixed order: a block takes 32
+// columns, 32 groups of rows, then the groups in order.
+__global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict__ part, int rows,
+                                                        int cols, int d, float* __restrict__ out0,
+                                                        float* __restrict__ out1) {
+  __shared__ float red[32][33];
+  const int cx = threadIdx.x & 31, gy = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;
+  float s = 0.0f;
+  if (c < cols)
+    for (int r = gy; r < rows; r += 32) s += part[(int64_t)r * cols + c];
+  red[gy][cx] = s;
+  __syncthreads();
+  if (gy == 0 && c < cols) {
+    float v = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 32; ++g) v += red[g][cx];
+    if (c < d) { if (out0) out0[c] = v; }
+    else if (out1) out1[c - d] = v;
+  }
+}
+
+bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <int TPR, int NV, int VEC>
+void start_norm(const NormArgs& a, hipStream_t stream) {
+  constexpr int BT = TPR < 256 ? 256 : TPR;
+  const unsigned blocks = (unsigned)((a.n + BT / TPR - 1) / (BT / TPR));
+  if (a.post_w)
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, VEC, true>), dim3(blocks), dim3(BT), 0, stream, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, VEC, false>), dim3(blocks), dim3(BT), 0, stream, a);
+}
+
+template <int TPR, int NV, int VEC>
+void start_norm_grad(const NormGradArgs& a, int blocks, hipStream_t stream) {
+  constexpr int BT = TPR < 256 ? 256 : TPR;
+  if (a.post_w)
+    hipLaunchKernelGGL((norm_grad_kernel<TPR, NV, VEC, true>), dim3((unsigned)blocks), dim3(BT), 0,
+                       stream, a);
+  else
+    hipLaunchKernelGGL((norm_grad_kernel<TPR, NV, VEC, false>), dim3((unsigned)blocks), dim3(BT),
+                       0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const uint16_t* x, const void* residual, const void* post_w,
+                           const void* w, int64_t n, int d, float eps, bool stream_f32,
+                           bool weight_f32, uint16_t* y, void* r_out, uint8_t* codes,
+                           float* scales, hipStream_t stream) {
+  if (n <= 0) return hipSuccess;
+  if (d < 1 || d > kNormMaxD) return hipErrorInvalidValue;
+  const NormArgs a{x, residual, post_w, w, n, d, eps, stream_f32, weight_f32, y, r_out, codes, scales};
+  const bool vec = d % 8 == 0 && al16(x) && al16(residual) && al16(post_w) && al16(w) && al16(y) &&
+                   al16(r_out) && al16(codes);
+  // a 1 x 128 group is 16 lanes of 8 columns
+  if (codes && (!vec || d % 128)) return hipErrorInvalidValue;
+  // Few rows: a block per row, so that a row's loads are in flight at once;
+  // many rows: a wave per row, no barrier.
+  const bool few = n < 2048;
+  if (vec) {
+    if (d <= 512 && !few) start_norm<64, 1, 8>(a, stream);
+    else if (d <= 1024 && !few) start_norm<64, 2, 8>(a, stream);
+    else if (d <= 2048 && !few) start_norm<64, 4, 8>(a, stream);
+    else if (d <= 2560 && !few) start_norm<64, 5, 8>(a, stream);
+    else if (d <= 2048) start_norm<256, 1, 8>(a, stream);
+    else if (d <= 4096) start_norm<256, 2, 8>(a, stream);
+    else start_norm<256, 4, 8>(a, stream);
+  } else {
+    if (d <= 1024) start_norm<64, 16, 1>(a, stream);
+    else if (d <= 4096) start_norm<256, 16, 1>(a, stream);
+    else start_norm<256, 32, 1>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+int rms_norm_grad_blocks(int64_t n, int d) {
+  // enough blocks for every CU; more rows per block, fewer partial rows
+  const int64_t most = d <= 2560 ? 1024 : 512;
+  const int64_t per = d <= 2560 ? 4 : 1;  // rows a block of waves takes at once
+  const int64_t need = (n + per - 1) / per;
+  return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+hipError_t launch_rms_norm_grad(const uint16_t* dy, const void* r, const uint16_t* x,
+                                const void* dres, const void* w, const void* post_w, int64_t n,
+                                int d, float eps, bool stream_f32, bool weight_f32, uint16_t* dx,
+                                void* dr_out, float* dw, float* dw_post, float* part,
+                                hipStream_t stream) {
+  if (n < 0 || d < 1 || d > kNormMaxD) return hipErrorInvalidValue;
+  const int blocks = rms_norm_grad_blocks(n, d);
+  const NormGradArgs a{dy, r, x, dres, w, post_w, n, d, eps, stream_f32, weight_f32, dx, dr_out, part};
+  const bool vec = d % 8 == 0 && al16(dy) && al16(r) && al16(x) && al16(dres) && al16(w) &&
+                   al16(post_w) && al16(dx) && al16(dr_out);
+  if (vec) {
+    if (d <= 512) start_norm_grad<64, 1, 8>(a, blocks, stream);
+    else if (d <= 1024) start_norm_grad<64, 2, 8>(a, blocks, stream);
+    else if (d <= 2048) start_norm_grad<64, 4, 8>(a, blocks, stream);
+    else if (d <= 2560) start_norm_grad<64, 5, 8>(a, blocks, stream);
+    else if (d <= 4096) start_norm_grad<256, 2, 8>(a, blocks, stream);
+    else start_norm_grad<256, 4, 8>(a, blocks, stream);
+  } else {
+    if (d <= 1024) start_norm_grad<64, 16, 1>(a, blocks, stream);
+    else if (d <= 4096) start_norm_grad<256, 16, 1>(a, blocks, stream);
+    else start_norm_grad<256, 32, 1>(a, blocks, stream);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (!dw && !dw_post) return hipSuccess;
+  const int cols = post_w ? 2 * d : d;
+  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream,
+                     part, blocks, cols, d, dw, dw_post);
+  return hipGetLastError();
+}
+
+}  // namespace moe
