@@ -552,6 +552,61 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
                                        void* stream);
 
 /*
+ * moe_backward - gradients of the layer (bf16 experts): of x, of the logits
+ * and of every weight, from grad_y = dL/dy, for the selection that topk_ids
+ * gives (the selection itself has no gradient).  With s = sigma(Z[t,e]) of a
+ * pair, G = x W_g^T, U = x W_u^T, H = SiLU(G) U (formed again, in fp32) and
+ * Q = grad_y W_d:
+ *   grad_logits_out = grad_logits + [e chosen] (Q . H) s (1 - s),
+ *   dU = s Q SiLU(G), dG = s Q U sigma(G) (1 + G (1 - sigma(G))),
+ *   grad_x = sum_k (dG W_g + dU W_u) [+ shared expert] + grad_logits_out W_r,
+ *   grad W_g = dG^T x, grad W_u = dU^T x, grad W_d = grad_y^T (s H),
+ *   grad W_r = grad_logits_out^T x,
+ * the shared expert with s = 1.  Q, G, U, H and the score gradients are fp32;
+ * dG, dU, s H and, for the router's two products, grad_logits_out are rounded
+ * to bf16 as matrix operands, a pair's part of grad_x once more; every sum is
+ * fp32, every gradient but the logits' leaves in bf16.
+ *
+ *  p            problem; sizes as moe_forward, and N*d*2 bytes and N*K*h*2
+ *               bytes each at most 4 GiB - 128 KiB.  The routing flags are not
+ *               used; MOE_PACKED_GATEUP is refused (row-major weights only).
+ *  w            the layer's weights; w_router NULL: logits that came from
+ *               elsewhere, grad_x then has no router term.
+ *  x, grad_y    [N,d] bf16 bits.
+ *  logits       [N,E] fp32, as the forward call used them (aux.logits).
+ *  topk_ids     [N,K] int32 (aux.topk_ids).  A pair whose id lies outside
+ *               [0,E) contributes nothing.
+ *  grad_logits  [N,E] fp32 or NULL (zero): the logits' gradient from
+ *               elsewhere (moe_lei_backward, moe_balance_loss_backward).
+ *  g            the gradients, all required: x [N,d] bf16, logits [N,E] fp32
+ *               (it may be grad_logits itself), and the weights' in the
+ *               layouts of moe_weights_t (w_router unless w->w_router is NULL,
+ *               ws_* with a shared expert).  Experts without rows get zeros.
+ *  workspace    moe_backward_workspace_bytes(p) bytes, 256-byte aligned; 0
+ *               from the query means an unsupported problem.
+ * Buffers of 16-bit words 16-byte aligned, the others 4-byte.  The first call
+ * on a device sets the kernels' LDS attributes: make one uncaptured call
+ * before capturing.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, WORKSPACE_TOO_SMALL, HIP.
+ */
+typedef struct {
+  uint16_t* x;         /* [N,d] */
+  float* logits;       /* [N,E] */
+  uint16_t* w_router;  /* [E,d] */
+  uint16_t* w_gate;    /* [E,h,d] */
+  uint16_t* w_up;      /* [E,h,d] */
+  uint16_t* w_down;    /* [E,d,h] */
+  uint16_t* ws_gate;   /* [n_shared,hs,d] */
+  uint16_t* ws_up;     /* [n_shared,hs,d] */
+  uint16_t* ws_down;   /* [n_shared,d,hs] */
+} moe_grads_t;
+size_t moe_backward_workspace_bytes(const moe_problem_t* p);
+moe_status_t moe_backward(const moe_problem_t* p, const moe_weights_t* w, const uint16_t* x,
+                          const uint16_t* grad_y, const float* logits, const int32_t* topk_ids,
+                          const float* grad_logits, const moe_grads_t* g, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * Stage timing (a profiling aid).  moe_stage_timing(1): every moe_forward
  * call records a HIP timing event on its stream at each stage boundary;
  * moe_stage_timing(2): only the two events around stage 3 (the routed

@@ -89,3 +89,67 @@ def balance_loss_backward(z, counts, coef, score, spans):
         dz[lo:hi] = w * slope * (f - along)
         size[lo:hi] = w * slope * (f + along)
     return dz, size
+
+
+def _sigmoid(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0, e) / (1.0 + e)
+
+
+def expert_backward(x, dy, s, wg, wu, wd):
+    """Gradients of sum_t dy_t . s_t (silu(x Wg^T) * (x Wu^T)) Wd^T for the rows
+    of one expert, and the sizes of the terms they are sums of.  Returns a dict:
+    dx, ds, wg, wu, wd, and under "mag" the same keys with every product's
+    operands replaced by their absolute values."""
+    x, dy, wg, wu, wd = (t.astype(np.float64) for t in (x, dy, wg, wu, wd))
+    s = s.astype(np.float64)[:, None]
+    G, U, Q = x @ wg.T, x @ wu.T, dy @ wd
+    sg = _sigmoid(G)
+    H = G * sg * U
+    dU, dG = s * Q * G * sg, s * Q * U * sg * (1 + G * (1 - sg))
+    out = dict(dx=dG @ wg + dU @ wu, ds=(Q * H).sum(1), wg=dG.T @ x, wu=dU.T @ x, wd=dy.T @ (s * H))
+    aG, aU, aQ = np.abs(x) @ np.abs(wg).T, np.abs(x) @ np.abs(wu).T, np.abs(dy) @ np.abs(wd)
+    out["mag"] = dict(dx=np.abs(dG) @ np.abs(wg) + np.abs(dU) @ np.abs(wu),
+                      # dQ H + Q dH for relative errors of Q, G and U taken as one
+                      ds=(aQ * np.abs(H) + np.abs(Q) * (1.1 * aG * np.abs(U) + np.abs(G * sg) * aU
+                                                        + np.abs(H))).sum(1),
+                      wg=np.abs(dG).T @ np.abs(x), wu=np.abs(dU).T @ np.abs(x),
+                      wd=np.abs(dy).T @ np.abs(s * H))
+    return out
+
+
+def layer_backward(x, dy, Z, ids, wr, wg, wu, wd, shared=None, grad=None):
+    """Gradients of the layer for given logits and selection.  Returns (out, mag)
+    with keys x, logits, w_router, w_gate, w_up, w_down, ws_gate, ws_up, ws_down
+    as far as they exist.  ids outside [0, E) contribute nothing."""
+    N, d = x.shape
+    E = Z.shape[1]
+    x64 = x.astype(np.float64)
+    out = dict(x=np.zeros((N, d)), logits=np.zeros((N, E)) if grad is None else grad.astype(np.float64),
+               w_gate=np.zeros(wg.shape), w_up=np.zeros(wu.shape), w_down=np.zeros(wd.shape))
+    mag = {k: np.zeros(v.shape) for k, v in out.items()}
+    t_of, k_of = np.nonzero((ids >= 0) & (ids < E))
+    e_of = ids[t_of, k_of]
+    for e in range(E):
+        t = t_of[e_of == e]
+        if t.size == 0:
+            continue
+        s = _sigmoid(Z[t, e].astype(np.float64))
+        r = expert_backward(x[t], dy[t], s, wg[e], wu[e], wd[e])
+        slope = s * _sigmoid(-Z[t, e].astype(np.float64))
+        for o, q in ((out, r), (mag, r["mag"])):
+            np.add.at(o["x"], t, q["dx"])
+            np.add.at(o["logits"], (t, np.full(t.size, e)), q["ds"] * slope)
+            o["w_gate"][e], o["w_up"][e], o["w_down"][e] = q["wg"], q["wu"], q["wd"]
+    if shared is not None:
+        r = expert_backward(x, dy, np.ones(N), *shared)
+        for o, q in ((out, r), (mag, r["mag"])):
+            o["x"] += q["dx"]
+            o["ws_gate"], o["ws_up"], o["ws_down"] = (q[k][None] for k in ("wg", "wu", "wd"))
+    if wr is not None:
+        w64 = wr.astype(np.float64)
+        out["x"] += out["logits"] @ w64
+        out["w_router"] = out["logits"].T @ x64
+        mag["x"] += np.abs(out["logits"]) @ np.abs(w64)
+        mag["w_router"] = np.abs(out["logits"]).T @ np.abs(x64)
+    return out, mag

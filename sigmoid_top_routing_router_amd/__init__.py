@@ -16,7 +16,7 @@ from typing import Optional
 from . import _lib
 from ._lib import (MOE_KEY32, MOE_PACKED_GATEUP, MOE_RECOMPUTE_BIAS, MOE_ROUTE_FUSED, MoeAux,
                    MoeError,
-                   MoeFp8Weights, MoeProblem, MoeWeights)
+                   MoeFp8Weights, MoeGrads, MoeProblem, MoeWeights)
 
 __all__ = ["route", "eqb_bias", "eqb_workspace_bytes", "EqbState", "eqb_bias_parts",
            "route_stats", "read_route_stats", "lei_backward", "forward",
@@ -24,7 +24,8 @@ __all__ = ["route", "eqb_bias", "eqb_workspace_bytes", "EqbState", "eqb_bias_par
            "Fp8ExpertWeights", "quantize_experts", "forward_fp8", "forward_fp8_workspace_bytes",
            "ExpertWeights", "MoeError", "load_library", "stage_timing", "stage_times",
            "forward_noalloc", "pack_gateup", "pack_gateup_weights", "rms_norm",
-           "rms_norm_backward", "balance_loss", "balance_loss_backward"]
+           "rms_norm_backward", "balance_loss", "balance_loss_backward", "backward",
+           "backward_workspace_bytes"]
 
 AUX_FIELDS = [f for f, _ in MoeAux._fields_]
 
@@ -558,6 +559,57 @@ def forward_fp8(x, weights: Fp8ExpertWeights, K: int, beta_in=None,
     return _run_forward(True, x, w, N, d, E, K, h, n_shared, hs, beta_in, recompute_bias,
                         key_bits, logit_offset, logits_in, aux, workspace, out, stream, flags,
                         x_quant)
+
+
+def backward_workspace_bytes(N, d, E, K, h, n_shared=1, h_shared=None) -> int:
+    p = _problem(N, d, E, K, h, n_shared, h_shared or h, 0, None, None)
+    return int(_lib.load().moe_backward_workspace_bytes(C.byref(p)))
+
+
+def backward(grad_y, x, weights: ExpertWeights, logits, topk_ids, grad_logits=None,
+             inplace: bool = False, workspace=None, stream=None):
+    """Gradients of the layer (moe_backward): grad_y, x: [N, d] bf16; logits
+    fp32 [N, E] and topk_ids int32 [N, K] of the forward call (aux outputs
+    "logits" and "topk_ids"); grad_logits: fp32 [N, E], the logits' gradient
+    from elsewhere (balance_loss_backward, lei_backward).  Row-major weights
+    only; without w_router grad_x has no router term.
+
+    Returns (grad_x [N, d] bf16, grad_logits [N, E] fp32, ExpertWeights holding
+    the weights' gradients in bf16).  With ``inplace`` the logits' gradient is
+    added into grad_logits itself."""
+    torch = _torch()
+    lib = _lib.load()
+    if weights.packed:
+        raise ValueError("backward takes row-major weights, not packed ones")
+    x, w, N, d, E, h, n_shared, h_shared = _bf16_weights(x, weights)
+    grad_y = _dev(grad_y, "grad_y", _bf16(), (N, d))
+    logits = _dev(logits, "logits", torch.float32, (N, E))
+    topk_ids = _dev(topk_ids, "topk_ids", torch.int32)
+    if topk_ids is None or topk_ids.dim() != 2 or topk_ids.shape[0] != N:
+        raise ValueError(f"topk_ids must be [{N}, K]")
+    K = topk_ids.shape[1]
+    grad_logits = _dev(grad_logits, "grad_logits", torch.float32, (N, E))
+    if inplace and grad_logits is None:
+        raise ValueError("inplace needs grad_logits")
+    names = [f for f, _ in MoeWeights._fields_ if getattr(weights, f) is not None]
+    _one_device(x, grad_y=grad_y, logits=logits, topk_ids=topk_ids, grad_logits=grad_logits,
+                workspace=workspace, **{f: getattr(weights, f) for f in names})
+    p = _problem(N, d, E, K, h, n_shared, h_shared, 0, None, None)
+    with _on_device(x, stream):
+        dev = x.device
+        if workspace is None:
+            need = int(lib.moe_backward_workspace_bytes(C.byref(p)))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        dx = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+        dz = grad_logits if inplace else torch.empty_like(logits)
+        grads = {f: torch.empty(getattr(weights, f).shape, dtype=torch.bfloat16, device=dev)
+                 for f in names}
+        g = MoeGrads(_ptr(dx), _ptr(dz), *[_ptr(grads.get(f)) for f, _ in MoeWeights._fields_])
+        _lib.check(lib.moe_backward(
+            C.byref(p), C.byref(w), _ptr(x), _ptr(grad_y), _ptr(logits), _ptr(topk_ids),
+            _ptr(grad_logits), C.byref(g), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dx, dz, ExpertWeights(**{"w_router": None, **grads})
 
 
 def _norm_weights(weight, post_weight, d):

@@ -33,6 +33,7 @@ EXPORTED = ["moe_route", "moe_eqb_workspace_bytes", "moe_eqb_bias", "moe_eqb_sta
             "moe_forward_noalloc", "moe_forward_fp8_quantized",
             "moe_rms_norm", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
             "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+            "moe_backward_workspace_bytes", "moe_backward",
             "moe_status_string",
             "moe_last_error_message", "moe_abi_version", "moe_stage_timing",
             "moe_stage_times", "moe_stage_name"]
@@ -68,6 +69,12 @@ class MoeAux(C.Structure):
                 ("counts_before", C.c_void_p), ("counts", C.c_void_p),
                 ("offsets", C.c_void_p), ("sorted_src", C.c_void_p),
                 ("src_pos", C.c_void_p)]
+
+
+class MoeGrads(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("logits", C.c_void_p), ("w_router", C.c_void_p),
+                ("w_gate", C.c_void_p), ("w_up", C.c_void_p), ("w_down", C.c_void_p),
+                ("ws_gate", C.c_void_p), ("ws_up", C.c_void_p), ("ws_down", C.c_void_p)]
 
 
 class MoeRouteStats(C.Structure):
@@ -156,6 +163,11 @@ def load(path: str = LIB_PATH):
     lib.moe_balance_loss_backward.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, f32, vp, vp, vp,
                                               vp]
     lib.moe_balance_loss_backward.restype = C.c_int
+    lib.moe_backward_workspace_bytes.argtypes = [C.POINTER(MoeProblem)]
+    lib.moe_backward_workspace_bytes.restype = C.c_size_t
+    lib.moe_backward.argtypes = [C.POINTER(MoeProblem), C.POINTER(MoeWeights), vp, vp, vp, vp, vp,
+                                 C.POINTER(MoeGrads), vp, C.c_size_t, vp]
+    lib.moe_backward.restype = C.c_int
     lib.moe_status_string.argtypes = [C.c_int]
     lib.moe_status_string.restype = C.c_char_p
     lib.moe_last_error_message.argtypes = []

@@ -1,5 +1,5 @@
-// C ABI of the operators around the layer: the residual norm and the balance
-// loss, forward and backward.  Argument checks, workspace carving and the
+// C ABI of the operators around the layer (the residual norm and the balance
+// loss, forward and backward) and of the layer's backward pass.  Argument checks, workspace carving and the
 // launches on the caller's stream; nothing else.
 #include <hip/hip_runtime.h>
 
@@ -102,9 +102,267 @@ moe::BalanceWork carve_balance(void* ws, int64_t N, int32_t E, int32_t n_seg, si
   return w;
 }
 
+// ---- layer backward
+struct GradLayout {
+  int32_t *ids, *counts, *offsets, *sorted_src, *src_pos, *tiles, *n_tiles, *row_tiles, *n_row_tiles;
+  uint32_t* block_counts;
+  float *S, *Q, *Qs, *dscore;
+  uint16_t *dGU, *sH, *dXp, *dGUs, *Hs, *dzb, *base;
+  int64_t max_tiles, max_row_tiles;
+  int ldb;
+  size_t bytes;
+};
+GradLayout carve_grad(void* ws, const moe_problem_t& p) {
+  char* const base = (char*)ws;
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> void* {
+    void* q = base ? base + off : nullptr;
+    off += up(bytes);
+    return q;
+  };
+  GradLayout l{};
+  const size_t N = (size_t)p.N, pairs = N * p.K, hs = p.n_shared ? (size_t)p.h_shared : 0;
+  l.ldb = (p.E + 63) / 64 * 64;
+  l.ids = (int32_t*)take(pairs * 4);
+  l.S = (float*)take(pairs * 4);
+  l.block_counts = (uint32_t*)take((size_t)moe::perm_count_rows((int64_t)pairs) * p.E * 4);
+  l.counts = (int32_t*)take((size_t)p.E * 4);
+  l.offsets = (int32_t*)take(((size_t)p.E + 1) * 4);
+  l.sorted_src = (int32_t*)take(pairs * 4);
+  l.src_pos = (int32_t*)take(pairs * 4);
+  l.max_tiles = moe::perm_max_tiles((int64_t)pairs, p.E, moe::gemm_bm());
+  l.tiles = (int32_t*)take((size_t)l.max_tiles * 16);
+  l.n_tiles = (int32_t*)take(16);
+  l.max_row_tiles = moe::perm_max_tiles((int64_t)pairs, p.E, moe::grad_tile_rows());
+  l.row_tiles = (int32_t*)take((size_t)l.max_row_tiles * 16);
+  l.n_row_tiles = (int32_t*)take(16);
+  // Q is read for the last time before the pairs' part of grad_x is written
+  void* q = take(pairs * (size_t)(p.h * 4 > p.d * 2 ? p.h * 4 : p.d * 2));
+  l.Q = (float*)q;
+  l.dXp = (uint16_t*)q;
+  l.dGU = (uint16_t*)take(pairs * 2 * p.h * 2);
+  l.sH = (uint16_t*)take(pairs * p.h * 2);
+  l.dscore = (float*)take(pairs * (size_t)moe::gateup_col_tiles(p.h) * 4);
+  l.Qs = (float*)take(N * hs * 4);
+  l.dGUs = (uint16_t*)take(N * 2 * hs * 2);
+  l.Hs = (uint16_t*)take(N * hs * 2);
+  l.dzb = (uint16_t*)take(N * (size_t)l.ldb * 2);
+  l.base = (uint16_t*)take(N * p.d * 2);
+  l.bytes = off;
+  return l;
+}
+
+moe_status_t check_grad_problem(const moe_problem_t* p) {
+  const moe_status_t s = moe::check_layer(p);
+  if (s != MOE_OK) return s;
+  if (p->flags & MOE_PACKED_GATEUP)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the backward pass takes row-major weights only");
+  const uint64_t most = moe::kGradMaxOperandBytes;
+  if ((uint64_t)p->N * p->d * 2 > most || (uint64_t)p->N * p->K * p->h * 2 > most ||
+      (p->n_shared && (uint64_t)p->N * p->h_shared * 2 > most))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "N=%lld too large: x and the hidden rows must each be "
+                "at most 4 GiB - 128 KiB", (long long)p->N);
+  return MOE_OK;
+}
+
+#define MOE_TRY(expr, where)                                  \
+  do {                                                        \
+    const hipError_t _e = (expr);                             \
+    if (_e != hipSuccess) return done(_e, "moe_backward: " where); \
+  } while (0)
+
+moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, const uint16_t* x,
+                               const uint16_t* dy, const float* Z, const int32_t* ids,
+                               const float* grad_logits, const moe_grads_t& g, const GradLayout& l,
+                               hipStream_t st) {
+  const int64_t N = p.N, pairs = N * p.K;
+  const int d = p.d, h = p.h, hs = p.h_shared, E = p.E, K = p.K;
+  const bool shared = p.n_shared == 1, router = w.w_router != nullptr;
+  // the pairs' weights and their grouping by expert
+  MOE_TRY(moe::launch_pairs(ids, Z, pairs, E, K, l.ids, l.S, st), "pairs");
+  moe::PermWork pw;
+  pw.block_counts = l.block_counts;
+  pw.counts = l.counts;
+  pw.offsets = l.offsets;
+  pw.sorted_src = l.sorted_src;
+  pw.src_pos = l.src_pos;
+  pw.tiles = l.tiles;
+  pw.n_tiles = l.n_tiles;
+  MOE_TRY(moe::launch_permute(l.ids, N, E, K, moe::gemm_bm(), moe::gemm_xrows(), pw, st),
+          "grouping");
+  MOE_TRY(moe::launch_row_tiles(l.offsets, E, l.row_tiles, l.n_row_tiles, st), "row tiles");
+
+  auto pair_rows = [&] {
+    moe::RowsProblem r{};
+    r.tiles = l.row_tiles;
+    r.n_tiles = l.n_row_tiles;
+    r.max_tiles = l.max_row_tiles;
+    r.gather_div = 1;
+    return r;
+  };
+  auto token_rows = [&] {
+    moe::RowsProblem r{};
+    r.rows_dense = N;
+    r.gather_div = 1;
+    return r;
+  };
+  // Q = dy W_d
+  {
+    moe::RowsProblem r = pair_rows(), t = token_rows();
+    r.seg[0] = {dy, d, w.w_down, (int64_t)d * h, d};
+    r.n_seg = 1;
+    r.gather = l.sorted_src;
+    r.gather_div = K;
+    r.a_rows = N;
+    r.ncols = h;
+    r.out = l.Q;
+    r.ldo = h;
+    r.out_f32 = true;
+    if (shared) {
+      t.seg[0] = {dy, d, w.ws_down, 0, d};
+      t.n_seg = 1;
+      t.ncols = hs;
+      t.out = l.Qs;
+      t.ldo = hs;
+      t.out_f32 = true;
+    }
+    MOE_TRY(moe::launch_rows(shared ? &t : nullptr, &r, st), "hidden gradient");
+  }
+  // G, U again; dG, dU, s H and the score gradients
+  MOE_TRY(moe::launch_gateup_grad(x, N, l.sorted_src, K, l.tiles, l.n_tiles, l.max_tiles, 0,
+                                  w.w_gate, w.w_up, d, h, l.Q, l.S, l.dGU, l.sH, l.dscore, st),
+          "gate/up gradient");
+  if (shared)
+    MOE_TRY(moe::launch_gateup_grad(x, N, nullptr, 1, nullptr, nullptr, 0, N, w.ws_gate, w.ws_up,
+                                    d, hs, l.Qs, nullptr, l.dGUs, l.Hs, nullptr, st),
+            "shared gate/up gradient");
+  MOE_TRY(moe::launch_logits_grad(Z, ids, l.src_pos, l.dscore, moe::gateup_col_tiles(h), N, E, K,
+                                  grad_logits, g.logits, router ? l.dzb : nullptr, l.ldb, st),
+          "logits gradient");
+  // grad_x: the pairs' parts, and the tokens' (shared expert and router)
+  {
+    moe::RowsProblem r = pair_rows(), t = token_rows();
+    const int64_t es = (int64_t)h * d;
+    r.seg[0] = {l.dGU, 2 * (int64_t)h, w.w_gate, es, h};
+    r.seg[1] = {l.dGU + h, 2 * (int64_t)h, w.w_up, es, h};
+    r.n_seg = 2;
+    r.ncols = d;
+    r.out = l.dXp;
+    r.ldo = d;
+    if (shared) {
+      t.seg[t.n_seg++] = {l.dGUs, 2 * (int64_t)hs, w.ws_gate, 0, hs};
+      t.seg[t.n_seg++] = {l.dGUs + hs, 2 * (int64_t)hs, w.ws_up, 0, hs};
+    }
+    if (router) t.seg[t.n_seg++] = {l.dzb, l.ldb, w.w_router, 0, E};
+    t.ncols = d;
+    t.out = l.base;
+    t.ldo = d;
+    MOE_TRY(moe::launch_rows(t.n_seg ? &t : nullptr, &r, st), "x gradient");
+    MOE_TRY(moe::launch_sum_pairs(t.n_seg ? l.base : nullptr, l.dXp, l.src_pos, N, K, d, g.x, st),
+            "x gradient sum");
+  }
+  // the weights' gradients, one launch
+  moe::WeightsLaunch wl{};
+  auto dense = [&](const uint16_t* A, int64_t lda, int a_cols, const uint16_t* B, int64_t ldb,
+                   int b_cols, uint16_t* out0, uint16_t* out1, int split) {
+    moe::WeightsProblem& q = wl.dense[wl.n_dense++];
+    q = {};
+    q.A = A;
+    q.lda = lda;
+    q.a_cols = a_cols;
+    q.B = B;
+    q.ldb = ldb;
+    q.b_cols = b_cols;
+    q.rows_dense = N;
+    q.src_div = 1;
+    q.out0 = out0;
+    q.out1 = out1;
+    q.split = split;
+  };
+  if (shared) {
+    dense(l.dGUs, 2 * (int64_t)hs, 2 * hs, x, d, d, g.ws_gate, g.ws_up, hs);
+    dense(dy, d, d, l.Hs, hs, hs, g.ws_down, nullptr, d);
+  }
+  if (router) dense(l.dzb, l.ldb, E, x, d, d, g.w_router, nullptr, E);
+  wl.E = E;
+  for (int i = 0; i < 2; ++i) {
+    moe::WeightsProblem& q = wl.expert[i];
+    q.offsets = l.offsets;
+    q.src = l.sorted_src;
+    q.src_div = K;
+    q.src_rows = N;
+    q.out_stride = (int64_t)h * d;
+  }
+  moe::WeightsProblem& gu = wl.expert[0];
+  gu.A = l.dGU;
+  gu.lda = 2 * (int64_t)h;
+  gu.a_cols = 2 * h;
+  gu.B = x;
+  gu.ldb = d;
+  gu.b_cols = d;
+  gu.gather_b = true;
+  gu.out0 = g.w_gate;
+  gu.out1 = g.w_up;
+  gu.split = h;
+  moe::WeightsProblem& dn = wl.expert[1];
+  dn.A = dy;
+  dn.lda = d;
+  dn.a_cols = d;
+  dn.B = l.sH;
+  dn.ldb = h;
+  dn.b_cols = h;
+  dn.gather_a = true;
+  dn.out0 = g.w_down;
+  dn.split = d;
+  MOE_TRY(moe::launch_weights(wl, st), "weight gradients");
+  return moe::set_error(MOE_OK, "");
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_backward_workspace_bytes(const moe_problem_t* p) {
+  if (check_grad_problem(p) != MOE_OK) return 0;
+  return carve_grad(nullptr, *p).bytes;
+}
+
+moe_status_t moe_backward(const moe_problem_t* p, const moe_weights_t* w, const uint16_t* x,
+                          const uint16_t* grad_y, const float* logits, const int32_t* topk_ids,
+                          const float* grad_logits, const moe_grads_t* g, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  moe_status_t s = check_grad_problem(p);
+  if (s != MOE_OK) return s;
+  if (!w || !x || !grad_y || !logits || !topk_ids || !g)
+    return fail(MOE_ERR_INVALID_ARGUMENT,
+                "weights, x, grad_y, logits, topk_ids and gradients are required");
+  if (!w->w_gate || !w->w_up || !w->w_down || !g->w_gate || !g->w_up || !g->w_down || !g->x ||
+      !g->logits)
+    return fail(MOE_ERR_INVALID_ARGUMENT,
+                "routed expert weights and the gradients of x, logits and them are required");
+  if ((w->w_router != nullptr) != (g->w_router != nullptr))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "w_router and its gradient: both or neither");
+  if (p->n_shared == 1 && (!w->ws_gate || !w->ws_up || !w->ws_down || !g->ws_gate || !g->ws_up ||
+                           !g->ws_down))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "shared expert weights and gradients are required");
+  const void* in[] = {x, grad_y, w->w_router, w->w_gate, w->w_up, w->w_down, w->ws_gate, w->ws_up,
+                      w->ws_down};
+  const void* out[] = {g->x, g->w_router, g->w_gate, g->w_up, g->w_down, g->ws_gate, g->ws_up,
+                       g->ws_down};
+  const void* f4[] = {logits, topk_ids, grad_logits, g->logits};
+  if ((s = check_aligned(in, 9, 16, "bf16 inputs")) != MOE_OK) return s;
+  if ((s = check_aligned(out, 8, 16, "bf16 gradients")) != MOE_OK) return s;
+  if ((s = check_aligned(f4, 4, 4, "logits and ids")) != MOE_OK) return s;
+  if (g->logits == logits)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the logits' gradient must not be the logits");
+  for (const void* i : in)
+    for (const void* o : out)
+      if (i && i == o) return fail(MOE_ERR_INVALID_ARGUMENT, "a gradient aliases an input");
+  const GradLayout need = carve_grad(nullptr, *p);
+  if ((s = check_workspace(workspace, workspace_bytes, need.bytes)) != MOE_OK) return s;
+  return backward_launches(*p, *w, x, grad_y, logits, topk_ids, grad_logits, *g,
+                           carve_grad(workspace, *p), (hipStream_t)stream);
+}
 
 moe_status_t moe_rms_norm(const uint16_t* x, const void* residual, const void* post_weight,
                           const void* weight, int64_t n, int32_t d, float eps, uint32_t flags,

@@ -12,8 +12,10 @@ namespace moe {
 constexpr int kTileN = 256;  // output columns (B rows) of one n-tile of the tile engine
 
 // kRouterNarrow: the router product in 256 x 128 tiles (a launch mode of
-// gemm_kernel; the tile itself is gemm_tile<kRouter, ..., NARROW = true>)
-enum Mode { kGateUp = 0, kDown = 1, kRouter = 2, kRouterNarrow = 3 };
+// gemm_kernel; the tile itself is gemm_tile<kRouter, ..., NARROW = true>).
+// kGateUpGrad: the gate/up product of the backward pass, whose epilogue forms
+// the gradients of gate and up and the scaled hidden row.
+enum Mode { kGateUp = 0, kDown = 1, kRouter = 2, kRouterNarrow = 3, kGateUpGrad = 4 };
 
 struct GemmArgs {
   const uint16_t* A;       // x (gate/up, router) or H (down)
@@ -66,6 +68,12 @@ struct GemmArgs {
   const float* sbs0;
   const float* sbs1;
   int64_t shared_row0;
+  // Backward gate/up only (kGateUpGrad), rows as the output rows of gate/up:
+  const float* q_in;       // Q = dy W_d [rows][h] fp32
+  const float* row_scale;  // s of pair sorted_src[row], or NULL (1)
+  uint16_t* dgu_out;       // [rows][2h]: dG, then dU
+  uint16_t* sh_out;        // [rows][h]: s H
+  float* dscore_part;      // [rows][n_tiles_n]: Q . H over the tile's columns, or NULL
 };
 
 // Row-major B (every builder's default).

@@ -354,6 +354,106 @@ __device__ __forceinline__ void router_tile_select(const GemmArgs& a, int nt, in
   }
 }
 
+// Epilogue of the backward gate/up tile ("Kolibri 1 im Detail", SwiGLU
+// paragraph, differentiated): with G and U of a row in the accumulators,
+// Q = dy W_d from memory and the row's weight s, sg = sigma(G),
+//   H = G sg U,  dU = s Q G sg,  dG = s Q U sg (1 + G (1 - sg)),
+// and the row's score gradient Q . H over the tile's columns, added over the
+// four column quarters in order.  dG, dU and s H leave in bf16 (they are the
+// operands of the next products); everything else is fp32.  Four consecutive
+// columns per lane go out as 8-byte stores.
+template <int XR>
+__device__ __forceinline__ void epilogue_grad(const GemmArgs& a, floatx16_t (&acc)[4][2],
+                                              floatx16_t& accx, int nt, int64_t row0, int rows,
+                                              int lane, int wg, int wp, int tid, bool any,
+                                              int live_m, char* lds_raw) {
+  const int orow_l = lane & 31;
+  const int ocol_l = 4 * (lane >> 5);
+  float* dsum = reinterpret_cast<float*>(lds_raw);  // [BM + XR][4]
+  constexpr int kExOff = 16 * 1024;                 // behind it: up of the extra rows
+  static_assert((BM + XR) * 16 <= kExOff, "row sums overlap the exchange area");
+  float4* ex = reinterpret_cast<float4*>(lds_raw + kExOff) + wp * 256;
+  const int h = a.b_rows;
+  const int col0 = nt * (BN / 2) + wp * 32;
+  const bool cols = col0 < h;  // h % 32 == 0: 32 columns are inside or outside
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  auto pack2 = [](float x, float y) {
+    const bf16x2_t v = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  };
+  // one row's 16 columns of this lane: g and u by register index
+  auto emit = [&](int rr, auto g_of, auto u_of) {
+    float part = 0.0f;
+    if (rr < rows && cols) {
+      const int64_t orow = row0 + rr;
+      const float s = a.row_scale ? a.row_scale[a.gather[orow]] : 1.0f;
+      const float* q = a.q_in + orow * h + col0 + ocol_l;
+      uint16_t* dg = a.dgu_out + orow * 2 * h + col0 + ocol_l;
+      uint16_t* hh = a.sh_out + orow * h + col0 + ocol_l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 qv = *reinterpret_cast<const float4*>(q + 8 * k);
+        const float qs[4] = {qv.x, qv.y, qv.z, qv.w};
+        float o0[4], o1[4], o2[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float g = g_of(4 * k + j), u = u_of(4 * k + j);
+          const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+          const float gs = g * sg;
+          const float hv = gs * u;
+          part += qs[j] * hv;
+          const float sq = s * qs[j];
+          o0[j] = sq * u * sg * (1.0f + g * (1.0f - sg));
+          o1[j] = sq * gs;
+          o2[j] = s * hv;
+        }
+        *reinterpret_cast<uint2*>(dg + 8 * k) = make_uint2(pack2(o0[0], o0[1]), pack2(o0[2], o0[3]));
+        *reinterpret_cast<uint2*>(dg + h + 8 * k) =
+            make_uint2(pack2(o1[0], o1[1]), pack2(o1[2], o1[3]));
+        *reinterpret_cast<uint2*>(hh + 8 * k) = make_uint2(pack2(o2[0], o2[1]), pack2(o2[2], o2[3]));
+      }
+    }
+    part += __shfl_xor(part, 32);
+    if (lane < 32) dsum[rr * 4 + wp] = part;
+  };
+  __syncthreads();  // all fragment reads of the last stage are done
+  if (any) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (m >= live_m) break;
+      // with extra rows, waves of the second row half hold up in acc[m][0]
+      const int gi = (XR > 0 && wg) ? 1 : 0;
+      emit(wg * 128 + m * 32 + orow_l, [&](int r) { return gi ? acc[m][1][r] : acc[m][0][r]; },
+           [&](int r) { return gi ? acc[m][0][r] : acc[m][1][r]; });
+    }
+    if (XR > 0 && wg == 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        ex[k * 64 + lane] = make_float4(accx[4 * k], accx[4 * k + 1], accx[4 * k + 2],
+                                        accx[4 * k + 3]);
+    }
+  }
+  __syncthreads();
+  if constexpr (XR > 0) {
+    if (any && wg == 0) {
+      floatx16_t up;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = ex[k * 64 + lane];
+        up[4 * k] = v.x; up[4 * k + 1] = v.y; up[4 * k + 2] = v.z; up[4 * k + 3] = v.w;
+      }
+      emit(BM + orow_l, [&](int r) { return accx[r]; }, [&](int r) { return up[r]; });
+    }
+    __syncthreads();
+  }
+  if (a.dscore_part) {
+    for (int r = tid; r < rows; r += 512) {
+      const float4 v = *reinterpret_cast<const float4*>(dsum + 4 * r);
+      a.dscore_part[(row0 + r) * a.n_tiles_n + nt] = (v.x + v.y) + (v.z + v.w);
+    }
+  }
+}
+
 // Epilogue of one tile: accumulators acc[m][f] of wave (wg, wp) -> the output
 // (router: fp32 logits + offset; gate/up: SiLU(g) * u in bf16; down: bf16).
 template <int MODE, int XR, bool NARROW = false>
@@ -507,6 +607,7 @@ template <int MODE, bool GROUPED, int XR = 0, bool BNT = false, bool NARROW = fa
 __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
                                           char* lds_raw) {
   static_assert(XR == 0 || (XR == 32 && GROUPED && MODE != kRouter), "extra rows: grouped only");
+  constexpr bool kGU = MODE == kGateUp || MODE == kGateUpGrad;
   static_assert(!NARROW || (MODE == kRouter && XR == 0), "narrow tiles: router only");
   constexpr int A_TILE = (BM + XR) * ROW_BYTES;          // bytes per A slot
   constexpr int B_BASE = A_SLOTS * A_TILE;               // byte offset of the B ring
@@ -565,7 +666,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
     if (i < 4) {
       // narrow tiles: B rows nt*128 .. +127 in quarters 0 and 1; quarters 2
       // and 3 load zeros without a memory access and are never read
-      const int brow = (MODE == kGateUp) ? nt * (BN / 2) + (r & (BN / 2 - 1))
+      const int brow = (kGU) ? nt * (BN / 2) + (r & (BN / 2 - 1))
                        : NARROW ? (r < BN / 2 ? nt * (BN / 2) + r : a.b_rows)
                                 : nt * BN + r;
       b_voff[i] = (brow < a.b_rows) ? (uint32_t)brow * a.b_row_pitch + (uint32_t)chunk * 16u
@@ -576,7 +677,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, a.a_bytes);
   const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(a.B0 + (int64_t)expert * a.b_expert_stride, b_bytes);
   const __amdgpu_buffer_rsrc_t rb1 =
-      make_rsrc((MODE == kGateUp ? a.B1 : a.B0) + (int64_t)expert * a.b_expert_stride, b_bytes);
+      make_rsrc((kGU ? a.B1 : a.B0) + (int64_t)expert * a.b_expert_stride, b_bytes);
   // K tail: kdim % 64 == 32 leaves a last stage with 32 valid k.  There the
   // upper four chunks of each row are loaded from the lower four (64 bytes
   // lower), so every access stays inside its row; they are never multiplied.
@@ -603,7 +704,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
   };
   // B load i of stage ks fills quarter i (B rows 64*i .. +63)
   auto dma_b = [&](int ks, int i) {
-    dma16<BNT ? kCpolNT : 0>((MODE == kGateUp && i >= 2) ? rb1 : rb0, voff_at(b_voff[i], ks, tail_adj),
+    dma16<BNT ? kCpolNT : 0>((kGU && i >= 2) ? rb1 : rb0, voff_at(b_voff[i], ks, tail_adj),
           (uint32_t)ks * a.b_kblk_pitch,
           (lds_void_t*)(lds_raw + B_BASE + bq(ks, i) * QUARTER + wave * 1024));
   };
@@ -625,7 +726,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
 #pragma unroll
   for (int r = 0; r < 16; ++r) accx[r] = 0.0f;
   int b_row[2];
-  if (MODE == kGateUp) { b_row[0] = wp * 32; b_row[1] = BN / 2 + wp * 32; }
+  if (kGU) { b_row[0] = wp * 32; b_row[1] = BN / 2 + wp * 32; }
   else if (NARROW) { b_row[0] = (wp & 1) * 64; b_row[1] = (wp & 1) * 64 + 32; }
   else { b_row[0] = wp * 64; b_row[1] = wp * 64 + 32; }
   if (XR > 0 && wg == 1) { const int t = b_row[0]; b_row[0] = b_row[1]; b_row[1] = t; }
@@ -643,7 +744,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
   int live_m = (rows - row_base + 31) / 32;
   live_m = live_m < 0 ? 0 : (live_m > MAX_LIVE ? MAX_LIVE : live_m);
   live_m = __builtin_amdgcn_readfirstlane(live_m);
-  const bool live_n = (MODE == kGateUp) ? true
+  const bool live_n = (kGU) ? true
                       : NARROW ? (nt * (BN / 2) + b_row[0]) < a.b_rows
                                : (nt * BN + wp * 64) < a.b_rows;
   const bool any = __builtin_amdgcn_readfirstlane((live_m > 0 && live_n) ? 1 : 0) != 0;
@@ -802,8 +903,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t mt, int nt,
     else run(std::integral_constant<int, 2>{});
   }
 
-  gemm_epilogue<MODE, XR, NARROW>(a, acc, accx, nt, row0, rows, lane, wg, wp, tid, b_row, any,
-                                  live_m, lds_raw);
+  if constexpr (MODE == kGateUpGrad)
+    epilogue_grad<XR>(a, acc, accx, nt, row0, rows, lane, wg, wp, tid, any, live_m, lds_raw);
+  else
+    gemm_epilogue<MODE, XR, NARROW>(a, acc, accx, nt, row0, rows, lane, wg, wp, tid, b_row, any,
+                                    live_m, lds_raw);
 }
 
 // ---------------------------------------------------------------- FP8 tiles
@@ -1297,6 +1401,9 @@ static hipError_t launch_gemm(int mode, const GemmArgs& a, int64_t max_m_tiles,
     case kGateUp:
       return grouped ? launch_mode<kGateUp, true>(a, grid, stream)
                      : launch_mode<kGateUp, false>(a, grid, stream);
+    case kGateUpGrad:
+      return grouped ? launch_mode<kGateUpGrad, true>(a, grid, stream)
+                     : launch_mode<kGateUpGrad, false>(a, grid, stream);
     case kDown:
       return grouped ? launch_mode<kDown, true>(a, grid, stream)
                      : launch_mode<kDown, false>(a, grid, stream);
@@ -1345,6 +1452,22 @@ hipError_t launch_gateup(const uint16_t* x, int64_t x_rows, const int32_t* sorte
   if (kblock_major) b_kblock_major(a);
   const int64_t mt = tiles ? max_tiles : (rows_dense + BM - 1) / BM;
   return launch_gemm(kGateUp, a, mt, stream);
+}
+
+hipError_t launch_gateup_grad(const uint16_t* x, int64_t x_rows, const int32_t* sorted_src, int K,
+                              const int32_t* tiles, const int32_t* n_tiles, int64_t max_tiles,
+                              int64_t rows_dense, const uint16_t* w_gate, const uint16_t* w_up,
+                              int d, int h, const float* Q, const float* row_scale, uint16_t* dGU,
+                              uint16_t* sH, float* dscore_part, hipStream_t stream) {
+  GemmArgs a = gateup_args(x, x_rows, sorted_src, K, tiles, n_tiles, rows_dense, w_gate, w_up, d,
+                           h, nullptr);
+  a.q_in = Q;
+  a.row_scale = row_scale;
+  a.dgu_out = dGU;
+  a.sh_out = sH;
+  a.dscore_part = dscore_part;
+  const int64_t mt = tiles ? max_tiles : (rows_dense + BM - 1) / BM;
+  return launch_gemm(kGateUpGrad, a, mt, stream);
 }
 
 hipError_t launch_down(const uint16_t* H, int64_t h_rows, const int32_t* tiles, const int32_t* n_tiles,

@@ -119,6 +119,16 @@ hipError_t launch_gateup(const uint16_t* x, int64_t x_rows, const int32_t* sorte
                          hipStream_t stream, bool kblock_major = false);
 // Grouped down projection: Y rows = H rows W_d^T (bf16 out).  H has h_rows
 // rows; h_rows * h * 2 < 4 GiB.
+// The gate/up product of the backward pass over the same rows (see the
+// kernel's epilogue): from Q [rows][h] fp32 and the pairs' weights row_scale
+// [N*K] (NULL: 1) it writes dGU [rows][2h] = dG | dU, sH [rows][h] and, when
+// given, the score gradients' partial sums [rows][gateup_col_tiles(h)].
+hipError_t launch_gateup_grad(const uint16_t* x, int64_t x_rows, const int32_t* sorted_src, int K,
+                              const int32_t* tiles, const int32_t* n_tiles, int64_t max_tiles,
+                              int64_t rows_dense, const uint16_t* w_gate, const uint16_t* w_up,
+                              int d, int h, const float* Q, const float* row_scale, uint16_t* dGU,
+                              uint16_t* sH, float* dscore_part, hipStream_t stream);
+inline int gateup_col_tiles(int h) { return (h + 127) / 128; }
 hipError_t launch_down(const uint16_t* H, int64_t h_rows, const int32_t* tiles, const int32_t* n_tiles,
                        int64_t max_tiles, int64_t rows_dense, const uint16_t* w_down,
                        int d, int h, uint16_t* Y, hipStream_t stream);
@@ -208,6 +218,79 @@ hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int3
                                const int32_t* end, int64_t N, int E, int G, int score, float coef,
                                const float* grad_loss, const float* grad_in, float* grad_out,
                                hipStream_t stream);
+
+// ---------------------------------------------------------------- layer backward
+// Gathered operands (x, dy) and the tiles' rows of direct ones are smaller
+// than this.
+constexpr uint32_t kGradMaxOperandBytes = 0xFFFE0000u;
+// C[row, n] = sum over the segments of sum_k A[row, k] B[k, n]; rows of A from
+// the tile table (expert, first row, rows, offset), through gather when set
+// (row -> gather[row] / gather_div of a_rows), or 0 .. rows_dense - 1.
+struct RowsSegment {
+  const uint16_t* A;
+  int64_t lda;             // elements
+  const uint16_t* B;       // [expert][kdim][ncols]
+  int64_t b_expert_stride;
+  int kdim;                // rows of A are padded to a multiple of 8
+};
+struct RowsProblem {
+  RowsSegment seg[3];
+  int n_seg;
+  const int32_t* gather;
+  int gather_div;
+  int64_t a_rows;
+  const int32_t* tiles;
+  const int32_t* n_tiles;
+  int64_t max_tiles;
+  int64_t rows_dense;
+  int ncols;               // multiple of 8 (bf16 out) or 4
+  int n_tiles_n;           // set by the launcher
+  void* out;
+  int64_t ldo;
+  bool out_f32;
+};
+int grad_tile_rows();      // rows of a tile in the tables below
+hipError_t launch_rows(const RowsProblem* token, const RowsProblem* pair, hipStream_t stream);
+// C[m, n] = sum_row A[row, m] B[row, n] in bf16, rows offsets[e] ..
+// offsets[e + 1] - 1 (or all rows_dense); A or B may be gathered through
+// src[row] / src_div (of src_rows rows).  Output rows m < split go to out0,
+// the others to out1.
+struct WeightsProblem {
+  const uint16_t* A;
+  int64_t lda;
+  int a_cols;              // rows of the output
+  const uint16_t* B;
+  int64_t ldb;
+  int b_cols;
+  const int32_t* offsets;
+  int64_t rows_dense;
+  const int32_t* src;
+  int src_div;
+  int64_t src_rows;
+  bool gather_a, gather_b;
+  uint16_t* out0;
+  uint16_t* out1;
+  int split;
+  int64_t out_stride;      // elements between experts
+  int tiles_m, tiles_n;    // set by the launcher
+};
+struct WeightsLaunch {
+  WeightsProblem dense[3];
+  int n_dense;
+  WeightsProblem expert[2];
+  int E;
+};
+hipError_t launch_weights(WeightsLaunch w, hipStream_t stream);
+hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E, int K,
+                        int32_t* ids_out, float* S, hipStream_t stream);
+hipError_t launch_row_tiles(const int32_t* offsets, int E, int32_t* tiles, int32_t* n_tiles,
+                            hipStream_t stream);
+hipError_t launch_logits_grad(const float* Z, const int32_t* ids, const int32_t* src_pos,
+                              const float* dscore_part, int parts, int64_t N, int E, int K,
+                              const float* grad_in, float* grad_out, uint16_t* dzb, int ldb,
+                              hipStream_t stream);
+hipError_t launch_sum_pairs(const uint16_t* base, const uint16_t* Y, const int32_t* src_pos,
+                            int64_t N, int K, int d, uint16_t* out, hipStream_t stream);
 
 // ---------------------------------------------------------------- FP8
 // Rows of X [N,C] bf16 (C % 128 == 0) -> E4M3 codes Q [N,C] and one fp32

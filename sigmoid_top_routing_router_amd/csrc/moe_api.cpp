@@ -952,6 +952,8 @@ moe_status_t moe::forward_bf16(const moe_problem_t* p, const moe_weights_t* w, c
   return forward_impl(p, ex, x, beta_in, y, aux, workspace, workspace_bytes, stream);
 }
 
+moe_status_t moe::check_layer(const moe_problem_t* p) { return check_problem(p); }
+
 moe_status_t moe::set_error(moe_status_t s, const char* msg) { return fail(s, "%s", msg); }
 
 extern "C" {

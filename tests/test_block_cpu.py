@@ -194,3 +194,84 @@ def test_balance_gradient_formula(score):
     dz, size = B.balance_loss_backward(z, counts, 0.5, score, spans)
     assert np.abs(dz - _differences(value, z, 1e-5)).max() < 1e-8
     assert np.all(dz[3] == 0) and np.all(np.abs(dz) <= size + 1e-18)
+
+
+@built
+def test_backward_refusals(lib, mem):
+    from sigmoid_top_routing_router_amd._lib import MoeGrads, MoeProblem, MoeWeights
+
+    def problem(**kw):
+        return MoeProblem(**dict(dict(N=4, d=64, E=4, K=2, h=32, n_shared=1, h_shared=32, flags=0), **kw))
+    need = lib.moe_backward_workspace_bytes(C.byref(problem()))
+    assert need > 0
+    # the routing flags of the forward call are allowed, packed weights are not
+    assert lib.moe_backward_workspace_bytes(C.byref(problem(flags=11))) == need
+    for bad in (dict(flags=4), dict(flags=16), dict(N=0), dict(K=9), dict(E=2), dict(d=96),
+                dict(h=40), dict(n_shared=2), dict(N=1 << 18, d=8192)):
+        assert lib.moe_backward_workspace_bytes(C.byref(problem(**bad))) == 0, bad
+    # N d of exactly 4 GiB - 128 KiB passes, a row more does not
+    rows = (2 ** 32 - 2 ** 17) // (2 * 8192)
+    assert lib.moe_backward_workspace_bytes(C.byref(problem(N=rows, d=8192, h=32))) > 0
+    assert lib.moe_backward_workspace_bytes(C.byref(problem(N=rows + 1, d=8192, h=32))) == 0
+    w = MoeWeights(*([mem] * 7))
+    outs = [mem + 4096, mem + 8192] + [mem + 16384] * 7
+    base = dict(p=problem(), w=w, x=mem, dy=mem, z=mem, ids=mem, gz=None, g=MoeGrads(*outs),
+                ws=mem + 65536, wsb=need)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        ref = [None if a[k] is None else C.byref(a[k]) for k in ("p", "w", "g")]
+        return lib.moe_backward(ref[0], ref[1], a["x"], a["dy"], a["z"], a["ids"], a["gz"], ref[2],
+                                a["ws"], a["wsb"], None)
+
+    def grads(i, v):
+        return MoeGrads(*[v if j == i else o for j, o in enumerate(outs)])
+
+    def weights(i, v):
+        return MoeWeights(*[v if j == i else mem for j in range(7)])
+    assert call(p=None) == 2 or call(p=None) == 1
+    for name in ("w", "x", "dy", "z", "ids", "g"):
+        assert call(**{name: None}) == 1, name
+    for i in range(9):
+        assert call(g=grads(i, None)) == 1, i                 # every gradient is required
+    for i in range(7):
+        assert call(w=weights(i, None)) == 1, i               # w_router: its gradient is given
+        assert call(w=weights(i, mem + 8)) == 1, i
+    assert call(x=mem + 8) == 1 and call(z=mem + 2) == 1 and call(g=grads(3, mem + 8)) == 1
+    assert call(g=grads(1, mem)) == 1                         # the logits themselves
+    assert call(g=grads(0, mem)) == 1                         # grad_x is x
+    assert call(p=problem(flags=4)) == 1
+    assert call(ws=None) == 1 and call(ws=mem + 65540) == 1
+    assert call(wsb=need - 1) == 3
+
+
+def test_layer_gradient_formula():
+    rng = np.random.default_rng(3)
+    N, d, E, K, h, hs = 4, 3, 4, 2, 2, 3
+    t = dict(x=rng.standard_normal((N, d)), wr=rng.standard_normal((E, d)),
+             wg=rng.standard_normal((E, h, d)), wu=rng.standard_normal((E, h, d)),
+             wd=rng.standard_normal((E, d, h)), sg=rng.standard_normal((hs, d)),
+             su=rng.standard_normal((hs, d)), sd=rng.standard_normal((d, hs)))
+    dy, extra = rng.standard_normal((N, d)), rng.standard_normal((N, E))
+    ids = np.argsort(-(t["x"] @ t["wr"].T), axis=1)[:, :K]
+
+    def mlp(x, g, u, w):
+        a = x @ g.T
+        return (a / (1 + np.exp(-a)) * (x @ u.T)) @ w.T
+
+    def value():
+        z = t["x"] @ t["wr"].T
+        y = mlp(t["x"], t["sg"], t["su"], t["sd"])
+        for i in range(N):
+            for e in ids[i]:
+                y[i] += mlp(t["x"][i:i + 1], t["wg"][e], t["wu"][e], t["wd"][e])[0] / (1 + np.exp(-z[i, e]))
+        return float((y * dy).sum() + (z * extra).sum())
+
+    out, mag = B.layer_backward(t["x"], dy, t["x"] @ t["wr"].T, ids, t["wr"], t["wg"], t["wu"],
+                                t["wd"], (t["sg"], t["su"], t["sd"]), extra)
+    for name, key in (("x", "x"), ("wr", "w_router"), ("wg", "w_gate"), ("wu", "w_up"),
+                      ("wd", "w_down"), ("sg", "ws_gate"), ("su", "ws_up"), ("sd", "ws_down")):
+        got = out[key].reshape(t[name].shape)
+        assert np.abs(got - _differences(value, t[name], 1e-5)).max() < 1e-6, name
+        if key != "x":  # the sizes bound the sums
+            assert np.all(np.abs(out[key]) <= mag[key] + 1e-12)
