@@ -197,13 +197,11 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     r.tiles = l.row_tiles;
     r.n_tiles = l.n_row_tiles;
     r.max_tiles = l.max_row_tiles;
-    r.gather_div = 1;
     return r;
   };
   auto token_rows = [&] {
     moe::RowsProblem r{};
     r.rows_dense = N;
-    r.gather_div = 1;
     return r;
   };
   // Q = dy W_d
@@ -217,16 +215,14 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     r.ncols = h;
     r.out = l.Q;
     r.ldo = h;
-    r.out_f32 = true;
     if (shared) {
       t.seg[0] = {dy, d, w.ws_down, 0, d};
       t.n_seg = 1;
       t.ncols = hs;
       t.out = l.Qs;
       t.ldo = hs;
-      t.out_f32 = true;
     }
-    MOE_TRY(moe::launch_rows(shared ? &t : nullptr, &r, st), "hidden gradient");
+    MOE_TRY(moe::launch_rows(shared ? &t : nullptr, r, true, st), "hidden gradient");
   }
   // G, U again; dG, dU, s H and the score gradients
   MOE_TRY(moe::launch_gateup_grad(x, N, l.sorted_src, K, l.tiles, l.n_tiles, l.max_tiles, 0,
@@ -257,7 +253,7 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     t.ncols = d;
     t.out = l.base;
     t.ldo = d;
-    MOE_TRY(moe::launch_rows(t.n_seg ? &t : nullptr, &r, st), "x gradient");
+    MOE_TRY(moe::launch_rows(t.n_seg ? &t : nullptr, r, false, st), "x gradient");
     MOE_TRY(moe::launch_sum_pairs(t.n_seg ? l.base : nullptr, l.dXp, l.src_pos, N, K, d, g.x, st),
             "x gradient sum");
   }
@@ -300,7 +296,6 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   gu.B = x;
   gu.ldb = d;
   gu.b_cols = d;
-  gu.gather_b = true;
   gu.out0 = g.w_gate;
   gu.out1 = g.w_up;
   gu.split = h;
@@ -311,7 +306,6 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   dn.B = l.sH;
   dn.ldb = h;
   dn.b_cols = h;
-  dn.gather_a = true;
   dn.out0 = g.w_down;
   dn.split = d;
   MOE_TRY(moe::launch_weights(wl, st), "weight gradients");

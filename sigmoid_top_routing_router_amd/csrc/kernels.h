@@ -223,9 +223,10 @@ hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int3
 // Gathered operands (x, dy) and the tiles' rows of direct ones are smaller
 // than this.
 constexpr uint32_t kGradMaxOperandBytes = 0xFFFE0000u;
-// C[row, n] = sum over the segments of sum_k A[row, k] B[k, n]; rows of A from
-// the tile table (expert, first row, rows, offset), through gather when set
-// (row -> gather[row] / gather_div of a_rows), or 0 .. rows_dense - 1.
+// C[row, n] = sum over the segments of sum_k A[row, k] B[k, n].  Pairs: rows
+// from the tile table (expert, first row, rows, offset); with an fp32 result
+// A's rows are gathered (row -> gather[row] / gather_div of a_rows).  Tokens:
+// rows 0 .. rows_dense - 1.
 struct RowsSegment {
   const uint16_t* A;
   int64_t lda;             // elements
@@ -245,15 +246,16 @@ struct RowsProblem {
   int64_t rows_dense;
   int ncols;               // multiple of 8 (bf16 out) or 4
   int n_tiles_n;           // set by the launcher
-  void* out;
+  void* out;               // fp32 or bf16
   int64_t ldo;
-  bool out_f32;
 };
-int grad_tile_rows();      // rows of a tile in the tables below
-hipError_t launch_rows(const RowsProblem* token, const RowsProblem* pair, hipStream_t stream);
+int grad_tile_rows();      // rows of a tile in the table of launch_row_tiles
+hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool out_f32,
+                       hipStream_t stream);
 // C[m, n] = sum_row A[row, m] B[row, n] in bf16, rows offsets[e] ..
-// offsets[e + 1] - 1 (or all rows_dense); A or B may be gathered through
-// src[row] / src_div (of src_rows rows).  Output rows m < split go to out0,
+// offsets[e + 1] - 1 (dense: all rows_dense).  The expert problems gather
+// through src[row] / src_div (of src_rows rows): B of the first (gate and up,
+// x), A of the second (down, dy).  Output rows m < split go to out0,
 // the others to out1.
 struct WeightsProblem {
   const uint16_t* A;
@@ -267,7 +269,6 @@ struct WeightsProblem {
   const int32_t* src;
   int src_div;
   int64_t src_rows;
-  bool gather_a, gather_b;
   uint16_t* out0;
   uint16_t* out1;
   int split;

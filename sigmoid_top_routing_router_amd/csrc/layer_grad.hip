@@ -21,7 +21,11 @@
 // v_mfma_f32_32x32x16_bf16, eight waves of 128 x 64, two waves to a SIMD.
 // A stage (32 KB of each operand) is in LDS twice; the next one's LDS-DMA
 // loads are issued as soon as every wave has left the stage before, so they
-// have a whole stage of MFMAs to land.  An operand whose k runs across rows
+// have a whole stage of MFMAs to land.  The loads are written in assembly
+// (they have no register result): as builtins, the compiler waits for all of
+// them in front of the first transposing LDS read, which it takes for a
+// possible reader of what they write, and a stage then never overlaps the
+// next one's loads.  An operand whose k runs across rows
 // is kept as [k][256] in LDS and read with the transposing LDS read
 // (ds_read_b64_tr_b16: 16 lanes fetch 4 k x 16 columns and each gets one
 // column's four k), so no transposed copy of a weight or an activation is
@@ -58,6 +62,26 @@ __device__ __forceinline__ void stage_barrier() {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const bf16x2_t v = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, v);
+}
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+// Raw buffer descriptor in scalar registers (stride 0; reads past `bytes`
+// return zeros).
+__device__ __forceinline__ i32x4_t buffer_at(const void* base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)base;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// LDS-DMA: 16 bytes per lane from buffer + off to LDS at l + 16 * lane.
+// Counted on vmcnt; the waits are this file's own (wait_vmcnt).  m0 (the LDS
+// address) is set and used inside; nothing else in these kernels uses it.
+__device__ __forceinline__ void dma(i32x4_t r, uint32_t off, const char* l) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know these operands
+  const int at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(lds_void_t*)l);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(at), "v"(off), "s"(r) : "memory");
+#endif
 }
 
 // Work item of a block: blocks are dealt to the XCDs in turn, each XCD takes
@@ -169,12 +193,16 @@ __device__ __forceinline__ void clear_acc(floatx16_t (&acc)[4][2]) {
 }
 
 // ---------------------------------------------------------------- rows
+// PAIR: rows of the tile table, else tokens.  F32: the fp32 result (Q), whose
+// pairs gather their rows of A; else bf16 (parts of dx).
+template <bool PAIR, bool F32>
 __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, char* lds) {
+  constexpr bool GATHER = PAIR && F32;
   const int64_t mt = item / p.n_tiles_n;
   const int nt = (int)(item % p.n_tiles_n);
   int expert = 0, rows;
   int64_t row0;
-  if (p.tiles) {
+  if constexpr (PAIR) {
     const int4 ent = reinterpret_cast<const int4*>(p.tiles)[mt];
     expert = ent.x;
     row0 = ent.y;
@@ -195,11 +223,12 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
   const int b_k = 2 * wave + (lane >> 5);
   const int b_chunk = (lane & 31) ^ (4 * (b_k & 3));
   const bool b_col = n0 + 8 * b_chunk < p.ncols;
-  int64_t a_row[4];
+  uint32_t a_row[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * (8 * i + wave) + (lane >> 3);
-    a_row[i] = r < rows ? (p.gather ? (int64_t)(p.gather[row0 + r] / p.gather_div) : (int64_t)r) : -1;
+    a_row[i] = r >= rows ? 0xFFFFFFFFu
+               : GATHER ? (uint32_t)p.gather[row0 + r] / (uint32_t)p.gather_div : (uint32_t)r;
   }
   floatx16_t acc[4][2];
   clear_acc(acc);
@@ -212,16 +241,16 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
   for (int sgi = 0; sgi < p.n_seg; ++sgi) {
     const RowsSegment& sg = p.seg[sgi];
     // a gathered A spans the whole buffer, a direct one this tile's rows
-    const __amdgpu_buffer_rsrc_t ra =
-        p.gather ? make_rsrc(sg.A, (uint32_t)(p.a_rows * sg.lda * 2))
-                 : make_rsrc(sg.A + row0 * sg.lda, (uint32_t)(rows * sg.lda * 2));
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(sg.B + (int64_t)expert * sg.b_expert_stride,
-                                                (uint32_t)sg.kdim * (uint32_t)p.ncols * 2u);
+    const i32x4_t ra = buffer_at(GATHER ? sg.A : sg.A + row0 * sg.lda,
+                                 (uint32_t)((GATHER ? p.a_rows : rows) * sg.lda * 2));
+    const i32x4_t rb = buffer_at(sg.B + (int64_t)expert * sg.b_expert_stride,
+                                 (uint32_t)sg.kdim * (uint32_t)p.ncols * 2u);
     const int nk = (sg.kdim + TK - 1) / TK;
     uint32_t a_off[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      a_off[i] = a_row[i] >= 0 ? (uint32_t)(a_row[i] * sg.lda * 2) + (uint32_t)a_chunk * 16u : kNoAddr;
+      a_off[i] = a_row[i] != 0xFFFFFFFFu
+                     ? a_row[i] * (uint32_t)(sg.lda * 2) + (uint32_t)a_chunk * 16u : kNoAddr;
     const uint32_t b_base = (uint32_t)(n0 + 8 * b_chunk) * 2u;
     const uint32_t b_pitch = (uint32_t)p.ncols * 2u;
     auto issue = [&](int ks, int slot) {
@@ -230,13 +259,12 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
       const bool ka = k0 + 8 * a_chunk < sg.kdim;  // kdim % 8 == 0: whole chunks
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        dma16(ra, ka && a_row[i] >= 0 ? a_off[i] + (uint32_t)k0 * 2u : kNoAddr, 0,
-              (lds_void_t*)(s + (8 * i + wave) * 1024));
+        dma(ra, ka ? a_off[i] + (uint32_t)k0 * 2u : kNoAddr, s + (8 * i + wave) * 1024);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = k0 + 16 * i + b_k;
-        dma16(rb, b_col && k < sg.kdim ? b_base + (uint32_t)k * b_pitch : kNoAddr, 0,
-              (lds_void_t*)(s + kOpBytes + (8 * i + wave) * 1024));
+        dma(rb, b_col && k < sg.kdim ? b_base + (uint32_t)k * b_pitch : kNoAddr,
+            s + kOpBytes + (8 * i + wave) * 1024);
       }
     };
     // the slot is free: the barrier that opened the stage before this one (the
@@ -257,7 +285,7 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
     }
   }
 
-  if (p.out_f32) {
+  if constexpr (F32) {
     float* out = reinterpret_cast<float*>(p.out);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -282,23 +310,30 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
                   [&](int r) { return r < rows ? out + r * p.ldo : nullptr; });
 }
 
-// Problem t first (rows of tokens: fewer, longer items), then problem r (rows
-// of pairs).
-__global__ __launch_bounds__(512, 2) void rows_kernel(RowsProblem t, RowsProblem r,
-                                                      int64_t t_blocks) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  const bool first = (int64_t)blockIdx.x < t_blocks;
-  const RowsProblem& p = first ? t : r;
-  const int64_t b = first ? blockIdx.x : (int64_t)blockIdx.x - t_blocks;
-  const int64_t m_tiles = p.tiles ? (int64_t)*p.n_tiles : (p.rows_dense + TM - 1) / TM;
+// The work item of block b of a problem's share of the grid.
+template <bool PAIR, bool F32>
+__device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b, char* lds) {
+  const int64_t m_tiles = PAIR ? (int64_t)*p.n_tiles : (p.rows_dense + TM - 1) / TM;
   const int64_t work = m_tiles * p.n_tiles_n;
   const int64_t share = (work + kXcds - 1) / kXcds;
   if (b / kXcds >= share) return;
   const int64_t item = xcd_item(b, share);
-  if (item < work) rows_tile(p, item, lds);
+  if (item < work) rows_tile<PAIR, F32>(p, item, lds);
+}
+
+// The tokens' blocks first (fewer items), then the pairs'.
+template <bool F32>
+__global__ __launch_bounds__(512, 2) void rows_kernel(RowsProblem token, RowsProblem pair,
+                                                      int64_t token_blocks) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int64_t b = blockIdx.x;
+  if (b < token_blocks) rows_block<false, F32>(token, b, lds);
+  else rows_block<true, F32>(pair, b - token_blocks, lds);
 }
 
 // ---------------------------------------------------------------- weights
+enum Gathered { kNeither, kA, kB };
+template <Gathered GATHER>
 __device__ __forceinline__ void weights_tile(const WeightsProblem& p, int expert, int tile,
                                              char* lds) {
   const int m0 = (tile / p.tiles_n) * TM;
@@ -319,8 +354,8 @@ __device__ __forceinline__ void weights_tile(const WeightsProblem& p, int expert
   const bool a_in = m0 + 8 * chunk < p.a_cols, b_in = n0 + 8 * chunk < p.b_cols;
   const uint32_t a_col = (uint32_t)(m0 + 8 * chunk) * 2u, b_col = (uint32_t)(n0 + 8 * chunk) * 2u;
   uint32_t* ids = reinterpret_cast<uint32_t*>(lds + kIdsOff);
-  const bool gather = p.gather_a || p.gather_b;
-  const uint32_t g_pitch = (uint32_t)(p.gather_a ? p.lda : p.ldb) * 2u;
+  const uint32_t a_pitch = (uint32_t)p.lda * 2u, b_pitch = (uint32_t)p.ldb * 2u;
+  const uint32_t g_pitch = GATHER == kA ? a_pitch : b_pitch;
 
   floatx16_t acc[4][2];
   clear_acc(acc);
@@ -331,32 +366,32 @@ __device__ __forceinline__ void weights_tile(const WeightsProblem& p, int expert
     const int cr = (int)min((int64_t)kIdsMax, rows - c0);
     const int nk = (cr + TK - 1) / TK;
     if (c0 > 0) stage_barrier();  // the chunk before is read to its end
-    if (gather) {
+    if constexpr (GATHER != kNeither) {
       for (int r = tid; r < nk * TK; r += 512)
         ids[r] = r < cr ? (uint32_t)(p.src[first + c0 + r] / p.src_div) * g_pitch : kNoAddr;
       __syncthreads();
     }
     // direct operands: this chunk's rows; gathered ones: the whole buffer
     const int64_t base = first + c0;
-    const __amdgpu_buffer_rsrc_t ra =
-        p.gather_a ? make_rsrc(p.A, (uint32_t)(p.src_rows * p.lda * 2))
-                   : make_rsrc(p.A + base * p.lda, (uint32_t)(cr * p.lda * 2));
-    const __amdgpu_buffer_rsrc_t rb =
-        p.gather_b ? make_rsrc(p.B, (uint32_t)(p.src_rows * p.ldb * 2))
-                   : make_rsrc(p.B + base * p.ldb, (uint32_t)(cr * p.ldb * 2));
+    const i32x4_t ra = buffer_at(GATHER == kA ? p.A : p.A + base * p.lda,
+                                 (uint32_t)((GATHER == kA ? p.src_rows : cr) * p.lda * 2));
+    const i32x4_t rb = buffer_at(GATHER == kB ? p.B : p.B + base * p.ldb,
+                                 (uint32_t)((GATHER == kB ? p.src_rows : cr) * p.ldb * 2));
     auto issue = [&](int ks, int slot) {
       char* s = lds + slot * kSlotBytes;
+      uint32_t at[4];
+      if constexpr (GATHER != kNeither) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = ids[ks * TK + 16 * i + kr];
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = ks * TK + 16 * i + kr;
         const bool in = r < cr;
-        uint32_t ga = 0, gb = 0;
-        if (gather) ga = gb = ids[r];
-        if (!p.gather_a) ga = (uint32_t)r * (uint32_t)p.lda * 2u;
-        if (!p.gather_b) gb = (uint32_t)r * (uint32_t)p.ldb * 2u;
-        dma16(ra, in && a_in ? ga + a_col : kNoAddr, 0, (lds_void_t*)(s + (8 * i + wave) * 1024));
-        dma16(rb, in && b_in ? gb + b_col : kNoAddr, 0,
-              (lds_void_t*)(s + kOpBytes + (8 * i + wave) * 1024));
+        const uint32_t ga = GATHER == kA ? at[i] : (uint32_t)r * a_pitch;
+        const uint32_t gb = GATHER == kB ? at[i] : (uint32_t)r * b_pitch;
+        dma(ra, in && a_in ? ga + a_col : kNoAddr, s + (8 * i + wave) * 1024);
+        dma(rb, in && b_in ? gb + b_col : kNoAddr, s + kOpBytes + (8 * i + wave) * 1024);
       }
     };
     issue(0, 0);
@@ -386,7 +421,7 @@ __global__ __launch_bounds__(512, 2) void weights_kernel(WeightsLaunch w) {
   for (int i = 0; i < w.n_dense; ++i) {
     const int t = w.dense[i].tiles_m * w.dense[i].tiles_n;
     if (b < t) {
-      weights_tile(w.dense[i], 0, (int)b, lds);
+      weights_tile<kNeither>(w.dense[i], 0, (int)b, lds);
       return;
     }
     b -= t;
@@ -400,8 +435,8 @@ __global__ __launch_bounds__(512, 2) void weights_kernel(WeightsLaunch w) {
   if (item >= work) return;
   const int e = (int)(item / (t0 + t1));
   const int r = (int)(item % (t0 + t1));
-  if (r < t0) weights_tile(w.expert[0], e, r, lds);
-  else weights_tile(w.expert[1], e, r - t0, lds);
+  if (r < t0) weights_tile<kB>(w.expert[0], e, r, lds);
+  else weights_tile<kA>(w.expert[1], e, r - t0, lds);
 }
 
 // ---------------------------------------------------------------- small kernels
@@ -543,21 +578,28 @@ static int64_t rows_blocks(const RowsProblem& p) {
   return (m_tiles * p.n_tiles_n + kXcds - 1) / kXcds * kXcds;
 }
 
-hipError_t launch_rows(const RowsProblem* token, const RowsProblem* pair, hipStream_t stream) {
+template <bool F32>
+static hipError_t start_rows(const RowsProblem& t, const RowsProblem& r, int64_t token_blocks,
+                             int64_t blocks, hipStream_t stream) {
   static std::atomic<uint32_t> configured{0};
-  hipError_t e = set_lds_limit_once((const void*)rows_kernel, kLdsBytes, configured);
+  const hipError_t e = set_lds_limit_once((const void*)rows_kernel<F32>, kLdsBytes, configured);
   if (e != hipSuccess) return e;
-  RowsProblem t{}, r{};
+  hipLaunchKernelGGL(rows_kernel<F32>, dim3((unsigned)blocks), dim3(512), kLdsBytes, stream, t, r,
+                     token_blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool out_f32,
+                       hipStream_t stream) {
+  RowsProblem t{}, r = pair;
   if (token) t = *token;
-  if (pair) r = *pair;
   t.n_tiles_n = (t.ncols + TN - 1) / TN;
   r.n_tiles_n = (r.ncols + TN - 1) / TN;
   const int64_t tb = token ? rows_blocks(t) : 0;
-  const int64_t blocks = tb + (pair ? rows_blocks(r) : 0);
+  const int64_t blocks = tb + rows_blocks(r);
   if (blocks > 0x7FFFFFF0LL) return hipErrorInvalidConfiguration;
-  if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL(rows_kernel, dim3((unsigned)blocks), dim3(512), kLdsBytes, stream, t, r, tb);
-  return hipGetLastError();
+  return out_f32 ? start_rows<true>(t, r, tb, blocks, stream)
+                 : start_rows<false>(t, r, tb, blocks, stream);
 }
 
 hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
