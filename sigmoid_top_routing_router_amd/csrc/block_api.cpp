@@ -104,14 +104,19 @@ moe::BalanceWork carve_balance(void* ws, int64_t N, int32_t E, int32_t n_seg, si
 
 // ---- layer backward
 struct GradLayout {
-  int32_t *ids, *counts, *offsets, *sorted_src, *src_pos, *tiles, *n_tiles, *row_tiles, *n_row_tiles;
+  int32_t *ids, *counts, *offsets, *sorted_src, *src_pos, *tiles, *n_tiles, *row_tiles, *n_row_tiles,
+      *tok;
   uint32_t* block_counts;
   float *S, *Q, *Qs, *dscore;
-  uint16_t *dGU, *sH, *dXp, *dGUs, *Hs, *dzb, *base;
+  uint16_t *hid, *dXp, *hids, *dzb, *base;
+  int64_t ld, lds;  // row pitch of hid and of hids (the shared expert's)
   int64_t max_tiles, max_row_tiles;
   int ldb;
   size_t bytes;
 };
+// Rows of dG | dU | s H: an odd number of 128-byte lines, so that the same
+// columns of neighbouring rows lie in different channels of the cache.
+int64_t hidden_pitch(int h) { return ((3 * (int64_t)h + 63) / 64 | 1) * 64; }
 GradLayout carve_grad(void* ws, const moe_problem_t& p) {
   char* const base = (char*)ws;
   size_t off = 0;
@@ -136,16 +141,17 @@ GradLayout carve_grad(void* ws, const moe_problem_t& p) {
   l.max_row_tiles = moe::perm_max_tiles((int64_t)pairs, p.E, moe::grad_tile_rows());
   l.row_tiles = (int32_t*)take((size_t)l.max_row_tiles * 16);
   l.n_row_tiles = (int32_t*)take(16);
+  l.tok = (int32_t*)take(pairs * 4);
   // Q is read for the last time before the pairs' part of grad_x is written
   void* q = take(pairs * (size_t)(p.h * 4 > p.d * 2 ? p.h * 4 : p.d * 2));
   l.Q = (float*)q;
   l.dXp = (uint16_t*)q;
-  l.dGU = (uint16_t*)take(pairs * 2 * p.h * 2);
-  l.sH = (uint16_t*)take(pairs * p.h * 2);
+  l.ld = hidden_pitch(p.h);
+  l.lds = hidden_pitch((int)hs);
+  l.hid = (uint16_t*)take(pairs * l.ld * 2);
   l.dscore = (float*)take(pairs * (size_t)moe::gateup_col_tiles(p.h) * 4);
   l.Qs = (float*)take(N * hs * 4);
-  l.dGUs = (uint16_t*)take(N * 2 * hs * 2);
-  l.Hs = (uint16_t*)take(N * hs * 2);
+  l.hids = (uint16_t*)take(hs ? N * l.lds * 2 : 0);
   l.dzb = (uint16_t*)take(N * (size_t)l.ldb * 2);
   l.base = (uint16_t*)take(N * p.d * 2);
   l.bytes = off;
@@ -190,7 +196,9 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   pw.n_tiles = l.n_tiles;
   MOE_TRY(moe::launch_permute(l.ids, N, E, K, moe::gemm_bm(), moe::gemm_xrows(), pw, st),
           "grouping");
-  MOE_TRY(moe::launch_row_tiles(l.offsets, E, l.row_tiles, l.n_row_tiles, st), "row tiles");
+  MOE_TRY(moe::launch_grouped_rows(l.sorted_src, pairs, K, l.offsets, E, l.tok, l.row_tiles,
+                                   l.n_row_tiles, st),
+          "grouped rows");
 
   auto pair_rows = [&] {
     moe::RowsProblem r{};
@@ -209,8 +217,7 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     moe::RowsProblem r = pair_rows(), t = token_rows();
     r.seg[0] = {dy, d, w.w_down, (int64_t)d * h, d};
     r.n_seg = 1;
-    r.gather = l.sorted_src;
-    r.gather_div = K;
+    r.gather = l.tok;
     r.a_rows = N;
     r.ncols = h;
     r.out = l.Q;
@@ -226,11 +233,11 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   }
   // G, U again; dG, dU, s H and the score gradients
   MOE_TRY(moe::launch_gateup_grad(x, N, l.sorted_src, K, l.tiles, l.n_tiles, l.max_tiles, 0,
-                                  w.w_gate, w.w_up, d, h, l.Q, l.S, l.dGU, l.sH, l.dscore, st),
+                                  w.w_gate, w.w_up, d, h, l.Q, l.S, l.hid, l.ld, l.dscore, st),
           "gate/up gradient");
   if (shared)
     MOE_TRY(moe::launch_gateup_grad(x, N, nullptr, 1, nullptr, nullptr, 0, N, w.ws_gate, w.ws_up,
-                                    d, hs, l.Qs, nullptr, l.dGUs, l.Hs, nullptr, st),
+                                    d, hs, l.Qs, nullptr, l.hids, l.lds, nullptr, st),
             "shared gate/up gradient");
   MOE_TRY(moe::launch_logits_grad(Z, ids, l.src_pos, l.dscore, moe::gateup_col_tiles(h), N, E, K,
                                   grad_logits, g.logits, router ? l.dzb : nullptr, l.ldb, st),
@@ -239,15 +246,15 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   {
     moe::RowsProblem r = pair_rows(), t = token_rows();
     const int64_t es = (int64_t)h * d;
-    r.seg[0] = {l.dGU, 2 * (int64_t)h, w.w_gate, es, h};
-    r.seg[1] = {l.dGU + h, 2 * (int64_t)h, w.w_up, es, h};
+    r.seg[0] = {l.hid, l.ld, w.w_gate, es, h};
+    r.seg[1] = {l.hid + h, l.ld, w.w_up, es, h};
     r.n_seg = 2;
     r.ncols = d;
     r.out = l.dXp;
     r.ldo = d;
     if (shared) {
-      t.seg[t.n_seg++] = {l.dGUs, 2 * (int64_t)hs, w.ws_gate, 0, hs};
-      t.seg[t.n_seg++] = {l.dGUs + hs, 2 * (int64_t)hs, w.ws_up, 0, hs};
+      t.seg[t.n_seg++] = {l.hids, l.lds, w.ws_gate, 0, hs};
+      t.seg[t.n_seg++] = {l.hids + hs, l.lds, w.ws_up, 0, hs};
     }
     if (router) t.seg[t.n_seg++] = {l.dzb, l.ldb, w.w_router, 0, E};
     t.ncols = d;
@@ -259,10 +266,9 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   }
   // the weights' gradients, one launch
   moe::WeightsLaunch wl{};
-  auto dense = [&](const uint16_t* A, int64_t lda, int a_cols, const uint16_t* B, int64_t ldb,
-                   int b_cols, uint16_t* out0, uint16_t* out1, int split) {
-    moe::WeightsProblem& q = wl.dense[wl.n_dense++];
-    q = {};
+  auto problem = [&](const uint16_t* A, int64_t lda, int a_cols, const uint16_t* B, int64_t ldb,
+                     int b_cols, uint16_t* out) {
+    moe::WeightsProblem q{};
     q.A = A;
     q.lda = lda;
     q.a_cols = a_cols;
@@ -270,44 +276,23 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     q.ldb = ldb;
     q.b_cols = b_cols;
     q.rows_dense = N;
-    q.src_div = 1;
-    q.out0 = out0;
-    q.out1 = out1;
-    q.split = split;
+    q.out = out;
+    q.offsets = l.offsets;
+    q.tok = l.tok;
+    q.tok_rows = N;
+    q.out_stride = (int64_t)h * d;
+    return q;
   };
   if (shared) {
-    dense(l.dGUs, 2 * (int64_t)hs, 2 * hs, x, d, d, g.ws_gate, g.ws_up, hs);
-    dense(dy, d, d, l.Hs, hs, hs, g.ws_down, nullptr, d);
+    wl.dense[wl.n_dense++] = problem(l.hids, l.lds, hs, x, d, d, g.ws_gate);
+    wl.dense[wl.n_dense++] = problem(l.hids + hs, l.lds, hs, x, d, d, g.ws_up);
+    wl.dense[wl.n_dense++] = problem(dy, d, d, l.hids + 2 * hs, l.lds, hs, g.ws_down);
   }
-  if (router) dense(l.dzb, l.ldb, E, x, d, d, g.w_router, nullptr, E);
+  if (router) wl.dense[wl.n_dense++] = problem(l.dzb, l.ldb, E, x, d, d, g.w_router);
+  wl.expert[0] = problem(l.hid, l.ld, h, x, d, d, g.w_gate);
+  wl.expert[1] = problem(l.hid + h, l.ld, h, x, d, d, g.w_up);
+  wl.expert[2] = problem(dy, d, d, l.hid + 2 * h, l.ld, h, g.w_down);
   wl.E = E;
-  for (int i = 0; i < 2; ++i) {
-    moe::WeightsProblem& q = wl.expert[i];
-    q.offsets = l.offsets;
-    q.src = l.sorted_src;
-    q.src_div = K;
-    q.src_rows = N;
-    q.out_stride = (int64_t)h * d;
-  }
-  moe::WeightsProblem& gu = wl.expert[0];
-  gu.A = l.dGU;
-  gu.lda = 2 * (int64_t)h;
-  gu.a_cols = 2 * h;
-  gu.B = x;
-  gu.ldb = d;
-  gu.b_cols = d;
-  gu.out0 = g.w_gate;
-  gu.out1 = g.w_up;
-  gu.split = h;
-  moe::WeightsProblem& dn = wl.expert[1];
-  dn.A = dy;
-  dn.lda = d;
-  dn.a_cols = d;
-  dn.B = l.sH;
-  dn.ldb = h;
-  dn.b_cols = h;
-  dn.out0 = g.w_down;
-  dn.split = d;
   MOE_TRY(moe::launch_weights(wl, st), "weight gradients");
   return moe::set_error(MOE_OK, "");
 }

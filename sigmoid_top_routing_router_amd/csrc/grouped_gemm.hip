@@ -388,8 +388,7 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& a, floatx16_t (&ac
       const int64_t orow = row0 + rr;
       const float s = a.row_scale ? a.row_scale[a.gather[orow]] : 1.0f;
       const float* q = a.q_in + orow * h + col0 + ocol_l;
-      uint16_t* dg = a.dgu_out + orow * 2 * h + col0 + ocol_l;
-      uint16_t* hh = a.sh_out + orow * h + col0 + ocol_l;
+      uint16_t* dg = a.hid_out + orow * a.hid_ld + col0 + ocol_l;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 qv = *reinterpret_cast<const float4*>(q + 8 * k);
@@ -410,7 +409,8 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& a, floatx16_t (&ac
         *reinterpret_cast<uint2*>(dg + 8 * k) = make_uint2(pack2(o0[0], o0[1]), pack2(o0[2], o0[3]));
         *reinterpret_cast<uint2*>(dg + h + 8 * k) =
             make_uint2(pack2(o1[0], o1[1]), pack2(o1[2], o1[3]));
-        *reinterpret_cast<uint2*>(hh + 8 * k) = make_uint2(pack2(o2[0], o2[1]), pack2(o2[2], o2[3]));
+        *reinterpret_cast<uint2*>(dg + 2 * h + 8 * k) =
+            make_uint2(pack2(o2[0], o2[1]), pack2(o2[2], o2[3]));
       }
     }
     part += __shfl_xor(part, 32);
@@ -1457,14 +1457,15 @@ hipError_t launch_gateup(const uint16_t* x, int64_t x_rows, const int32_t* sorte
 hipError_t launch_gateup_grad(const uint16_t* x, int64_t x_rows, const int32_t* sorted_src, int K,
                               const int32_t* tiles, const int32_t* n_tiles, int64_t max_tiles,
                               int64_t rows_dense, const uint16_t* w_gate, const uint16_t* w_up,
-                              int d, int h, const float* Q, const float* row_scale, uint16_t* dGU,
-                              uint16_t* sH, float* dscore_part, hipStream_t stream) {
+                              int d, int h, const float* Q, const float* row_scale,
+                              uint16_t* hid, int64_t hid_ld, float* dscore_part,
+                              hipStream_t stream) {
   GemmArgs a = gateup_args(x, x_rows, sorted_src, K, tiles, n_tiles, rows_dense, w_gate, w_up, d,
                            h, nullptr);
   a.q_in = Q;
   a.row_scale = row_scale;
-  a.dgu_out = dGU;
-  a.sh_out = sH;
+  a.hid_out = hid;
+  a.hid_ld = hid_ld;
   a.dscore_part = dscore_part;
   const int64_t mt = tiles ? max_tiles : (rows_dense + BM - 1) / BM;
   return launch_gemm(kGateUpGrad, a, mt, stream);

@@ -121,13 +121,14 @@ hipError_t launch_gateup(const uint16_t* x, int64_t x_rows, const int32_t* sorte
 // rows; h_rows * h * 2 < 4 GiB.
 // The gate/up product of the backward pass over the same rows (see the
 // kernel's epilogue): from Q [rows][h] fp32 and the pairs' weights row_scale
-// [N*K] (NULL: 1) it writes dGU [rows][2h] = dG | dU, sH [rows][h] and, when
-// given, the score gradients' partial sums [rows][gateup_col_tiles(h)].
+// [N*K] (NULL: 1) it writes hid [rows][hid_ld] = dG | dU | s H and, when given,
+// the score gradients' partial sums [rows][gateup_col_tiles(h)].
 hipError_t launch_gateup_grad(const uint16_t* x, int64_t x_rows, const int32_t* sorted_src, int K,
                               const int32_t* tiles, const int32_t* n_tiles, int64_t max_tiles,
                               int64_t rows_dense, const uint16_t* w_gate, const uint16_t* w_up,
-                              int d, int h, const float* Q, const float* row_scale, uint16_t* dGU,
-                              uint16_t* sH, float* dscore_part, hipStream_t stream);
+                              int d, int h, const float* Q, const float* row_scale,
+                              uint16_t* hid, int64_t hid_ld, float* dscore_part,
+                              hipStream_t stream);
 inline int gateup_col_tiles(int h) { return (h + 127) / 128; }
 hipError_t launch_down(const uint16_t* H, int64_t h_rows, const int32_t* tiles, const int32_t* n_tiles,
                        int64_t max_tiles, int64_t rows_dense, const uint16_t* w_down,
@@ -225,8 +226,8 @@ hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int3
 constexpr uint32_t kGradMaxOperandBytes = 0xFFFE0000u;
 // C[row, n] = sum over the segments of sum_k A[row, k] B[k, n].  Pairs: rows
 // from the tile table (expert, first row, rows, offset); with an fp32 result
-// A's rows are gathered (row -> gather[row] / gather_div of a_rows).  Tokens:
-// rows 0 .. rows_dense - 1.
+// A's rows are gathered (row -> gather[row] of a_rows).  Tokens: rows 0 ..
+// rows_dense - 1.
 struct RowsSegment {
   const uint16_t* A;
   int64_t lda;             // elements
@@ -238,7 +239,6 @@ struct RowsProblem {
   RowsSegment seg[3];
   int n_seg;
   const int32_t* gather;
-  int gather_div;
   int64_t a_rows;
   const int32_t* tiles;
   const int32_t* n_tiles;
@@ -249,14 +249,12 @@ struct RowsProblem {
   void* out;               // fp32 or bf16
   int64_t ldo;
 };
-int grad_tile_rows();      // rows of a tile in the table of launch_row_tiles
+int grad_tile_rows();      // rows of a tile in the table of launch_grouped_rows
 hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool out_f32,
                        hipStream_t stream);
 // C[m, n] = sum_row A[row, m] B[row, n] in bf16, rows offsets[e] ..
-// offsets[e + 1] - 1 (dense: all rows_dense).  The expert problems gather
-// through src[row] / src_div (of src_rows rows): B of the first (gate and up,
-// x), A of the second (down, dy).  Output rows m < split go to out0,
-// the others to out1.
+// offsets[e + 1] - 1 (dense: all rows_dense).  The expert problems are gate,
+// up (rows of B, x, through tok[row], of tok_rows rows) and down (A, dy).
 struct WeightsProblem {
   const uint16_t* A;
   int64_t lda;
@@ -266,26 +264,25 @@ struct WeightsProblem {
   int b_cols;
   const int32_t* offsets;
   int64_t rows_dense;
-  const int32_t* src;
-  int src_div;
-  int64_t src_rows;
-  uint16_t* out0;
-  uint16_t* out1;
-  int split;
+  const int32_t* tok;
+  int64_t tok_rows;
+  uint16_t* out;
   int64_t out_stride;      // elements between experts
   int tiles_m, tiles_n;    // set by the launcher
 };
 struct WeightsLaunch {
-  WeightsProblem dense[3];
+  WeightsProblem dense[4];
   int n_dense;
-  WeightsProblem expert[2];
+  WeightsProblem expert[3];
   int E;
+  int expert_items;        // set by the launcher
 };
 hipError_t launch_weights(WeightsLaunch w, hipStream_t stream);
 hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E, int K,
                         int32_t* ids_out, float* S, hipStream_t stream);
-hipError_t launch_row_tiles(const int32_t* offsets, int E, int32_t* tiles, int32_t* n_tiles,
-                            hipStream_t stream);
+hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K,
+                               const int32_t* offsets, int E, int32_t* tok, int32_t* tiles,
+                               int32_t* n_tiles, hipStream_t stream);
 hipError_t launch_logits_grad(const float* Z, const int32_t* ids, const int32_t* src_pos,
                               const float* dscore_part, int parts, int64_t N, int E, int K,
                               const float* grad_in, float* grad_out, uint16_t* dzb, int ldb,

@@ -17,11 +17,14 @@
 //  * weights_kernel: every weight gradient, C[m, n] = sum_row A[row, m]
 //    B[row, n] over the rows of an expert's segment: both operands n
 //    contiguous.
-// Both multiply 256 x 256 tiles in stages of 64 k with
-// v_mfma_f32_32x32x16_bf16, eight waves of 128 x 64, two waves to a SIMD.
-// A stage (32 KB of each operand) is in LDS twice; the next one's LDS-DMA
-// loads are issued as soon as every wave has left the stage before, so they
-// have a whole stage of MFMAs to land.  The loads are written in assembly
+// Both give every wave 128 x 64 outputs of v_mfma_f32_32x32x16_bf16, eight
+// waves to a CU.  rows_kernel has long sums: one block of eight waves, 256 x
+// 256 outputs, stages of 64 k kept twice in LDS; the next stage's LDS-DMA
+// loads are issued as soon as every wave has left the stage before.
+// weights_kernel has short ones (an expert's rows, some 256) and large
+// results: stages of 32 k kept four times, and a block takes up to four 256 x
+// 256 tiles under each other as one stream of stages, so that a tile's first
+// loads and the last tile's stores pass behind MFMAs.  The loads are written in assembly
 // (they have no register result): as builtins, the compiler waits for all of
 // them in front of the first transposing LDS read, which it takes for a
 // possible reader of what they write, and a stage then never overlaps the
@@ -31,6 +34,8 @@
 // column's four k), so no transposed copy of a weight or an activation is
 // ever made.  Its 16-byte chunk c of row k sits at c ^ 4 (k & 3): the four k
 // of one read are then on four different groups of banks.
+#include <type_traits>
+
 #include "common.h"
 #include "gemm_args.h"
 #include "kernels.h"
@@ -39,13 +44,23 @@ namespace moe {
 
 namespace {
 
-constexpr int TM = 256, TN = 256, TK = 64;
+constexpr int TN = 256;                        // columns of a tile
+// rows_kernel
+constexpr int TM = 256, TK = 64;
 constexpr int kOpBytes = 32 * 1024;            // one operand of one stage
 constexpr int kSlotBytes = 2 * kOpBytes;
-constexpr int kIdsOff = 2 * kSlotBytes;        // gathered row offsets (weights_kernel)
-constexpr int kIdsMax = 8192;
-constexpr int kLdsBytes = 160 * 1024;
-static_assert(kIdsOff + kIdsMax * 4 <= kLdsBytes, "LDS layout");
+constexpr int kRowsLds = 2 * kSlotBytes + 8 * 1024;  // and the staged result
+// weights_kernel
+constexpr int WM = 256, WK = 32;
+constexpr int kWaBytes = WK * WM * 2;          // A of one stage, then B
+constexpr int kWSlot = kWaBytes + WK * TN * 2;
+constexpr int kWSlots = 4;
+constexpr int kIdsOff = kWSlots * kWSlot;      // gathered rows of eight stages
+constexpr int kIdsSlot = 64 * 4;               // a wave loads 64, the first 32 are used
+constexpr int kIdsSlots = 8;
+constexpr int kWeightsLds = kIdsOff + kIdsSlots * kIdsSlot;
+constexpr int kWGroup = 4;                     // tiles of a block
+static_assert(kWeightsLds <= 160 * 1024, "LDS");
 constexpr int kXcds = 8;
 // An offset past the end of any operand: the load returns zeros.  Operands
 // are smaller than this (checked by the entry point).
@@ -73,15 +88,27 @@ __device__ __forceinline__ i32x4_t buffer_at(const void* base, uint32_t bytes) {
                  __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu)),
                  __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
-// LDS-DMA: 16 bytes per lane from buffer + off to LDS at l + 16 * lane.
-// Counted on vmcnt; the waits are this file's own (wait_vmcnt).  m0 (the LDS
-// address) is set and used inside; nothing else in these kernels uses it.
-__device__ __forceinline__ void dma(i32x4_t r, uint32_t off, const char* l) {
+// LDS addresses are byte offsets of the block's LDS (these kernels have no
+// static LDS, so the dynamic array starts at 0).
+// LDS-DMA: 16 (dma4: 4) bytes per lane from buffer + off to LDS at `at` + 16
+// (4) * lane.  Counted on vmcnt; the waits are this file's own (wait_vmcnt).
+// m0 (the LDS address) is set and used inside; nothing else in these kernels
+// uses it.
+__device__ __forceinline__ void dma(i32x4_t r, uint32_t off, int at) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know these operands
-  const int at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(lds_void_t*)l);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(at), "v"(off), "s"(r) : "memory");
+               :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(r) : "memory");
 #endif
+}
+__device__ __forceinline__ void dma4(i32x4_t r, uint32_t off, int at) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(r) : "memory");
+#endif
+}
+template <class T>
+__device__ __forceinline__ T lds_read(int at) {
+  return *(const __attribute__((address_space(3))) T*)(uint32_t)at;
 }
 
 // Work item of a block: blocks are dealt to the XCDs in turn, each XCD takes
@@ -91,70 +118,51 @@ __device__ __forceinline__ int64_t xcd_item(int64_t block, int64_t share) {
 }
 
 // Eight k of one column from a [k][256] stage: two transposing reads.
-__device__ __forceinline__ bf16x8_t read_tr(const char* p) {
-  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
-  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * 512));
+__device__ __forceinline__ bf16x8_t read_tr(int at) {
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uint32_t)at);
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uint32_t)(at + 4 * 512));
   typedef short s16x8_t __attribute__((ext_vector_type(8)));
   const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// What a wave reads of a stage.  A operand: [256 rows][64 k], chunk c of row r
-// at c ^ ((r >> 1) & 7) (ATR false), or [64 k][256] (ATR true); B: [64 k][256].
-template <bool ATR>
-struct Frags {
-  int a_base, a_x[4], b_x[2];
-  __device__ __forceinline__ Frags(int lane, int wg, int wp) {
-    const int i = lane & 15, kq = i >> 2, half = (lane >> 4) & 1;
-    const int krow = (8 * (lane >> 5) + kq) * 512;
-    const int sub = (2 * half + ((i & 3) >> 1)) * 16 + (i & 1) * 8;
-    if (ATR) {
-      a_base = krow;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) a_x[m] = (16 * wg + 4 * (m ^ kq)) * 16 + sub;
-    } else {
-      a_base = (wg * 128 + (lane & 31)) * 128;
-#pragma unroll
-      for (int m = 0; m < 4; ++m)  // by k-step: chunk 2 ks + (lane >> 5)
-        a_x[m] = ((2 * m + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
-    }
-#pragma unroll
-    for (int f = 0; f < 2; ++f) b_x[f] = krow + ((8 * wp + 4 * f) ^ (4 * kq)) * 16 + sub;
+// What a lane reads of a [k][256] operand for the 32 columns of block blk:
+// block_off(blk) + 512 k of the k-step's first row.
+struct KRows {
+  int kq, row, sub;
+  __device__ __forceinline__ explicit KRows(int lane) {
+    const int i = lane & 15;
+    kq = i >> 2;
+    row = (8 * (lane >> 5) + kq) * 512;
+    sub = (2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) * 16 + (i & 1) * 8;
   }
-  __device__ __forceinline__ bf16x8_t a(const char* s, int ks, int m) const {
-    if (ATR) return read_tr(s + a_base + a_x[m] + ks * (16 * 512));
-    return *reinterpret_cast<const bf16x8_t*>(s + a_base + m * (32 * 128) + a_x[ks]);
-  }
-  __device__ __forceinline__ bf16x8_t b(const char* s, int ks, int f) const {
-    return read_tr(s + b_x[f] + ks * (16 * 512));
+  __device__ __forceinline__ int block_off(int blk) const {
+    return row + ((4 * blk) ^ (4 * kq)) * 16 + sub;
   }
 };
 
-template <bool ATR, int LIVE>
-__device__ __forceinline__ void multiply_stage(const char* slot, const Frags<ATR>& fr,
-                                               floatx16_t (&acc)[4][2]) {
+template <int LIVE>
+struct Fragments {  // of one k-step
+  bf16x8_t A[LIVE], B[2];
+};
+// FIRST: the tile's first products.
+template <bool FIRST, int LIVE>
+__device__ __forceinline__ void multiply(const Fragments<LIVE>& f, floatx16_t (&acc)[4][2]) {
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    bf16x8_t A[4], B[2];
+  for (int m = 0; m < LIVE; ++m)
 #pragma unroll
-    for (int f = 0; f < 2; ++f) B[f] = fr.b(slot + kOpBytes, ks, f);
-#pragma unroll
-    for (int m = 0; m < LIVE; ++m) A[m] = fr.a(slot, ks, m);
-#pragma unroll
-    for (int m = 0; m < LIVE; ++m)
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-        acc[m][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(B[f], A[m], acc[m][f], 0, 0, 0);
-  }
+    for (int i = 0; i < 2; ++i)
+      acc[m][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          f.B[i], f.A[m], FIRST ? floatx16_t{} : acc[m][i], 0, 0, 0);
 }
 
 // The accumulators hold the tile transposed (the B fragment is the first
 // operand): lane l has tile row (l & 31) of a block and columns 8 (r / 4) +
-// 4 (l / 32) + r % 4.  bf16 results pass through the idle LDS and leave as
+// 4 (l / 32) + r % 4.  rows_kernel's bf16 results pass through the idle LDS and leave as
 // 16-byte pieces of whole rows; row_ptr(r) is the output of tile row r, or
 // null.
 constexpr int kOutStride = TN * 2 + 8;
-static_assert(TM * kOutStride <= kLdsBytes, "staged tile");
+static_assert(TM * kOutStride <= kRowsLds, "staged tile");
 template <class RowPtr>
 __device__ __forceinline__ void store_bf16_tile(floatx16_t (&acc)[4][2], int lane, int wg, int wp,
                                                 int tid, char* lds, int cols, RowPtr row_ptr) {
@@ -223,67 +231,103 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
   const int b_k = 2 * wave + (lane >> 5);
   const int b_chunk = (lane & 31) ^ (4 * (b_k & 3));
   const bool b_col = n0 + 8 * b_chunk < p.ncols;
+  const uint32_t b_pitch = (uint32_t)p.ncols * 2u;
+  const uint32_t b_lane = (uint32_t)b_k * b_pitch + (uint32_t)(n0 + 8 * b_chunk) * 2u;
   uint32_t a_row[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * (8 * i + wave) + (lane >> 3);
-    a_row[i] = r >= rows ? 0xFFFFFFFFu
-               : GATHER ? (uint32_t)p.gather[row0 + r] / (uint32_t)p.gather_div : (uint32_t)r;
+    a_row[i] = r >= rows ? 0xFFFFFFFFu : GATHER ? (uint32_t)p.gather[row0 + r] : (uint32_t)r;
   }
-  floatx16_t acc[4][2];
-  clear_acc(acc);
-  const Frags<false> fr(lane, wg, wp);
-  int live_m = (rows - wg * 128 + 31) / 32;
-  live_m = __builtin_amdgcn_readfirstlane(live_m < 0 ? 0 : live_m > 4 ? 4 : live_m);
-  const bool live = __builtin_amdgcn_readfirstlane(live_m > 0 && n0 + wp * 64 < p.ncols);
-
-  int parity = 0;  // LDS slot of the next stage; runs on over the segments
-  for (int sgi = 0; sgi < p.n_seg; ++sgi) {
-    const RowsSegment& sg = p.seg[sgi];
+  // The segments' stages as one stream; this is the next one to load.
+  i32x4_t ra, rb;
+  uint32_t a_off[4];
+  int seg = -1, ks = 0, nk = 0, kdim = 0;
+  auto next_segment = [&] {
+    ++seg;
+    const RowsSegment& sg = p.seg[seg];
     // a gathered A spans the whole buffer, a direct one this tile's rows
-    const i32x4_t ra = buffer_at(GATHER ? sg.A : sg.A + row0 * sg.lda,
-                                 (uint32_t)((GATHER ? p.a_rows : rows) * sg.lda * 2));
-    const i32x4_t rb = buffer_at(sg.B + (int64_t)expert * sg.b_expert_stride,
-                                 (uint32_t)sg.kdim * (uint32_t)p.ncols * 2u);
-    const int nk = (sg.kdim + TK - 1) / TK;
-    uint32_t a_off[4];
+    ra = buffer_at(GATHER ? sg.A : sg.A + row0 * sg.lda,
+                   (uint32_t)((GATHER ? p.a_rows : rows) * sg.lda * 2));
+    rb = buffer_at(sg.B + (int64_t)expert * sg.b_expert_stride,
+                   (uint32_t)sg.kdim * (uint32_t)p.ncols * 2u);
+    kdim = sg.kdim;
+    nk = (kdim + TK - 1) / TK;
+    ks = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       a_off[i] = a_row[i] != 0xFFFFFFFFu
                      ? a_row[i] * (uint32_t)(sg.lda * 2) + (uint32_t)a_chunk * 16u : kNoAddr;
-    const uint32_t b_base = (uint32_t)(n0 + 8 * b_chunk) * 2u;
-    const uint32_t b_pitch = (uint32_t)p.ncols * 2u;
-    auto issue = [&](int ks, int slot) {
-      char* s = lds + slot * kSlotBytes;
-      const int k0 = ks * TK;
-      const bool ka = k0 + 8 * a_chunk < sg.kdim;  // kdim % 8 == 0: whole chunks
+  };
+  int total = 0;
+  for (int i = 0; i < p.n_seg; ++i) total += (p.seg[i].kdim + TK - 1) / TK;
+  auto issue = [&](int s) {  // past the last stage: zeros
+    if (ks == nk && seg + 1 < p.n_seg) next_segment();
+    const int k0 = ks * TK;
+    const int left = kdim - k0;  // <= 0 past the end
+    ++ks;
+    const int at = (s & 1) * kSlotBytes + wave * 1024;
+    const bool ka = 8 * a_chunk < left;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dma(ra, ka ? a_off[i] + (uint32_t)k0 * 2u : kNoAddr, s + (8 * i + wave) * 1024);
+    for (int i = 0; i < 4; ++i)
+      dma(ra, ka ? a_off[i] + (uint32_t)k0 * 2u : kNoAddr, at + 8 * i * 1024);
+    const uint32_t b0 = (uint32_t)k0 * b_pitch + b_lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = k0 + 16 * i + b_k;
-        dma(rb, b_col && k < sg.kdim ? b_base + (uint32_t)k * b_pitch : kNoAddr,
-            s + kOpBytes + (8 * i + wave) * 1024);
-      }
+    for (int i = 0; i < 4; ++i)
+      dma(rb, b_col && 16 * i + b_k < left ? b0 + (uint32_t)(16 * i) * b_pitch : kNoAddr,
+          at + kOpBytes + 8 * i * 1024);
+  };
+
+  floatx16_t acc[4][2];
+  clear_acc(acc);
+  const KRows kb(lane);
+  const int b_off[2] = {kOpBytes + kb.block_off(2 * wp), kOpBytes + kb.block_off(2 * wp + 1)};
+  const int a_base = (wg * 128 + (lane & 31)) * 128;
+  int live_m = (rows - wg * 128 + 31) / 32;
+  live_m = __builtin_amdgcn_readfirstlane(live_m < 0 ? 0 : live_m > 4 ? 4 : live_m);
+  const bool live = __builtin_amdgcn_readfirstlane(live_m > 0 && n0 + wp * 64 < p.ncols);
+
+  // Fragments of a k-step are read during the MFMAs of the one before it.  In
+  // the last k-step of a stage the barrier that makes the next stage visible
+  // frees this one's slot for the stage after it, whose loads follow.
+  auto run = [&](auto live_tag) {
+    constexpr int LIVE = decltype(live_tag)::value;
+    auto read = [&](Fragments<LIVE>& f, int s, int k) {
+      const int slot = (s & 1) * kSlotBytes;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f.B[i] = read_tr(slot + b_off[i] + k * (16 * 512));
+      const int a_at = slot + a_base + ((2 * k + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
+#pragma unroll
+      for (int m = 0; m < LIVE; ++m) f.A[m] = lds_read<bf16x8_t>(a_at + m * (32 * 128));
     };
-    // the slot is free: the barrier that opened the stage before this one (the
-    // last segment's last) is behind every wave's reads of it
-    issue(0, parity);
-    for (int ks = 0; ks < nk; ++ks) {
-      wait_vmcnt<0>();
-      stage_barrier();
-      const int cur = parity;
-      parity ^= 1;
-      if (ks + 1 < nk) issue(ks + 1, parity);
-      const char* slot = lds + cur * kSlotBytes;
-      if (live) {
-        if (live_m > 2) multiply_stage<false, 4>(slot, fr, acc);
-        else multiply_stage<false, 2>(slot, fr, acc);
+    next_segment();
+    issue(0);
+    issue(1);
+    wait_vmcnt<8>();
+    stage_barrier();
+    Fragments<LIVE> f0, f1;
+    if (LIVE > 0) read(f0, 0, 0);
+    for (int s = 0; s < total; ++s) {
+      if (LIVE > 0) {
+        read(f1, s, 1);
+        multiply<false>(f0, acc);
+        read(f0, s, 2);
+        multiply<false>(f1, acc);
+        read(f1, s, 3);
+        multiply<false>(f0, acc);
       }
+      wait_vmcnt<0>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      stage_barrier();
+      if (LIVE > 0) read(f0, s + 1, 0);  // past the last stage: zeros, not used
+      issue(s + 2);
+      if (LIVE > 0) multiply<false>(f1, acc);
     }
-  }
+    wait_vmcnt<0>();  // nothing may still write the LDS when it is used again
+  };
+  if (!live) run(std::integral_constant<int, 0>{});
+  else if (live_m > 2) run(std::integral_constant<int, 4>{});
+  else run(std::integral_constant<int, 2>{});
 
   if constexpr (F32) {
     float* out = reinterpret_cast<float*>(p.out);
@@ -332,14 +376,47 @@ __global__ __launch_bounds__(512, 2) void rows_kernel(RowsProblem token, RowsPro
 }
 
 // ---------------------------------------------------------------- weights
+// The upper 32 lanes' a change places with the lower lanes' b; the odd rows'
+// (of 16 lanes) a with the even rows' b.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+// Within every 16 lanes, the upper eight's a change places with the lower
+// eight's b.
+__device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b, bool upper) {
+  const uint32_t give = upper ? a : b;
+  const uint32_t got = dpp_u32<0x128>(give);  // row_ror:8
+  a = upper ? got : a;
+  b = upper ? b : got;
+}
+
+// Tiles mt0 .. mt0 + T - 1 of column tile nt.  Stage s of the stream is k-block
+// s % nk of tile s / nk, two k-steps of 16.  Every stage opens with a wait and
+// a barrier after which stage s + 1 is in LDS for all waves; the fragments of
+// a k-step are read during the MFMAs of the one before it, across stages and
+// tiles.  In the middle of stage s every wave issues one batch: the gathered
+// rows of stage s + 6 (4-byte LDS-DMA, the same bytes from every wave) and the
+// four operand loads of stage s + 3, whose rows came with batch s - 3; past
+// the last stage the loads give zeros, so that every batch has as many.  The
+// opening wait lets batch s - 1 stay in flight, and in a tile's first two
+// stages the sixteen stores of the tile before: behind batch s - 2 in the
+// order that vmcnt counts.  The stages have no branches on data, so the
+// compiler's own waits for the fragments stay exact.
 enum Gathered { kNeither, kA, kB };
 template <Gathered GATHER>
-__device__ __forceinline__ void weights_tile(const WeightsProblem& p, int expert, int tile,
-                                             char* lds) {
-  const int m0 = (tile / p.tiles_n) * TM;
-  const int n0 = (tile % p.tiles_n) * TN;
+__device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int expert, int mt0, int T,
+                                              int nt, char* lds) {
+  const int n0 = nt * TN;
   int64_t first, rows;
-  if (p.offsets) {
+  if constexpr (GATHER != kNeither) {
     first = p.offsets[expert];
     rows = (int64_t)p.offsets[expert + 1] - first;
   } else {
@@ -348,95 +425,223 @@ __device__ __forceinline__ void weights_tile(const WeightsProblem& p, int expert
   }
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wg = wave >> 2, wp = wave & 3;
-  const int kr = 2 * wave + (lane >> 5);  // k-row of load i: 16 i + kr
+  const int wg = wave >> 2, wp = wave & 3;  // rows 128 wg .., columns 64 wp ..
+  // LDS-DMA: load i of a wave covers k-rows 2 (8 i + wave) .. + 1 of either
+  // operand (lane -> row + (l >> 5), slot l & 31), i < 2.
+  const int kr = 2 * wave + (lane >> 5);
   const int chunk = (lane & 31) ^ (4 * (kr & 3));
-  const bool a_in = m0 + 8 * chunk < p.a_cols, b_in = n0 + 8 * chunk < p.b_cols;
-  const uint32_t a_col = (uint32_t)(m0 + 8 * chunk) * 2u, b_col = (uint32_t)(n0 + 8 * chunk) * 2u;
-  uint32_t* ids = reinterpret_cast<uint32_t*>(lds + kIdsOff);
+  const bool b_in = n0 + 8 * chunk < p.b_cols;
+  const uint32_t b_col = (uint32_t)(n0 + 8 * chunk) * 2u;
   const uint32_t a_pitch = (uint32_t)p.lda * 2u, b_pitch = (uint32_t)p.ldb * 2u;
-  const uint32_t g_pitch = GATHER == kA ? a_pitch : b_pitch;
+  const int nk = (int)((rows + WK - 1) / WK);
+  const int total = T * nk;
+  const bool live = __builtin_amdgcn_readfirstlane(n0 + wp * 64 < p.b_cols);
+
+  const i32x4_t r_ids = buffer_at(p.tok + first, (uint32_t)min(rows * 4, (int64_t)0x7FFFFFFF));
+  const i32x4_t r_gather = GATHER == kA ? buffer_at(p.A, (uint32_t)(p.tok_rows * p.lda * 2))
+                                        : buffer_at(p.B, (uint32_t)(p.tok_rows * p.ldb * 2));
+  auto issue_ids = [&](int ks, int s) {
+    if constexpr (GATHER != kNeither)
+      dma4(r_ids, (uint32_t)(ks * WK + lane) * 4u, kIdsOff + s % kIdsSlots * kIdsSlot);
+  };
+  auto issue = [&](int mt, int ks, int s, bool any) {
+    const int at0 = (s % kWSlots) * kWSlot + wave * 1024;
+    const int64_t r0 = first + (int64_t)ks * WK;
+    // rows of this stage
+    const int left = any ? (int)min((int64_t)WK, rows - (int64_t)ks * WK) : 0;
+    const int m0 = mt * WM;
+    const bool a_in = m0 + 8 * chunk < p.a_cols;
+    const uint32_t a_col = (uint32_t)(m0 + 8 * chunk) * 2u;
+    uint32_t at[2];
+    if constexpr (GATHER != kNeither) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        at[i] = lds_read<uint32_t>(kIdsOff + s % kIdsSlots * kIdsSlot + (16 * i + kr) * 4);
+    }
+    const i32x4_t ra =
+        GATHER == kA ? r_gather : buffer_at(p.A + r0 * p.lda, (uint32_t)left * a_pitch);
+    const i32x4_t rb =
+        GATHER == kB ? r_gather : buffer_at(p.B + r0 * p.ldb, (uint32_t)left * b_pitch);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * i + kr;
+      const uint32_t oa = (GATHER == kA ? at[i] : (uint32_t)r) * a_pitch + a_col;
+      const uint32_t ob = (GATHER == kB ? at[i] : (uint32_t)r) * b_pitch + b_col;
+      dma(ra, r < left && a_in ? oa : kNoAddr, at0 + 8 * i * 1024);
+      dma(rb, r < left && b_in ? ob : kNoAddr, at0 + kWaBytes + 8 * i * 1024);
+    }
+  };
 
   floatx16_t acc[4][2];
-  clear_acc(acc);
-  const Frags<true> fr(lane, wg, wp);
-  const bool live =
-      __builtin_amdgcn_readfirstlane(m0 + wg * 128 < p.a_cols && n0 + wp * 64 < p.b_cols);
-  for (int64_t c0 = 0; c0 < rows; c0 += kIdsMax) {
-    const int cr = (int)min((int64_t)kIdsMax, rows - c0);
-    const int nk = (cr + TK - 1) / TK;
-    if (c0 > 0) stage_barrier();  // the chunk before is read to its end
-    if constexpr (GATHER != kNeither) {
-      for (int r = tid; r < nk * TK; r += 512)
-        ids[r] = r < cr ? (uint32_t)(p.src[first + c0 + r] / p.src_div) * g_pitch : kNoAddr;
-      __syncthreads();
+  const KRows cols(lane);
+  int a_off[4], b_off[2];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) a_off[m] = cols.block_off(4 * wg + m);
+#pragma unroll
+  for (int f = 0; f < 2; ++f) b_off[f] = cols.block_off(2 * wp + f);
+  auto read = [&](Fragments<4>& f, int s, int k) {  // k-step k of stage s
+    const int slot = (s % kWSlots) * kWSlot + k * (16 * 512);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f.B[i] = read_tr(slot + kWaBytes + b_off[i]);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) f.A[m] = read_tr(slot + a_off[m]);
+  };
+  // The wave's part of a tile, sixteen stores of 8 rows x 128 bytes: a lane's
+  // four columns of two register groups are joined with the other half's to
+  // eight (16 bytes), then rows trade places between lanes until eight lanes
+  // hold the 64 columns of one row, a whole cache line.  Always sixteen: rows
+  // and columns past the result fall outside the buffer.
+  const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out + (int64_t)expert * p.out_stride,
+                                              (uint32_t)p.a_cols * (uint32_t)p.b_cols * 2u);
+  auto store = [&](int mt) {
+    const bool upper = (lane & 8) != 0;
+    // lane -> row l & 7, columns 32 ((l >> 3) & 1) + 16 ((l >> 4) & 1) + 8 (l >> 5)
+    const int row0 = mt * WM + 128 * wg + (lane & 7);
+    const int col = n0 + wp * 64 + 32 * ((lane >> 3) & 1) + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      uint32_t v[2][2][4];  // [f][register groups 2 u and 2 u + 1]
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            v[f][u][j] = pack_bf16(acc[m][f][8 * u + 2 * j], acc[m][f][8 * u + 2 * j + 1]);
+            v[f][u][2 + j] = pack_bf16(acc[m][f][8 * u + 4 + 2 * j], acc[m][f][8 * u + 5 + 2 * j]);
+            swap_halves(v[f][u][j], v[f][u][2 + j]);
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) swap_rows16(v[f][0][j], v[f][1][j]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) swap_rows8(v[0][u][j], v[1][u][j], upper);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int r = row0 + 32 * m + 16 * u + 8 * f;
+          const uint32_t at = r < p.a_cols && col < p.b_cols
+                                  ? ((uint32_t)r * (uint32_t)p.b_cols + (uint32_t)col) * 2u : kNoAddr;
+          const i32x4_t out = {(int)v[f][u][0], (int)v[f][u][1], (int)v[f][u][2], (int)v[f][u][3]};
+          __builtin_amdgcn_raw_buffer_store_b128(out, ro, (int)at, 0, 0);
+        }
+      }
     }
-    // direct operands: this chunk's rows; gathered ones: the whole buffer
-    const int64_t base = first + c0;
-    const i32x4_t ra = buffer_at(GATHER == kA ? p.A : p.A + base * p.lda,
-                                 (uint32_t)((GATHER == kA ? p.src_rows : cr) * p.lda * 2));
-    const i32x4_t rb = buffer_at(GATHER == kB ? p.B : p.B + base * p.ldb,
-                                 (uint32_t)((GATHER == kB ? p.src_rows : cr) * p.ldb * 2));
-    auto issue = [&](int ks, int slot) {
-      char* s = lds + slot * kSlotBytes;
-      uint32_t at[4];
-      if constexpr (GATHER != kNeither) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = ids[ks * TK + 16 * i + kr];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ks * TK + 16 * i + kr;
-        const bool in = r < cr;
-        const uint32_t ga = GATHER == kA ? at[i] : (uint32_t)r * a_pitch;
-        const uint32_t gb = GATHER == kB ? at[i] : (uint32_t)r * b_pitch;
-        dma(ra, in && a_in ? ga + a_col : kNoAddr, s + (8 * i + wave) * 1024);
-        dma(rb, in && b_in ? gb + b_col : kNoAddr, s + kOpBytes + (8 * i + wave) * 1024);
-      }
+  };
+
+  if (rows == 0) {  // an expert without rows: zeros
+    clear_acc(acc);
+    if (live)
+      for (int t = 0; t < T; ++t) store(mt0 + t);
+    return;
+  }
+  // (tile, k-block) of the next batch's two parts
+  int di = 0, dk = 0;  // operand loads
+  int ik = 0;          // gathered rows
+  auto next_ids = [&](int s) {
+    issue_ids(ik, s);
+    ik = ik + 1 == nk ? 0 : ik + 1;
+  };
+  auto next_data = [&](int s) {
+    issue(mt0 + di, dk, s, s < total);
+    const bool wrap = dk + 1 == nk;
+    di += wrap ? 1 : 0;
+    dk = wrap ? 0 : dk + 1;
+  };
+  if constexpr (GATHER != kNeither) {
+    for (int s = 0; s < 3; ++s) next_ids(s);
+    wait_vmcnt<0>();
+    stage_barrier();
+  }
+  // batches -3, -2 and -1
+  for (int s = 0; s < 3; ++s) {
+    next_ids(3 + s);
+    next_data(s);
+  }
+  constexpr int kBatch = GATHER != kNeither ? 5 : 4;
+  wait_vmcnt<2 * kBatch>();
+  stage_barrier();  // stage 0
+  Fragments<4> f0, f1;
+  read(f0, 0, 0);
+  int s = 0;
+  bool stored = false;  // this wave, the tile before
+  for (int t = 0; t < T; ++t) {
+    const bool mine = live && (mt0 + t) * WM + wg * 128 < p.a_cols;
+    auto open = [&](bool behind_stores) {
+      if (behind_stores) wait_vmcnt<kBatch + 16>();
+      else wait_vmcnt<kBatch>();
+      stage_barrier();  // and every wave has left stage s - 1, whose slot is s + 3's
     };
-    issue(0, 0);
-    for (int ks = 0; ks < nk; ++ks) {
-      wait_vmcnt<0>();
-      stage_barrier();
-      if (ks + 1 < nk) issue(ks + 1, (ks + 1) & 1);
-      if (live) multiply_stage<true, 4>(lds + (ks & 1) * kSlotBytes, fr, acc);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    auto batch = [&] {
+      next_ids(s + 6);
+      next_data(s + 3);
+    };
+    if (mine) {
+      auto stage = [&](auto first_tag, bool behind_stores) {
+        open(behind_stores);
+        read(f1, s, 1);
+        multiply<decltype(first_tag)::value>(f0, acc);
+        batch();
+        read(f0, s + 1, 0);  // past the last stage: zeros, not used
+        multiply<false>(f1, acc);
+        ++s;
+      };
+      stage(std::true_type{}, stored);
+      if (nk > 1) stage(std::false_type{}, stored);
+      for (int k = 2; k < nk; ++k) stage(std::false_type{}, false);
+      store(mt0 + t);
+      stored = true;
+    } else {
+      // no rows or columns of this tile: only its share of the loads
+      for (int k = 0; k < nk; ++k) {
+        open(stored && k < 2);
+        batch();
+        ++s;
+      }
+      stored = false;
+      read(f0, s, 0);
     }
   }
-  const int64_t eo = (int64_t)expert * p.out_stride;
-  store_bf16_tile(acc, lane, wg, wp, tid, lds, p.b_cols - n0, [&](int r) -> uint16_t* {
-    const int m = m0 + r;
-    if (m >= p.a_cols || (!p.out1 && m >= p.split)) return nullptr;
-    return (m < p.split ? p.out0 + eo + (int64_t)m * p.b_cols
-                        : p.out1 + eo + (int64_t)(m - p.split) * p.b_cols) + n0;
-  });
+  wait_vmcnt<0>();  // nothing may still write the LDS when it is used again
 }
 
 // Items: the dense problems' tiles first (their sums run over all tokens),
-// then per expert the tiles of its gate/up and of its down gradient, which
-// share the expert's rows.
+// then per expert the tiles of its three gradients, which share its rows.
 __global__ __launch_bounds__(512, 2) void weights_kernel(WeightsLaunch w) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int64_t b = blockIdx.x;
   for (int i = 0; i < w.n_dense; ++i) {
     const int t = w.dense[i].tiles_m * w.dense[i].tiles_n;
     if (b < t) {
-      weights_tile<kNeither>(w.dense[i], 0, (int)b, lds);
+      weights_tiles<kNeither>(w.dense[i], 0, (int)b / w.dense[i].tiles_n, 1,
+                              (int)b % w.dense[i].tiles_n, lds);
       return;
     }
     b -= t;
   }
-  const int t0 = w.expert[0].tiles_m * w.expert[0].tiles_n;
-  const int t1 = w.expert[1].tiles_m * w.expert[1].tiles_n;
-  const int64_t work = (int64_t)w.E * (t0 + t1);
+  const int64_t work = (int64_t)w.E * w.expert_items;
   const int64_t share = (work + kXcds - 1) / kXcds;
   if (b / kXcds >= share) return;
   const int64_t item = xcd_item(b, share);
   if (item >= work) return;
-  const int e = (int)(item / (t0 + t1));
-  const int r = (int)(item % (t0 + t1));
-  if (r < t0) weights_tile<kB>(w.expert[0], e, r, lds);
-  else weights_tile<kA>(w.expert[1], e, r - t0, lds);
+  const int e = (int)(item / w.expert_items);
+  int r = (int)(item % w.expert_items);
+  // gate and up have the same tiles
+  const WeightsProblem& gu = w.expert[0];
+  const int groups = (gu.tiles_m + kWGroup - 1) / kWGroup;
+  const int one = groups * gu.tiles_n;
+  if (r < 2 * one) {
+    const int i = r >= one ? 1 : 0;
+    r -= i * one;
+    const int m = r / gu.tiles_n * kWGroup;
+    weights_tiles<kB>(w.expert[i], e, m, min(kWGroup, gu.tiles_m - m), r % gu.tiles_n, lds);
+  } else {
+    r -= 2 * one;
+    const WeightsProblem& dn = w.expert[2];
+    const int m = r / dn.tiles_n * kWGroup;
+    weights_tiles<kA>(dn, e, m, min(kWGroup, dn.tiles_m - m), r % dn.tiles_n, lds);
+  }
 }
 
 // ---------------------------------------------------------------- small kernels
@@ -454,11 +659,16 @@ __global__ __launch_bounds__(256) void pairs_kernel(const int32_t* __restrict__ 
   S[p] = in ? sigmoid_weight(Z[p / K * E + e]) : 0.0f;
 }
 
-// m-tiles of bm rows from the segment offsets: one block; thread e counts its
-// expert's tiles, a scan places them.
-__global__ __launch_bounds__(512) void row_tiles_kernel(const int32_t* __restrict__ offsets, int E,
-                                                        int32_t* __restrict__ tiles,
-                                                        int32_t* __restrict__ n_tiles) {
+// Of the grouped pairs: every row's token; block 0 also makes the m-tiles of
+// rows_kernel from the segment offsets (thread e counts its expert's tiles, a
+// scan places them).
+__global__ __launch_bounds__(512) void grouped_rows_kernel(
+    const int32_t* __restrict__ sorted_src, int64_t pairs, int K,
+    const int32_t* __restrict__ offsets, int E, int32_t* __restrict__ tok,
+    int32_t* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
+  const int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x;
+  if (i < pairs) tok[i] = sorted_src[i] / K;
+  if (blockIdx.x != 0) return;
   __shared__ uint32_t wsum[8];
   const int e = threadIdx.x, w = e >> 6;
   const int32_t off = e < E ? offsets[e] : 0;
@@ -468,7 +678,7 @@ __global__ __launch_bounds__(512) void row_tiles_kernel(const int32_t* __restric
   if (lane_id() == 63) wsum[w] = inc;
   __syncthreads();
   uint32_t base = 0;
-  for (int i = 0; i < w; ++i) base += wsum[i];
+  for (int j = 0; j < w; ++j) base += wsum[j];
   uint32_t t = base + inc - nt;
   for (int32_t r = 0; r < cnt; r += TM)
     reinterpret_cast<int4*>(tiles)[t++] = make_int4(e, off + r, min(TM, cnt - r), r);
@@ -565,9 +775,11 @@ hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E
   return hipGetLastError();
 }
 
-hipError_t launch_row_tiles(const int32_t* offsets, int E, int32_t* tiles, int32_t* n_tiles,
-                            hipStream_t stream) {
-  hipLaunchKernelGGL(row_tiles_kernel, dim3(1), dim3(512), 0, stream, offsets, E, tiles, n_tiles);
+hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K,
+                               const int32_t* offsets, int E, int32_t* tok, int32_t* tiles,
+                               int32_t* n_tiles, hipStream_t stream) {
+  hipLaunchKernelGGL(grouped_rows_kernel, dim3((unsigned)((pairs + 511) / 512)), dim3(512), 0,
+                     stream, sorted_src, pairs, K, offsets, E, tok, tiles, n_tiles);
   return hipGetLastError();
 }
 
@@ -582,9 +794,9 @@ template <bool F32>
 static hipError_t start_rows(const RowsProblem& t, const RowsProblem& r, int64_t token_blocks,
                              int64_t blocks, hipStream_t stream) {
   static std::atomic<uint32_t> configured{0};
-  const hipError_t e = set_lds_limit_once((const void*)rows_kernel<F32>, kLdsBytes, configured);
+  const hipError_t e = set_lds_limit_once((const void*)rows_kernel<F32>, kRowsLds, configured);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rows_kernel<F32>, dim3((unsigned)blocks), dim3(512), kLdsBytes, stream, t, r,
+  hipLaunchKernelGGL(rows_kernel<F32>, dim3((unsigned)blocks), dim3(512), kRowsLds, stream, t, r,
                      token_blocks);
   return hipGetLastError();
 }
@@ -604,23 +816,25 @@ hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool o
 
 hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
   static std::atomic<uint32_t> configured{0};
-  hipError_t e = set_lds_limit_once((const void*)weights_kernel, kLdsBytes, configured);
+  hipError_t e = set_lds_limit_once((const void*)weights_kernel, kWeightsLds, configured);
   if (e != hipSuccess) return e;
   int64_t blocks = 0;
+  auto set_tiles = [](WeightsProblem& q) {
+    q.tiles_m = (q.a_cols + WM - 1) / WM;
+    q.tiles_n = (q.b_cols + TN - 1) / TN;
+  };
   for (int i = 0; i < w.n_dense; ++i) {
-    w.dense[i].tiles_m = (w.dense[i].a_cols + TM - 1) / TM;
-    w.dense[i].tiles_n = (w.dense[i].b_cols + TN - 1) / TN;
+    set_tiles(w.dense[i]);
     blocks += (int64_t)w.dense[i].tiles_m * w.dense[i].tiles_n;
   }
-  int64_t per = 0;
-  for (int i = 0; i < 2; ++i) {
-    w.expert[i].tiles_m = (w.expert[i].a_cols + TM - 1) / TM;
-    w.expert[i].tiles_n = (w.expert[i].b_cols + TN - 1) / TN;
-    per += (int64_t)w.expert[i].tiles_m * w.expert[i].tiles_n;
+  w.expert_items = 0;
+  for (WeightsProblem& q : w.expert) {
+    set_tiles(q);
+    w.expert_items += (q.tiles_m + kWGroup - 1) / kWGroup * q.tiles_n;
   }
-  blocks += (w.E * per + kXcds - 1) / kXcds * kXcds;
+  blocks += ((int64_t)w.E * w.expert_items + kXcds - 1) / kXcds * kXcds;
   if (blocks > 0x7FFFFFF0LL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(weights_kernel, dim3((unsigned)blocks), dim3(512), kLdsBytes, stream, w);
+  hipLaunchKernelGGL(weights_kernel, dim3((unsigned)blocks), dim3(512), kWeightsLds, stream, w);
   return hipGetLastError();
 }
 
