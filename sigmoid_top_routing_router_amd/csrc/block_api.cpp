@@ -104,8 +104,8 @@ moe::BalanceWork carve_balance(void* ws, int64_t N, int32_t E, int32_t n_seg, si
 
 // ---- layer backward
 struct GradLayout {
-  int32_t *ids, *counts, *offsets, *sorted_src, *src_pos, *tiles, *n_tiles, *row_tiles, *n_row_tiles,
-      *tok;
+  int32_t *ids, *counts, *offsets, *sorted_src, *src_pos, *tiles, *n_tiles, *row_tiles, *n_row_tiles;
+  uint32_t* tok;
   uint32_t* block_counts;
   float *S, *Q, *Qs, *dscore;
   uint16_t *hid, *dXp, *hids, *dzb, *base;
@@ -141,7 +141,7 @@ GradLayout carve_grad(void* ws, const moe_problem_t& p) {
   l.max_row_tiles = moe::perm_max_tiles((int64_t)pairs, p.E, moe::grad_tile_rows());
   l.row_tiles = (int32_t*)take((size_t)l.max_row_tiles * 16);
   l.n_row_tiles = (int32_t*)take(16);
-  l.tok = (int32_t*)take(pairs * 4);
+  l.tok = (uint32_t*)take(pairs * 4);
   // Q is read for the last time before the pairs' part of grad_x is written
   void* q = take(pairs * (size_t)(p.h * 4 > p.d * 2 ? p.h * 4 : p.d * 2));
   l.Q = (float*)q;
@@ -196,8 +196,8 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   pw.n_tiles = l.n_tiles;
   MOE_TRY(moe::launch_permute(l.ids, N, E, K, moe::gemm_bm(), moe::gemm_xrows(), pw, st),
           "grouping");
-  MOE_TRY(moe::launch_grouped_rows(l.sorted_src, pairs, K, l.offsets, E, l.tok, l.row_tiles,
-                                   l.n_row_tiles, st),
+  MOE_TRY(moe::launch_grouped_rows(l.sorted_src, pairs, K, (uint32_t)d * 2u, l.offsets, E, l.tok,
+                                   l.row_tiles, l.n_row_tiles, st),
           "grouped rows");
 
   auto pair_rows = [&] {

@@ -226,8 +226,8 @@ hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int3
 constexpr uint32_t kGradMaxOperandBytes = 0xFFFE0000u;
 // C[row, n] = sum over the segments of sum_k A[row, k] B[k, n].  Pairs: rows
 // from the tile table (expert, first row, rows, offset); with an fp32 result
-// A's rows are gathered (row -> gather[row] of a_rows).  Tokens: rows 0 ..
-// rows_dense - 1.
+// A's rows are gathered (gather[row]: byte offset; a_rows rows in all).
+// Tokens: rows 0 .. rows_dense - 1.
 struct RowsSegment {
   const uint16_t* A;
   int64_t lda;             // elements
@@ -238,7 +238,7 @@ struct RowsSegment {
 struct RowsProblem {
   RowsSegment seg[3];
   int n_seg;
-  const int32_t* gather;
+  const uint32_t* gather;
   int64_t a_rows;
   const int32_t* tiles;
   const int32_t* n_tiles;
@@ -254,7 +254,7 @@ hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool o
                        hipStream_t stream);
 // C[m, n] = sum_row A[row, m] B[row, n] in bf16, rows offsets[e] ..
 // offsets[e + 1] - 1 (dense: all rows_dense).  The expert problems are gate,
-// up (rows of B, x, through tok[row], of tok_rows rows) and down (A, dy).
+// up (rows of B, x, at byte offset tok[row], of tok_rows rows) and down (A, dy).
 struct WeightsProblem {
   const uint16_t* A;
   int64_t lda;
@@ -264,7 +264,7 @@ struct WeightsProblem {
   int b_cols;
   const int32_t* offsets;
   int64_t rows_dense;
-  const int32_t* tok;
+  const uint32_t* tok;
   int64_t tok_rows;
   uint16_t* out;
   int64_t out_stride;      // elements between experts
@@ -275,13 +275,12 @@ struct WeightsLaunch {
   int n_dense;
   WeightsProblem expert[3];
   int E;
-  int expert_items;        // set by the launcher
 };
 hipError_t launch_weights(WeightsLaunch w, hipStream_t stream);
 hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E, int K,
                         int32_t* ids_out, float* S, hipStream_t stream);
-hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K,
-                               const int32_t* offsets, int E, int32_t* tok, int32_t* tiles,
+hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K, uint32_t pitch,
+                               const int32_t* offsets, int E, uint32_t* tok, int32_t* tiles,
                                int32_t* n_tiles, hipStream_t stream);
 hipError_t launch_logits_grad(const float* Z, const int32_t* ids, const int32_t* src_pos,
                               const float* dscore_part, int parts, int64_t N, int E, int K,

@@ -51,16 +51,16 @@ constexpr int kOpBytes = 32 * 1024;            // one operand of one stage
 constexpr int kSlotBytes = 2 * kOpBytes;
 constexpr int kRowsLds = 2 * kSlotBytes + 8 * 1024;  // and the staged result
 // weights_kernel
-constexpr int WM = 256, WK = 32;
+constexpr int WM = 128, WK = 32;
 constexpr int kWaBytes = WK * WM * 2;          // A of one stage, then B
 constexpr int kWSlot = kWaBytes + WK * TN * 2;
-constexpr int kWSlots = 4;
+constexpr int kWSlots = 3;
 constexpr int kIdsOff = kWSlots * kWSlot;      // gathered rows of eight stages
 constexpr int kIdsSlot = 64 * 4;               // a wave loads 64, the first 32 are used
 constexpr int kIdsSlots = 8;
 constexpr int kWeightsLds = kIdsOff + kIdsSlots * kIdsSlot;
-constexpr int kWGroup = 4;                     // tiles of a block
-static_assert(kWeightsLds <= 160 * 1024, "LDS");
+constexpr int kWGroup = 2;                     // tiles of a block
+static_assert(2 * kWeightsLds <= 160 * 1024, "two blocks share a CU");
 constexpr int kXcds = 8;
 // An offset past the end of any operand: the load returns zeros.  Operands
 // are smaller than this (checked by the entry point).
@@ -106,6 +106,23 @@ __device__ __forceinline__ void dma4(i32x4_t r, uint32_t off, int at) {
                :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(r) : "memory");
 #endif
 }
+// One stage of weights_kernel for a wave: two loads of A and four of B, each
+// 1 KB after the other in LDS.
+__device__ __forceinline__ void dma_2_4(i32x4_t ra, const uint32_t (&a)[2], int a_at, i32x4_t rb,
+                                        const uint32_t (&b)[4], int b_at) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %8, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %8, 0 offen lds\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %9, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %9, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %6, %9, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %7, %9, 0 offen lds"
+      :: "s"(__builtin_amdgcn_readfirstlane(a_at)), "s"(__builtin_amdgcn_readfirstlane(b_at)),
+         "v"(a[0]), "v"(a[1]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "s"(ra), "s"(rb)
+      : "memory", "scc");
+#endif
+}
 template <class T>
 __device__ __forceinline__ T lds_read(int at) {
   return *(const __attribute__((address_space(3))) T*)(uint32_t)at;
@@ -117,23 +134,26 @@ __device__ __forceinline__ int64_t xcd_item(int64_t block, int64_t share) {
   return (block % kXcds) * share + block / kXcds;
 }
 
-// Eight k of one column from a [k][256] stage: two transposing reads.
+// Eight k of one column from a stage of PITCH bytes a k-row: two transposing
+// reads.
+template <int PITCH>
 __device__ __forceinline__ bf16x8_t read_tr(int at) {
   const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uint32_t)at);
-  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uint32_t)(at + 4 * 512));
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uint32_t)(at + 4 * PITCH));
   typedef short s16x8_t __attribute__((ext_vector_type(8)));
   const s16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// What a lane reads of a [k][256] operand for the 32 columns of block blk:
-// block_off(blk) + 512 k of the k-step's first row.
+// What a lane reads of a [k][PITCH / 2] operand for the 32 columns of block
+// blk: block_off(blk) + PITCH k of the k-step's first row.
+template <int PITCH>
 struct KRows {
   int kq, row, sub;
   __device__ __forceinline__ explicit KRows(int lane) {
     const int i = lane & 15;
     kq = i >> 2;
-    row = (8 * (lane >> 5) + kq) * 512;
+    row = (8 * (lane >> 5) + kq) * PITCH;
     sub = (2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) * 16 + (i & 1) * 8;
   }
   __device__ __forceinline__ int block_off(int blk) const {
@@ -200,6 +220,11 @@ __device__ __forceinline__ void clear_acc(floatx16_t (&acc)[4][2]) {
       for (int r = 0; r < 16; ++r) acc[m][f][r] = 0.0f;
 }
 
+// Blocks of a share of the grid that deals `work` items to the XCDs.
+__host__ __device__ __forceinline__ int64_t xcd_blocks(int64_t work) {
+  return (work + kXcds - 1) / kXcds * kXcds;
+}
+
 // ---------------------------------------------------------------- rows
 // PAIR: rows of the tile table, else tokens.  F32: the fp32 result (Q), whose
 // pairs gather their rows of A; else bf16 (parts of dx).
@@ -237,7 +262,7 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * (8 * i + wave) + (lane >> 3);
-    a_row[i] = r >= rows ? 0xFFFFFFFFu : GATHER ? (uint32_t)p.gather[row0 + r] : (uint32_t)r;
+    a_row[i] = r >= rows ? 0xFFFFFFFFu : GATHER ? p.gather[row0 + r] : (uint32_t)r;
   }
   // The segments' stages as one stream; this is the next one to load.
   i32x4_t ra, rb;
@@ -257,7 +282,8 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       a_off[i] = a_row[i] != 0xFFFFFFFFu
-                     ? a_row[i] * (uint32_t)(sg.lda * 2) + (uint32_t)a_chunk * 16u : kNoAddr;
+                     ? a_row[i] * (GATHER ? 1u : (uint32_t)(sg.lda * 2)) + (uint32_t)a_chunk * 16u
+                     : kNoAddr;
   };
   int total = 0;
   for (int i = 0; i < p.n_seg; ++i) total += (p.seg[i].kdim + TK - 1) / TK;
@@ -280,7 +306,7 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
 
   floatx16_t acc[4][2];
   clear_acc(acc);
-  const KRows kb(lane);
+  const KRows<512> kb(lane);
   const int b_off[2] = {kOpBytes + kb.block_off(2 * wp), kOpBytes + kb.block_off(2 * wp + 1)};
   const int a_base = (wg * 128 + (lane & 31)) * 128;
   int live_m = (rows - wg * 128 + 31) / 32;
@@ -295,7 +321,7 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
     auto read = [&](Fragments<LIVE>& f, int s, int k) {
       const int slot = (s & 1) * kSlotBytes;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) f.B[i] = read_tr(slot + b_off[i] + k * (16 * 512));
+      for (int i = 0; i < 2; ++i) f.B[i] = read_tr<512>(slot + b_off[i] + k * (16 * 512));
       const int a_at = slot + a_base + ((2 * k + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
 #pragma unroll
       for (int m = 0; m < LIVE; ++m) f.A[m] = lds_read<bf16x8_t>(a_at + m * (32 * 128));
@@ -391,25 +417,29 @@ __device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
 
 // Within every 16 lanes, the upper eight's a change places with the lower
 // eight's b.
-__device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b, bool upper) {
-  const uint32_t give = upper ? a : b;
-  const uint32_t got = dpp_u32<0x128>(give);  // row_ror:8
-  a = upper ? got : a;
-  b = upper ? b : got;
+__device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b) {
+  constexpr int kRor8 = 0x128;  // row_ror:8; the bank masks write one half of the 16
+  const uint32_t a0 = a;
+  a = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, kRor8, 0xF, 0xC, false);
+  b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a0, kRor8, 0xF, 0x3, false);
 }
 
 // Tiles mt0 .. mt0 + T - 1 of column tile nt.  Stage s of the stream is k-block
-// s % nk of tile s / nk, two k-steps of 16.  Every stage opens with a wait and
-// a barrier after which stage s + 1 is in LDS for all waves; the fragments of
-// a k-step are read during the MFMAs of the one before it, across stages and
-// tiles.  In the middle of stage s every wave issues one batch: the gathered
-// rows of stage s + 6 (4-byte LDS-DMA, the same bytes from every wave) and the
-// four operand loads of stage s + 3, whose rows came with batch s - 3; past
-// the last stage the loads give zeros, so that every batch has as many.  The
-// opening wait lets batch s - 1 stay in flight, and in a tile's first two
-// stages the sixteen stores of the tile before: behind batch s - 2 in the
-// order that vmcnt counts.  The stages have no branches on data, so the
-// compiler's own waits for the fragments stay exact.
+// s % nk of tile s / nk, two k-steps of 16.  At the top of stage s every wave
+// waits for its loads of stage s, then passes the barrier that shows them to
+// all waves, and issues one batch: the gathered rows of stage s + 4 (4-byte
+// LDS-DMA, the same bytes from every wave) and the six operand loads of stage
+// s + 2, whose rows came with batch s - 2; past the last stage they go on
+// loading the last tile's rows, so that every batch has as many.  The wait lets
+// batch s - 1 stay in flight, and in a tile's first two stages the sixteen
+// stores of the tile before: behind batch s - 2 in the order that vmcnt counts.
+//
+// Row r of a stage in LDS holds k-row pi(r) of the block of 32, the same for A
+// and B (their products are summed over k, so its order is free): r = 8 w + 2 i
+// + x holds 8 w + 4 x + i, which lets a lane fetch its four gathered rows at
+// once.  Rows past the segment are zero in the operand that is not gathered;
+// the gathered one repeats the segment's last row there.  Columns past an
+// operand load column 0 instead; what they give is never stored.
 enum Gathered { kNeither, kA, kB };
 template <Gathered GATHER>
 __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int expert, int mt0, int T,
@@ -424,80 +454,25 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
     rows = p.rows_dense;
   }
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wg = wave >> 2, wp = wave & 3;  // rows 128 wg .., columns 64 wp ..
-  // LDS-DMA: load i of a wave covers k-rows 2 (8 i + wave) .. + 1 of either
-  // operand (lane -> row + (l >> 5), slot l & 31), i < 2.
-  const int kr = 2 * wave + (lane >> 5);
-  const int chunk = (lane & 31) ^ (4 * (kr & 3));
-  const bool b_in = n0 + 8 * chunk < p.b_cols;
-  const uint32_t b_col = (uint32_t)(n0 + 8 * chunk) * 2u;
-  const uint32_t a_pitch = (uint32_t)p.lda * 2u, b_pitch = (uint32_t)p.ldb * 2u;
-  const int nk = (int)((rows + WK - 1) / WK);
-  const int total = T * nk;
+  const int wp = __builtin_amdgcn_readfirstlane(tid >> 6);  // 0..3: columns 64 wp ..
   const bool live = __builtin_amdgcn_readfirstlane(n0 + wp * 64 < p.b_cols);
 
-  const i32x4_t r_ids = buffer_at(p.tok + first, (uint32_t)min(rows * 4, (int64_t)0x7FFFFFFF));
-  const i32x4_t r_gather = GATHER == kA ? buffer_at(p.A, (uint32_t)(p.tok_rows * p.lda * 2))
-                                        : buffer_at(p.B, (uint32_t)(p.tok_rows * p.ldb * 2));
-  auto issue_ids = [&](int ks, int s) {
-    if constexpr (GATHER != kNeither)
-      dma4(r_ids, (uint32_t)(ks * WK + lane) * 4u, kIdsOff + s % kIdsSlots * kIdsSlot);
-  };
-  auto issue = [&](int mt, int ks, int s, bool any) {
-    const int at0 = (s % kWSlots) * kWSlot + wave * 1024;
-    const int64_t r0 = first + (int64_t)ks * WK;
-    // rows of this stage
-    const int left = any ? (int)min((int64_t)WK, rows - (int64_t)ks * WK) : 0;
-    const int m0 = mt * WM;
-    const bool a_in = m0 + 8 * chunk < p.a_cols;
-    const uint32_t a_col = (uint32_t)(m0 + 8 * chunk) * 2u;
-    uint32_t at[2];
-    if constexpr (GATHER != kNeither) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        at[i] = lds_read<uint32_t>(kIdsOff + s % kIdsSlots * kIdsSlot + (16 * i + kr) * 4);
-    }
-    const i32x4_t ra =
-        GATHER == kA ? r_gather : buffer_at(p.A + r0 * p.lda, (uint32_t)left * a_pitch);
-    const i32x4_t rb =
-        GATHER == kB ? r_gather : buffer_at(p.B + r0 * p.ldb, (uint32_t)left * b_pitch);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 16 * i + kr;
-      const uint32_t oa = (GATHER == kA ? at[i] : (uint32_t)r) * a_pitch + a_col;
-      const uint32_t ob = (GATHER == kB ? at[i] : (uint32_t)r) * b_pitch + b_col;
-      dma(ra, r < left && a_in ? oa : kNoAddr, at0 + 8 * i * 1024);
-      dma(rb, r < left && b_in ? ob : kNoAddr, at0 + kWaBytes + 8 * i * 1024);
-    }
-  };
-
   floatx16_t acc[4][2];
-  const KRows cols(lane);
-  int a_off[4], b_off[2];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) a_off[m] = cols.block_off(4 * wg + m);
-#pragma unroll
-  for (int f = 0; f < 2; ++f) b_off[f] = cols.block_off(2 * wp + f);
-  auto read = [&](Fragments<4>& f, int s, int k) {  // k-step k of stage s
-    const int slot = (s % kWSlots) * kWSlot + k * (16 * 512);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) f.B[i] = read_tr(slot + kWaBytes + b_off[i]);
-#pragma unroll
-    for (int m = 0; m < 4; ++m) f.A[m] = read_tr(slot + a_off[m]);
-  };
   // The wave's part of a tile, sixteen stores of 8 rows x 128 bytes: a lane's
   // four columns of two register groups are joined with the other half's to
   // eight (16 bytes), then rows trade places between lanes until eight lanes
   // hold the 64 columns of one row, a whole cache line.  Always sixteen: rows
-  // and columns past the result fall outside the buffer.
+  // and columns past the result fall outside the buffer.  The results are not
+  // read again here: non-temporal, they leave the caches to the operands.
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out + (int64_t)expert * p.out_stride,
                                               (uint32_t)p.a_cols * (uint32_t)p.b_cols * 2u);
+  // lane -> row l & 7, columns 32 ((l >> 3) & 1) + 16 ((l >> 4) & 1) + 8 (l >> 5)
+  const int o_col = n0 + wp * 64 + 32 * ((lane >> 3) & 1) + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+  const uint32_t o_pitch = (uint32_t)p.b_cols * 2u;
+  const uint32_t o_lane = o_col < p.b_cols ? (uint32_t)(lane & 7) * o_pitch + (uint32_t)o_col * 2u
+                                           : 0x80000000u;  // results are below 2 GiB
   auto store = [&](int mt) {
-    const bool upper = (lane & 8) != 0;
-    // lane -> row l & 7, columns 32 ((l >> 3) & 1) + 16 ((l >> 4) & 1) + 8 (l >> 5)
-    const int row0 = mt * WM + 128 * wg + (lane & 7);
-    const int col = n0 + wp * 64 + 32 * ((lane >> 3) & 1) + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+    const uint32_t at = o_lane + (uint32_t)(mt * WM) * o_pitch;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       uint32_t v[2][2][4];  // [f][register groups 2 u and 2 u + 1]
@@ -517,98 +492,158 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) swap_rows8(v[0][u][j], v[1][u][j], upper);
+        for (int j = 0; j < 4; ++j) swap_rows8(v[0][u][j], v[1][u][j]);
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const int r = row0 + 32 * m + 16 * u + 8 * f;
-          const uint32_t at = r < p.a_cols && col < p.b_cols
-                                  ? ((uint32_t)r * (uint32_t)p.b_cols + (uint32_t)col) * 2u : kNoAddr;
           const i32x4_t out = {(int)v[f][u][0], (int)v[f][u][1], (int)v[f][u][2], (int)v[f][u][3]};
-          __builtin_amdgcn_raw_buffer_store_b128(out, ro, (int)at, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(
+              out, ro, (int)(at + (uint32_t)(32 * m + 16 * u + 8 * f) * o_pitch), 0, kCpolNT);
         }
       }
     }
   };
-
   if (rows == 0) {  // an expert without rows: zeros
     clear_acc(acc);
-    if (live)
-      for (int t = 0; t < T; ++t) store(mt0 + t);
+    for (int t = 0; t < T; ++t) store(mt0 + t);
     return;
   }
-  // (tile, k-block) of the next batch's two parts
-  int di = 0, dk = 0;  // operand loads
-  int ik = 0;          // gathered rows
-  auto next_ids = [&](int s) {
-    issue_ids(ik, s);
-    ik = ik + 1 == nk ? 0 : ik + 1;
+
+  // LDS-DMA: load i of a wave fills A rows 8 wp + 4 i + q of the stage (lane ->
+  // q = l >> 4, slot l & 15), i < 2, and B rows 8 wp + 2 i + x (lane -> x = l
+  // >> 5, slot l & 31), i < 4.
+  const int nk = (int)((rows + WK - 1) / WK);
+  const uint32_t a_pitch = (uint32_t)p.lda * 2u, b_pitch = (uint32_t)p.ldb * 2u;
+  const int q = lane >> 4, x = lane >> 5;
+  const int a_chunk = (lane & 15) ^ (4 * q);                   // row & 3 = q
+  const int b_slot = lane & 31;
+  int b_chunk[4];                                              // row & 3 = 2 (i & 1) + x
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b_chunk[i] = b_slot ^ (4 * (2 * (i & 1) + x));
+  uint32_t b_lane[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = n0 + 8 * b_chunk[i] < p.b_cols ? n0 + 8 * b_chunk[i] : 0;
+    b_lane[i] = (uint32_t)c * 2u + (GATHER == kB ? 0u : (uint32_t)(8 * wp + 4 * x + i) * b_pitch);
+  }
+  const int a_id = 8 * wp + 4 * (q & 1) + (q >> 1), b_id = 8 * wp + 4 * x;  // first gathered row
+  const char* a_base = reinterpret_cast<const char*>(p.A) + (GATHER == kA ? 0 : first * (int64_t)a_pitch);
+  const char* b_base = reinterpret_cast<const char*>(p.B) + (GATHER == kB ? 0 : first * (int64_t)b_pitch);
+  const uint32_t g_bytes = (uint32_t)(p.tok_rows * (int64_t)(GATHER == kA ? a_pitch : b_pitch));
+  const i32x4_t r_ids = buffer_at(p.tok + first, 0x7FFFFFFFu);
+  const int last_row = (int)rows - 1;
+
+  // the next batch's position: gathered rows, then operands
+  int ik = 0, dk = 0, dt = 0, islot = 0, dslot = 0, dids = 0;
+  uint32_t a_lane[2];
+  auto set_tile = [&] {
+    const int c = (mt0 + dt) * WM + 8 * a_chunk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      a_lane[i] = (uint32_t)(c < p.a_cols ? c : 0) * 2u +
+                  (GATHER == kA ? 0u : (uint32_t)(a_id + 2 * i) * a_pitch);
   };
-  auto next_data = [&](int s) {
-    issue(mt0 + di, dk, s, s < total);
-    const bool wrap = dk + 1 == nk;
-    di += wrap ? 1 : 0;
-    dk = wrap ? 0 : dk + 1;
+  auto next_ids = [&] {
+    if constexpr (GATHER != kNeither) {
+      dma4(r_ids, (uint32_t)min(ik * WK + lane, last_row) * 4u, kIdsOff + islot * kIdsSlot);
+      islot = (islot + 1) & (kIdsSlots - 1);
+      ik = ik + 1 == nk ? 0 : ik + 1;
+    }
   };
+  auto next_data = [&] {
+    const int64_t row = (int64_t)dk * WK;
+    const uint32_t left = (uint32_t)min((int64_t)WK, rows - row);
+    uint32_t a[2] = {a_lane[0], a_lane[1]}, b[4] = {b_lane[0], b_lane[1], b_lane[2], b_lane[3]};
+    const int id = kIdsOff + dids * kIdsSlot;
+    if constexpr (GATHER == kA) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] += lds_read<uint32_t>(id + (a_id + 2 * i) * 4);
+    } else if constexpr (GATHER == kB) {
+      typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+      const u32x4_t r = lds_read<u32x4_t>(id + b_id * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] += r[i];
+    }
+    const i32x4_t ra = GATHER == kA ? buffer_at(a_base, g_bytes)
+                                    : buffer_at(a_base + row * (int64_t)a_pitch, left * a_pitch);
+    const i32x4_t rb = GATHER == kB ? buffer_at(b_base, g_bytes)
+                                    : buffer_at(b_base + row * (int64_t)b_pitch, left * b_pitch);
+    const int at = dslot * kWSlot;
+    dma_2_4(ra, a, at + wp * 2048, rb, b, at + kWaBytes + wp * 4096);
+    dslot = dslot == kWSlots - 1 ? 0 : dslot + 1;
+    dids = (dids + 1) & (kIdsSlots - 1);
+    if (++dk == nk) {
+      dk = 0;
+      if (dt + 1 < T) {
+        ++dt;
+        set_tile();
+      }
+    }
+  };
+  set_tile();
   if constexpr (GATHER != kNeither) {
-    for (int s = 0; s < 3; ++s) next_ids(s);
+    next_ids();
+    next_ids();
     wait_vmcnt<0>();
     stage_barrier();
   }
-  // batches -3, -2 and -1
-  for (int s = 0; s < 3; ++s) {
-    next_ids(3 + s);
-    next_data(s);
+  // batches -2 and -1
+  for (int s = 0; s < 2; ++s) {
+    next_ids();
+    next_data();
   }
-  constexpr int kBatch = GATHER != kNeither ? 5 : 4;
-  wait_vmcnt<2 * kBatch>();
-  stage_barrier();  // stage 0
-  Fragments<4> f0, f1;
-  read(f0, 0, 0);
-  int s = 0;
-  bool stored = false;  // this wave, the tile before
-  for (int t = 0; t < T; ++t) {
-    const bool mine = live && (mt0 + t) * WM + wg * 128 < p.a_cols;
-    auto open = [&](bool behind_stores) {
+  constexpr int kBatch = GATHER != kNeither ? 7 : 6;
+
+  const KRows<256> ka(lane);
+  const KRows<512> kb(lane);
+  int a_off[4], b_off[2];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) a_off[m] = ka.block_off(m);
+#pragma unroll
+  for (int f = 0; f < 2; ++f) b_off[f] = kWaBytes + kb.block_off(2 * wp + f);
+  auto run = [&](auto live_tag) {
+    constexpr bool LIVE = decltype(live_tag)::value;
+    int slot = 0;
+    auto read = [&](Fragments<4>& f, int k) {  // k-step k of the stage in slot
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f.B[i] = read_tr<512>(slot + b_off[i] + k * (16 * 512));
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f.A[m] = read_tr<256>(slot + a_off[m] + k * (16 * 256));
+    };
+    auto stage = [&](auto first_tag, bool behind_stores) {
       if (behind_stores) wait_vmcnt<kBatch + 16>();
       else wait_vmcnt<kBatch>();
-      stage_barrier();  // and every wave has left stage s - 1, whose slot is s + 3's
-    };
-    auto batch = [&] {
-      next_ids(s + 6);
-      next_data(s + 3);
-    };
-    if (mine) {
-      auto stage = [&](auto first_tag, bool behind_stores) {
-        open(behind_stores);
-        read(f1, s, 1);
+      stage_barrier();  // and every wave has left stage s - 1, whose slot is s + 2's
+      Fragments<4> f0, f1;
+      if constexpr (LIVE) {
+        read(f0, 0);
+        read(f1, 1);
+      }
+      next_ids();
+      next_data();
+      if constexpr (LIVE) {
         multiply<decltype(first_tag)::value>(f0, acc);
-        batch();
-        read(f0, s + 1, 0);  // past the last stage: zeros, not used
         multiply<false>(f1, acc);
-        ++s;
-      };
+      }
+      slot = slot == (kWSlots - 1) * kWSlot ? 0 : slot + kWSlot;
+    };
+    for (int t = 0; t < T; ++t) {
+      const bool stored = LIVE && t > 0;
       stage(std::true_type{}, stored);
       if (nk > 1) stage(std::false_type{}, stored);
       for (int k = 2; k < nk; ++k) stage(std::false_type{}, false);
-      store(mt0 + t);
-      stored = true;
-    } else {
-      // no rows or columns of this tile: only its share of the loads
-      for (int k = 0; k < nk; ++k) {
-        open(stored && k < 2);
-        batch();
-        ++s;
-      }
-      stored = false;
-      read(f0, s, 0);
+      if constexpr (LIVE) store(mt0 + t);
     }
-  }
+  };
+  if (live) run(std::true_type{});
+  else run(std::false_type{});
   wait_vmcnt<0>();  // nothing may still write the LDS when it is used again
 }
 
 // Items: the dense problems' tiles first (their sums run over all tokens),
-// then per expert the tiles of its three gradients, which share its rows.
-__global__ __launch_bounds__(512, 2) void weights_kernel(WeightsLaunch w) {
+// then expert by expert the gate and up tiles, then the down tiles: what the
+// blocks of one XCD read at a time (one or two experts' rows of x and dG | dU,
+// or of dy and s H) then stays in its L2.
+__global__ __launch_bounds__(256, 2) void weights_kernel(WeightsLaunch w) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int64_t b = blockIdx.x;
   for (int i = 0; i < w.n_dense; ++i) {
@@ -620,25 +655,26 @@ __global__ __launch_bounds__(512, 2) void weights_kernel(WeightsLaunch w) {
     }
     b -= t;
   }
-  const int64_t work = (int64_t)w.E * w.expert_items;
+  // gate and up have the same tiles
+  const WeightsProblem &gu = w.expert[0], &dn = w.expert[2];
+  const int gm = (gu.tiles_m + kWGroup - 1) / kWGroup, dm = (dn.tiles_m + kWGroup - 1) / kWGroup;
+  const int per_gu = 2 * gm * gu.tiles_n, per_dn = dm * dn.tiles_n;
+  const int64_t gu_blocks = xcd_blocks((int64_t)w.E * per_gu);
+  const bool up_down = b >= gu_blocks;
+  if (up_down) b -= gu_blocks;
+  const int per = up_down ? per_dn : per_gu;
+  const int64_t work = (int64_t)w.E * per;
   const int64_t share = (work + kXcds - 1) / kXcds;
   if (b / kXcds >= share) return;
   const int64_t item = xcd_item(b, share);
   if (item >= work) return;
-  const int e = (int)(item / w.expert_items);
-  int r = (int)(item % w.expert_items);
-  // gate and up have the same tiles
-  const WeightsProblem& gu = w.expert[0];
-  const int groups = (gu.tiles_m + kWGroup - 1) / kWGroup;
-  const int one = groups * gu.tiles_n;
-  if (r < 2 * one) {
-    const int i = r >= one ? 1 : 0;
-    r -= i * one;
-    const int m = r / gu.tiles_n * kWGroup;
-    weights_tiles<kB>(w.expert[i], e, m, min(kWGroup, gu.tiles_m - m), r % gu.tiles_n, lds);
+  const int e = (int)(item / per);
+  const int r = (int)(item % per);
+  if (!up_down) {
+    const int n = r / (2 * gm), g = r % (2 * gm);  // the tiles of one column tile of x together
+    const int m = g % gm * kWGroup;
+    weights_tiles<kB>(w.expert[g / gm], e, m, min(kWGroup, gu.tiles_m - m), n, lds);
   } else {
-    r -= 2 * one;
-    const WeightsProblem& dn = w.expert[2];
     const int m = r / dn.tiles_n * kWGroup;
     weights_tiles<kA>(dn, e, m, min(kWGroup, dn.tiles_m - m), r % dn.tiles_n, lds);
   }
@@ -659,15 +695,16 @@ __global__ __launch_bounds__(256) void pairs_kernel(const int32_t* __restrict__ 
   S[p] = in ? sigmoid_weight(Z[p / K * E + e]) : 0.0f;
 }
 
-// Of the grouped pairs: every row's token; block 0 also makes the m-tiles of
+// Of the grouped pairs: the byte offset of every row's token in x (pitch bytes
+// a token; the same in dy); block 0 also makes the m-tiles of
 // rows_kernel from the segment offsets (thread e counts its expert's tiles, a
 // scan places them).
 __global__ __launch_bounds__(512) void grouped_rows_kernel(
-    const int32_t* __restrict__ sorted_src, int64_t pairs, int K,
-    const int32_t* __restrict__ offsets, int E, int32_t* __restrict__ tok,
+    const int32_t* __restrict__ sorted_src, int64_t pairs, int K, uint32_t pitch,
+    const int32_t* __restrict__ offsets, int E, uint32_t* __restrict__ tok,
     int32_t* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
   const int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x;
-  if (i < pairs) tok[i] = sorted_src[i] / K;
+  if (i < pairs) tok[i] = (uint32_t)(sorted_src[i] / K) * pitch;
   if (blockIdx.x != 0) return;
   __shared__ uint32_t wsum[8];
   const int e = threadIdx.x, w = e >> 6;
@@ -775,11 +812,11 @@ hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K,
-                               const int32_t* offsets, int E, int32_t* tok, int32_t* tiles,
+hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K, uint32_t pitch,
+                               const int32_t* offsets, int E, uint32_t* tok, int32_t* tiles,
                                int32_t* n_tiles, hipStream_t stream) {
   hipLaunchKernelGGL(grouped_rows_kernel, dim3((unsigned)((pairs + 511) / 512)), dim3(512), 0,
-                     stream, sorted_src, pairs, K, offsets, E, tok, tiles, n_tiles);
+                     stream, sorted_src, pairs, K, pitch, offsets, E, tok, tiles, n_tiles);
   return hipGetLastError();
 }
 
@@ -787,7 +824,7 @@ int grad_tile_rows() { return TM; }
 
 static int64_t rows_blocks(const RowsProblem& p) {
   const int64_t m_tiles = p.tiles ? p.max_tiles : (p.rows_dense + TM - 1) / TM;
-  return (m_tiles * p.n_tiles_n + kXcds - 1) / kXcds * kXcds;
+  return xcd_blocks(m_tiles * p.n_tiles_n);
 }
 
 template <bool F32>
@@ -827,14 +864,11 @@ hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
     set_tiles(w.dense[i]);
     blocks += (int64_t)w.dense[i].tiles_m * w.dense[i].tiles_n;
   }
-  w.expert_items = 0;
-  for (WeightsProblem& q : w.expert) {
-    set_tiles(q);
-    w.expert_items += (q.tiles_m + kWGroup - 1) / kWGroup * q.tiles_n;
-  }
-  blocks += ((int64_t)w.E * w.expert_items + kXcds - 1) / kXcds * kXcds;
+  for (WeightsProblem& q : w.expert) set_tiles(q);
+  auto items = [](const WeightsProblem& q) { return (q.tiles_m + kWGroup - 1) / kWGroup * q.tiles_n; };
+  blocks += xcd_blocks((int64_t)w.E * 2 * items(w.expert[0])) + xcd_blocks((int64_t)w.E * items(w.expert[2]));
   if (blocks > 0x7FFFFFF0LL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(weights_kernel, dim3((unsigned)blocks), dim3(512), kWeightsLds, stream, w);
+  hipLaunchKernelGGL(weights_kernel, dim3((unsigned)blocks), dim3(256), kWeightsLds, stream, w);
   return hipGetLastError();
 }
 
