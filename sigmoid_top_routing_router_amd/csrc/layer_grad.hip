@@ -17,13 +17,13 @@
 //  * weights_kernel: every weight gradient, C[m, n] = sum_row A[row, m]
 //    B[row, n] over the rows of an expert's segment: both operands n
 //    contiguous.
-// Both give every wave 128 x 64 outputs of v_mfma_f32_32x32x16_bf16, eight
-// waves to a CU.  rows_kernel has long sums: one block of eight waves, 256 x
-// 256 outputs, stages of 64 k kept twice in LDS; the next stage's LDS-DMA
-// loads are issued as soon as every wave has left the stage before.
-// weights_kernel has short ones (an expert's rows, some 256) and large
-// results: stages of 32 k kept four times, and a block takes up to four 256 x
-// 256 tiles under each other as one stream of stages, so that a tile's first
+// Both multiply 128 x 256 tiles with v_mfma_f32_32x32x16_bf16, four waves of
+// 128 x 64, two blocks to a CU, so that one block's start, loads and stores
+// pass behind the other's MFMAs.  rows_kernel has long sums: A in stages of 64
+// k (whole 128-byte lines of its rows) kept twice, B in halves of 32 k kept
+// three times.  weights_kernel has short ones (an expert's rows, some 256) and
+// large results: stages of 32 k kept three times, and a block takes up to two
+// tiles under each other as one stream of stages, so that a tile's first
 // loads and the last tile's stores pass behind MFMAs.  The loads are written in assembly
 // (they have no register result): as builtins, the compiler waits for all of
 // them in front of the first transposing LDS read, which it takes for a
@@ -44,15 +44,17 @@ namespace moe {
 
 namespace {
 
-constexpr int TN = 256;                        // columns of a tile
+constexpr int TM = 128, TN = 256;              // rows and columns of a tile
 // rows_kernel
-constexpr int TM = 256, TK = 64;
-constexpr int kOpBytes = 32 * 1024;            // one operand of one stage
-constexpr int kSlotBytes = 2 * kOpBytes;
-constexpr int kRowsLds = 2 * kSlotBytes + 8 * 1024;  // and the staged result
+constexpr int TK = 64;
+constexpr int kRaBytes = TM * TK * 2;          // A of one stage, two slots
+constexpr int kRbOff = 2 * kRaBytes;
+constexpr int kRbBytes = TK / 2 * TN * 2;      // B of half a stage, three slots
+constexpr int kRowsLds = kRbOff + 3 * kRbBytes;
+static_assert(2 * kRowsLds <= 160 * 1024, "two blocks share a CU");
 // weights_kernel
-constexpr int WM = 128, WK = 32;
-constexpr int kWaBytes = WK * WM * 2;          // A of one stage, then B
+constexpr int WK = 32;
+constexpr int kWaBytes = WK * TM * 2;          // A of one stage, then B
 constexpr int kWSlot = kWaBytes + WK * TN * 2;
 constexpr int kWSlots = 3;
 constexpr int kIdsOff = kWSlots * kWSlot;      // gathered rows of eight stages
@@ -62,15 +64,15 @@ constexpr int kWeightsLds = kIdsOff + kIdsSlots * kIdsSlot;
 constexpr int kWGroup = 2;                     // tiles of a block
 static_assert(2 * kWeightsLds <= 160 * 1024, "two blocks share a CU");
 constexpr int kXcds = 8;
-// An offset past the end of any operand: the load returns zeros.  Operands
-// are smaller than this (checked by the entry point).
-constexpr uint32_t kNoAddr = kGradMaxOperandBytes;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
+// The wave's LDS reads have come back before it lets the others on: what they
+// read may be overwritten then.
 __device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -82,45 +84,48 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 // Raw buffer descriptor in scalar registers (stride 0; reads past `bytes`
 // return zeros).
-__device__ __forceinline__ i32x4_t buffer_at(const void* base, uint32_t bytes) {
-  const uint64_t a = (uint64_t)base;
+__device__ __forceinline__ i32x4_t buffer_at(uint64_t a, uint32_t bytes) {
   return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
                  __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu)),
                  __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
+__device__ __forceinline__ i32x4_t buffer_at(const void* base, uint32_t bytes) {
+  return buffer_at((uint64_t)base, bytes);
+}
+// An offset past the end of any operand: the load returns zeros.  Operands
+// are smaller than this (checked by the entry point).
+constexpr uint32_t kNoAddr = kGradMaxOperandBytes;
 // LDS addresses are byte offsets of the block's LDS (these kernels have no
 // static LDS, so the dynamic array starts at 0).
-// LDS-DMA: 16 (dma4: 4) bytes per lane from buffer + off to LDS at `at` + 16
-// (4) * lane.  Counted on vmcnt; the waits are this file's own (wait_vmcnt).
-// m0 (the LDS address) is set and used inside; nothing else in these kernels
-// uses it.
-__device__ __forceinline__ void dma(i32x4_t r, uint32_t off, int at) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know these operands
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(r) : "memory");
-#endif
-}
+// LDS-DMA: 16 (dma4: 4) bytes per lane from a buffer to LDS at `at` + 16 (4) *
+// lane.  Counted on vmcnt; the waits are this file's own (wait_vmcnt).  m0 (the
+// LDS address) is set and used inside; nothing else in these kernels uses it.
+#define MOE_DMA16_NEXT(v, r) "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 " v ", " r
 __device__ __forceinline__ void dma4(i32x4_t r, uint32_t off, int at) {
-#ifdef __HIP_DEVICE_COMPILE__
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know these operands
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(r) : "memory");
 #endif
 }
-// One stage of weights_kernel for a wave: two loads of A and four of B, each
-// 1 KB after the other in LDS.
-__device__ __forceinline__ void dma_2_4(i32x4_t ra, const uint32_t (&a)[2], int a_at, i32x4_t rb,
-                                        const uint32_t (&b)[4], int b_at) {
+// Four loads, each 1 KB after the other in LDS, at off + soff of the buffer.
+__device__ __forceinline__ void dma_4(i32x4_t r, const uint32_t (&v)[4], uint32_t soff, int at) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %8, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %8, 0 offen lds\n\t"
-      "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %9, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %9, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %6, %9, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %7, %9, 0 offen lds"
-      :: "s"(__builtin_amdgcn_readfirstlane(a_at)), "s"(__builtin_amdgcn_readfirstlane(b_at)),
-         "v"(a[0]), "v"(a[1]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "s"(ra), "s"(rb)
-      : "memory", "scc");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
+               MOE_DMA16_NEXT("%2", "%5, %6 offen lds\n\t")
+               MOE_DMA16_NEXT("%3", "%5, %6 offen lds\n\t")
+               MOE_DMA16_NEXT("%4", "%5, %6 offen lds")
+               :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(v[0]), "v"(v[1]), "v"(v[2]),
+                  "v"(v[3]), "s"(r), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+               : "memory", "scc");
+#endif
+}
+// Two loads of one buffer.
+__device__ __forceinline__ void dma_2(i32x4_t r, const uint32_t (&v)[2], int at) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+               MOE_DMA16_NEXT("%2", "%3, 0 offen lds")
+               :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(v[0]), "v"(v[1]), "s"(r)
+               : "memory", "scc");
 #endif
 }
 template <class T>
@@ -176,38 +181,73 @@ __device__ __forceinline__ void multiply(const Fragments<LIVE>& f, floatx16_t (&
           f.B[i], f.A[m], FIRST ? floatx16_t{} : acc[m][i], 0, 0, 0);
 }
 
-// The accumulators hold the tile transposed (the B fragment is the first
-// operand): lane l has tile row (l & 31) of a block and columns 8 (r / 4) +
-// 4 (l / 32) + r % 4.  rows_kernel's bf16 results pass through the idle LDS and leave as
-// 16-byte pieces of whole rows; row_ptr(r) is the output of tile row r, or
-// null.
-constexpr int kOutStride = TN * 2 + 8;
-static_assert(TM * kOutStride <= kRowsLds, "staged tile");
-template <class RowPtr>
-__device__ __forceinline__ void store_bf16_tile(floatx16_t (&acc)[4][2], int lane, int wg, int wp,
-                                                int tid, char* lds, int cols, RowPtr row_ptr) {
-  __syncthreads();
+// The accumulators hold the wave's 128 x 64 outputs transposed (the B fragment
+// is the first operand): lane l has row (l & 31) of a block and columns
+// 8 (r / 4) + 4 (l / 32) + r % 4 of its register r.
+//
+// The upper 32 lanes' a change places with the lower lanes' b; the odd rows'
+// (of 16 lanes) a with the even rows' b; within every 16 lanes, the upper
+// eight's a with the lower eight's b.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b) {
+  constexpr int kRor8 = 0x128;  // row_ror:8; the bank masks write one half of the 16
+  const uint32_t a0 = a;
+  a = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, kRor8, 0xF, 0xC, false);
+  b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a0, kRor8, 0xF, 0x3, false);
+}
+
+// bf16 results, sixteen stores of 8 rows x 128 bytes: a lane's four columns of
+// two register groups are joined with the other half's to eight (16 bytes),
+// then rows trade places between lanes until eight lanes hold the 64 columns
+// of one row, a whole cache line (32 rows x 32 bytes a store took twice the
+// time).  Always sixteen: rows and columns past the result fall outside the
+// buffer.  Lane l stores row line_row(l), columns line_col(l) .. + 7 of every
+// group of eight rows; `at` is that place's byte offset, pitch a row's bytes.
+__device__ __forceinline__ int line_row(int lane) { return lane & 7; }
+__device__ __forceinline__ int line_col(int lane) {
+  return 32 * ((lane >> 3) & 1) + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+}
+constexpr uint32_t kNoStore = 0x80000000u;  // past any result (below 2 GiB)
+template <int CPOL>
+__device__ __forceinline__ void store_lines(const floatx16_t (&acc)[4][2],
+                                            __amdgpu_buffer_rsrc_t out, uint32_t at,
+                                            uint32_t pitch) {
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    char* row = lds + (wg * 128 + m * 32 + (lane & 31)) * kOutStride + (wp * 64 + 4 * (lane >> 5)) * 2;
+    uint32_t v[2][2][4];  // [f][register groups 2 u and 2 u + 1]
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 2; ++f) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint2*>(row + (32 * f + 8 * q) * 2) =
-            make_uint2(pack_bf16(acc[m][f][4 * q], acc[m][f][4 * q + 1]),
-                       pack_bf16(acc[m][f][4 * q + 2], acc[m][f][4 * q + 3]));
-  }
-  __syncthreads();
-  const int ch = tid & 31;
-  if (ch * 8 >= cols) return;
-  for (int r = tid >> 5; r < TM; r += 16) {
-    uint16_t* p = row_ptr(r);
-    if (!p) break;  // rows run out in order
-    const char* src = lds + r * kOutStride + ch * 16;
-    const uint2 lo = *reinterpret_cast<const uint2*>(src);
-    const uint2 hi = *reinterpret_cast<const uint2*>(src + 8);
-    *reinterpret_cast<uint4*>(p + ch * 8) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          v[f][u][j] = pack_bf16(acc[m][f][8 * u + 2 * j], acc[m][f][8 * u + 2 * j + 1]);
+          v[f][u][2 + j] = pack_bf16(acc[m][f][8 * u + 4 + 2 * j], acc[m][f][8 * u + 5 + 2 * j]);
+          swap_halves(v[f][u][j], v[f][u][2 + j]);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) swap_rows16(v[f][0][j], v[f][1][j]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) swap_rows8(v[0][u][j], v[1][u][j]);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const i32x4_t w = {(int)v[f][u][0], (int)v[f][u][1], (int)v[f][u][2], (int)v[f][u][3]};
+        __builtin_amdgcn_raw_buffer_store_b128(
+            w, out, (int)(at + (uint32_t)(32 * m + 16 * u + 8 * f) * pitch), 0, CPOL);
+      }
+    }
   }
 }
 
@@ -228,11 +268,18 @@ __host__ __device__ __forceinline__ int64_t xcd_blocks(int64_t work) {
 // ---------------------------------------------------------------- rows
 // PAIR: rows of the tile table, else tokens.  F32: the fp32 result (Q), whose
 // pairs gather their rows of A; else bf16 (parts of dx).
+//
+// The segments' stages are one stream.  Half-stage h (32 k) opens with a wait
+// for the wave's own loads of it and the barrier that shows them to all waves
+// and frees what half-stage h - 1 read; then it loads B of half-stage h + 2
+// and, when h is the first half of stage j, A of stage j + 1.  Rows past the
+// tile repeat its last row and columns past the result column 0 (what they
+// give is not stored); k past a segment reads zeros of both.
 template <bool PAIR, bool F32>
-__device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, char* lds) {
+__device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item) {
   constexpr bool GATHER = PAIR && F32;
   const int64_t mt = item / p.n_tiles_n;
-  const int nt = (int)(item % p.n_tiles_n);
+  const int n0 = (int)(item % p.n_tiles_n) * TN;
   int expert = 0, rows;
   int64_t row0;
   if constexpr (PAIR) {
@@ -245,185 +292,189 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item, ch
     rows = (int)min((int64_t)TM, p.rows_dense - row0);
   }
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wg = wave >> 2, wp = wave & 3;
-  const int n0 = nt * TN;
+  const int wp = __builtin_amdgcn_readfirstlane(tid >> 6);  // columns 64 wp ..
 
-  // LDS-DMA: load i of a wave covers A rows 8 (8 i + wave) .. + 7 (lane ->
-  // row + (l >> 3), slot l & 7) and B k-rows 2 (8 i + wave) .. + 1 (lane ->
-  // row + (l >> 5), slot l & 31).
-  const int a_chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
-  const int b_k = 2 * wave + (lane >> 5);
-  const int b_chunk = (lane & 31) ^ (4 * (b_k & 3));
-  const bool b_col = n0 + 8 * b_chunk < p.ncols;
-  const uint32_t b_pitch = (uint32_t)p.ncols * 2u;
-  const uint32_t b_lane = (uint32_t)b_k * b_pitch + (uint32_t)(n0 + 8 * b_chunk) * 2u;
-  uint32_t a_row[4];
+  // LDS-DMA: load i of a wave covers A rows 32 wp + 8 i .. + 7 (lane -> row +
+  // (l >> 3), slot l & 7, which holds chunk (l & 7) ^ ((row >> 1) & 7)) and B
+  // k-rows 8 wp + 2 i + x (lane -> x = l >> 5, slot l & 31).
+  uint32_t a_row[4];  // row index, or byte offset when gathered
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = 8 * (8 * i + wave) + (lane >> 3);
-    a_row[i] = r >= rows ? 0xFFFFFFFFu : GATHER ? p.gather[row0 + r] : (uint32_t)r;
+    const int r = min(32 * wp + 8 * i + (lane >> 3), rows - 1);
+    a_row[i] = GATHER ? p.gather[row0 + r] : (uint32_t)r;
   }
-  // The segments' stages as one stream; this is the next one to load.
-  i32x4_t ra, rb;
-  uint32_t a_off[4];
-  int seg = -1, ks = 0, nk = 0, kdim = 0;
-  auto next_segment = [&] {
-    ++seg;
-    const RowsSegment& sg = p.seg[seg];
-    // a gathered A spans the whole buffer, a direct one this tile's rows
-    ra = buffer_at(GATHER ? sg.A : sg.A + row0 * sg.lda,
-                   (uint32_t)((GATHER ? p.a_rows : rows) * sg.lda * 2));
-    rb = buffer_at(sg.B + (int64_t)expert * sg.b_expert_stride,
-                   (uint32_t)sg.kdim * (uint32_t)p.ncols * 2u);
-    kdim = sg.kdim;
-    nk = (kdim + TK - 1) / TK;
-    ks = 0;
+  const uint32_t b_pitch = (uint32_t)p.ncols * 2u;
+  uint32_t b_lane[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      a_off[i] = a_row[i] != 0xFFFFFFFFu
-                     ? a_row[i] * (GATHER ? 1u : (uint32_t)(sg.lda * 2)) + (uint32_t)a_chunk * 16u
-                     : kNoAddr;
+  for (int i = 0; i < 4; ++i) {
+    const int k = 8 * wp + 2 * i + (lane >> 5);
+    const int c = n0 + 8 * ((lane & 31) ^ (4 * (k & 3)));
+    b_lane[i] = (uint32_t)k * b_pitch + (uint32_t)(c < p.ncols ? c : 0) * 2u;
+  }
+  // the next stage to load
+  i32x4_t ra = {};
+  uint64_t b_at = 0;     // address of the stage in B
+  uint32_t a_lane[4] = {};
+  int seg = -1, left = 0;  // left: k of the segment from this stage on
+  uint32_t a_k = 0;        // byte offset of the stage in A's rows
+  const int chunk0 = (lane & 7) ^ (lane >> 4);  // of loads 0 and 2; 1 and 3: ^ 4
+  auto next_stage = [&] {
+    left -= TK;
+    a_k += TK * 2;
+    b_at += (uint64_t)TK * b_pitch;
+    if (left <= 0 && seg + 1 < p.n_seg) {
+      ++seg;
+      const RowsSegment& sg = p.seg[seg];
+      // a gathered A spans the whole buffer, a direct one this tile's rows
+      ra = buffer_at(GATHER ? sg.A : sg.A + row0 * sg.lda,
+                     (uint32_t)((GATHER ? p.a_rows : rows) * sg.lda * 2));
+      b_at = (uint64_t)(sg.B + (int64_t)expert * sg.b_expert_stride);
+      left = sg.kdim;
+      a_k = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a_lane[i] = a_row[i] * (GATHER ? 1u : (uint32_t)(sg.lda * 2)) +
+                    (uint32_t)(chunk0 ^ (4 * (i & 1))) * 16u;
+    }
+    if (left < TK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a_lane[i] = 8 * (chunk0 ^ (4 * (i & 1))) < left ? a_lane[i] + a_k : kNoAddr;
+      a_k = 0;
+    }
   };
   int total = 0;
   for (int i = 0; i < p.n_seg; ++i) total += (p.seg[i].kdim + TK - 1) / TK;
-  auto issue = [&](int s) {  // past the last stage: zeros
-    if (ks == nk && seg + 1 < p.n_seg) next_segment();
-    const int k0 = ks * TK;
-    const int left = kdim - k0;  // <= 0 past the end
-    ++ks;
-    const int at = (s & 1) * kSlotBytes + wave * 1024;
-    const bool ka = 8 * a_chunk < left;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      dma(ra, ka ? a_off[i] + (uint32_t)k0 * 2u : kNoAddr, at + 8 * i * 1024);
-    const uint32_t b0 = (uint32_t)k0 * b_pitch + b_lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      dma(rb, b_col && 16 * i + b_k < left ? b0 + (uint32_t)(16 * i) * b_pitch : kNoAddr,
-          at + kOpBytes + 8 * i * 1024);
+  int a_slot = 0, b_slot = 0;  // of the next loads
+  auto load_a = [&] {
+    dma_4(ra, a_lane, a_k, a_slot + wp * 4096);
+    a_slot ^= kRaBytes;
+  };
+  auto load_b = [&](int half) {
+    const int n = min(max(left - half * (TK / 2), 0), TK / 2);  // past the last stage: none
+    const i32x4_t rb = buffer_at(b_at + (uint64_t)(half * (TK / 2)) * b_pitch, (uint32_t)n * b_pitch);
+    dma_4(rb, b_lane, 0u, kRbOff + b_slot + wp * 4096);
+    b_slot = b_slot == 2 * kRbBytes ? 0 : b_slot + kRbBytes;
   };
 
   floatx16_t acc[4][2];
   clear_acc(acc);
   const KRows<512> kb(lane);
-  const int b_off[2] = {kOpBytes + kb.block_off(2 * wp), kOpBytes + kb.block_off(2 * wp + 1)};
-  const int a_base = (wg * 128 + (lane & 31)) * 128;
-  int live_m = (rows - wg * 128 + 31) / 32;
-  live_m = __builtin_amdgcn_readfirstlane(live_m < 0 ? 0 : live_m > 4 ? 4 : live_m);
-  const bool live = __builtin_amdgcn_readfirstlane(live_m > 0 && n0 + wp * 64 < p.ncols);
-
-  // Fragments of a k-step are read during the MFMAs of the one before it.  In
-  // the last k-step of a stage the barrier that makes the next stage visible
-  // frees this one's slot for the stage after it, whose loads follow.
+  const int b_off[2] = {kRbOff + kb.block_off(2 * wp), kRbOff + kb.block_off(2 * wp + 1)};
+  const int a_base = (lane & 31) * 128, a_swz = (lane >> 1) & 7, a_hi = lane >> 5;
   auto run = [&](auto live_tag) {
-    constexpr int LIVE = decltype(live_tag)::value;
-    auto read = [&](Fragments<LIVE>& f, int s, int k) {
-      const int slot = (s & 1) * kSlotBytes;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) f.B[i] = read_tr<512>(slot + b_off[i] + k * (16 * 512));
-      const int a_at = slot + a_base + ((2 * k + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
-#pragma unroll
-      for (int m = 0; m < LIVE; ++m) f.A[m] = lds_read<bf16x8_t>(a_at + m * (32 * 128));
-    };
-    next_segment();
-    issue(0);
-    issue(1);
-    wait_vmcnt<8>();
-    stage_barrier();
-    Fragments<LIVE> f0, f1;
-    if (LIVE > 0) read(f0, 0, 0);
-    for (int s = 0; s < total; ++s) {
-      if (LIVE > 0) {
-        read(f1, s, 1);
-        multiply<false>(f0, acc);
-        read(f0, s, 2);
-        multiply<false>(f1, acc);
-        read(f1, s, 3);
-        multiply<false>(f0, acc);
-      }
-      wait_vmcnt<0>();
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    constexpr int LIVE = decltype(live_tag)::value;  // row blocks with valid rows
+    constexpr int NF = LIVE > 0 ? LIVE : 1;
+    int a_read = 0, b_read = 0;
+    auto half = [&](auto half_tag) {
+      constexpr int HALF = decltype(half_tag)::value;
+      if (HALF == 0) wait_vmcnt<4>();
+      else wait_vmcnt<8>();
       stage_barrier();
-      if (LIVE > 0) read(f0, s + 1, 0);  // past the last stage: zeros, not used
-      issue(s + 2);
-      if (LIVE > 0) multiply<false>(f1, acc);
+      Fragments<NF> f[2];
+      if constexpr (LIVE > 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) f[k].B[i] = read_tr<512>(b_read + b_off[i] + k * (16 * 512));
+          const int at = a_read + a_base + ((2 * (2 * HALF + k) + a_hi) ^ a_swz) * 16;
+#pragma unroll
+          for (int m = 0; m < NF; ++m) f[k].A[m] = lds_read<bf16x8_t>(at + m * (32 * 128));
+        }
+      }
+      if (HALF == 0) {
+        next_stage();
+        load_a();
+      }
+      load_b(HALF);
+      if constexpr (LIVE > 0) {
+        multiply<false>(f[0], acc);
+        multiply<false>(f[1], acc);
+      }
+      b_read = b_read == 2 * kRbBytes ? 0 : b_read + kRbBytes;
+    };
+    for (int j = 0; j < total; ++j) {
+      half(std::integral_constant<int, 0>{});
+      half(std::integral_constant<int, 1>{});
+      a_read ^= kRaBytes;
     }
-    wait_vmcnt<0>();  // nothing may still write the LDS when it is used again
   };
+  next_stage();
+  load_a();
+  load_b(0);
+  load_b(1);
+  const bool live = __builtin_amdgcn_readfirstlane(n0 + wp * 64 < p.ncols);
+  const int live_m = (rows + 31) / 32;
   if (!live) run(std::integral_constant<int, 0>{});
-  else if (live_m > 2) run(std::integral_constant<int, 4>{});
-  else run(std::integral_constant<int, 2>{});
+  else if (live_m == 1) run(std::integral_constant<int, 1>{});
+  else if (live_m == 2) run(std::integral_constant<int, 2>{});
+  else if (live_m == 3) run(std::integral_constant<int, 3>{});
+  else run(std::integral_constant<int, 4>{});
+  wait_vmcnt<0>();  // nothing may still write the LDS when another block has it
+  if (!live) return;
 
   if constexpr (F32) {
-    float* out = reinterpret_cast<float*>(p.out);
+    // Thirty-two stores of 16 rows x 64 bytes: two register groups of four
+    // columns trade the rows of their 16 lanes.
+    const uint32_t pitch = (uint32_t)p.ldo * 4u;
+    const __amdgpu_buffer_rsrc_t out =
+        make_rsrc(reinterpret_cast<float*>(p.out) + row0 * p.ldo, (uint32_t)rows * pitch);
+    const int col = n0 + wp * 64 + 8 * ((lane >> 4) & 1) + 4 * (lane >> 5);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int r = wg * 128 + m * 32 + (lane & 31);
-      if (!live || r >= rows) continue;
-      float* o = out + (row0 + r) * p.ldo + n0;
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int u = 0; u < 2; ++u) {
+        const int c = col + 32 * f + 16 * u;
+        const uint32_t at = c < p.ncols ? (uint32_t)(lane & 15) * pitch + (uint32_t)c * 4u : kNoStore;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = wp * 64 + 32 * f + 8 * q + 4 * (lane >> 5);
-          if (n0 + c < p.ncols)
-            *reinterpret_cast<float4*>(o + c) =
-                make_float4(acc[m][f][4 * q], acc[m][f][4 * q + 1], acc[m][f][4 * q + 2],
-                            acc[m][f][4 * q + 3]);
+        for (int m = 0; m < 4; ++m) {
+          uint32_t v[2][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[0][j] = __float_as_uint(acc[m][f][8 * u + j]);
+            v[1][j] = __float_as_uint(acc[m][f][8 * u + 4 + j]);
+            swap_rows16(v[0][j], v[1][j]);
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const i32x4_t w = {(int)v[g][0], (int)v[g][1], (int)v[g][2], (int)v[g][3]};
+            __builtin_amdgcn_raw_buffer_store_b128(w, out, (int)(at + (uint32_t)(32 * m + 16 * g) * pitch),
+                                                   0, 0);
+          }
         }
-    }
-    return;
+      }
+  } else {
+    const uint32_t pitch = (uint32_t)p.ldo * 2u;
+    const __amdgpu_buffer_rsrc_t out =
+        make_rsrc(reinterpret_cast<uint16_t*>(p.out) + row0 * p.ldo, (uint32_t)rows * pitch);
+    const int col = n0 + wp * 64 + line_col(lane);
+    store_lines<0>(acc, out,
+                   col < p.ncols ? (uint32_t)line_row(lane) * pitch + (uint32_t)col * 2u : kNoStore,
+                   pitch);
   }
-  uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row0 * p.ldo + n0;
-  store_bf16_tile(acc, lane, wg, wp, tid, lds, p.ncols - n0,
-                  [&](int r) { return r < rows ? out + r * p.ldo : nullptr; });
 }
 
 // The work item of block b of a problem's share of the grid.
 template <bool PAIR, bool F32>
-__device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b, char* lds) {
+__device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b) {
   const int64_t m_tiles = PAIR ? (int64_t)*p.n_tiles : (p.rows_dense + TM - 1) / TM;
   const int64_t work = m_tiles * p.n_tiles_n;
   const int64_t share = (work + kXcds - 1) / kXcds;
   if (b / kXcds >= share) return;
   const int64_t item = xcd_item(b, share);
-  if (item < work) rows_tile<PAIR, F32>(p, item, lds);
+  if (item < work) rows_tile<PAIR, F32>(p, item);
 }
 
 // The tokens' blocks first (fewer items), then the pairs'.
 template <bool F32>
-__global__ __launch_bounds__(512, 2) void rows_kernel(RowsProblem token, RowsProblem pair,
+__global__ __launch_bounds__(256, 2) void rows_kernel(RowsProblem token, RowsProblem pair,
                                                       int64_t token_blocks) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int64_t b = blockIdx.x;
-  if (b < token_blocks) rows_block<false, F32>(token, b, lds);
-  else rows_block<true, F32>(pair, b - token_blocks, lds);
+  if (b < token_blocks) rows_block<false, F32>(token, b);
+  else rows_block<true, F32>(pair, b - token_blocks);
 }
 
 // ---------------------------------------------------------------- weights
-// The upper 32 lanes' a change places with the lower lanes' b; the odd rows'
-// (of 16 lanes) a with the even rows' b.
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-
-// Within every 16 lanes, the upper eight's a change places with the lower
-// eight's b.
-__device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b) {
-  constexpr int kRor8 = 0x128;  // row_ror:8; the bank masks write one half of the 16
-  const uint32_t a0 = a;
-  a = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, kRor8, 0xF, 0xC, false);
-  b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a0, kRor8, 0xF, 0x3, false);
-}
-
 // Tiles mt0 .. mt0 + T - 1 of column tile nt.  Stage s of the stream is k-block
 // s % nk of tile s / nk, two k-steps of 16.  At the top of stage s every wave
 // waits for its loads of stage s, then passes the barrier that shows them to
@@ -443,7 +494,7 @@ __device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b) {
 enum Gathered { kNeither, kA, kB };
 template <Gathered GATHER>
 __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int expert, int mt0, int T,
-                                              int nt, char* lds) {
+                                              int nt) {
   const int n0 = nt * TN;
   int64_t first, rows;
   if constexpr (GATHER != kNeither) {
@@ -458,49 +509,16 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
   const bool live = __builtin_amdgcn_readfirstlane(n0 + wp * 64 < p.b_cols);
 
   floatx16_t acc[4][2];
-  // The wave's part of a tile, sixteen stores of 8 rows x 128 bytes: a lane's
-  // four columns of two register groups are joined with the other half's to
-  // eight (16 bytes), then rows trade places between lanes until eight lanes
-  // hold the 64 columns of one row, a whole cache line.  Always sixteen: rows
-  // and columns past the result fall outside the buffer.  The results are not
-  // read again here: non-temporal, they leave the caches to the operands.
+  // The results are not read again here: non-temporal, they leave the caches
+  // to the operands.
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out + (int64_t)expert * p.out_stride,
                                               (uint32_t)p.a_cols * (uint32_t)p.b_cols * 2u);
-  // lane -> row l & 7, columns 32 ((l >> 3) & 1) + 16 ((l >> 4) & 1) + 8 (l >> 5)
-  const int o_col = n0 + wp * 64 + 32 * ((lane >> 3) & 1) + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
   const uint32_t o_pitch = (uint32_t)p.b_cols * 2u;
-  const uint32_t o_lane = o_col < p.b_cols ? (uint32_t)(lane & 7) * o_pitch + (uint32_t)o_col * 2u
-                                           : 0x80000000u;  // results are below 2 GiB
+  const int o_col = n0 + wp * 64 + line_col(lane);
+  const uint32_t o_lane =
+      o_col < p.b_cols ? (uint32_t)line_row(lane) * o_pitch + (uint32_t)o_col * 2u : kNoStore;
   auto store = [&](int mt) {
-    const uint32_t at = o_lane + (uint32_t)(mt * WM) * o_pitch;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      uint32_t v[2][2][4];  // [f][register groups 2 u and 2 u + 1]
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            v[f][u][j] = pack_bf16(acc[m][f][8 * u + 2 * j], acc[m][f][8 * u + 2 * j + 1]);
-            v[f][u][2 + j] = pack_bf16(acc[m][f][8 * u + 4 + 2 * j], acc[m][f][8 * u + 5 + 2 * j]);
-            swap_halves(v[f][u][j], v[f][u][2 + j]);
-          }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) swap_rows16(v[f][0][j], v[f][1][j]);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) swap_rows8(v[0][u][j], v[1][u][j]);
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const i32x4_t out = {(int)v[f][u][0], (int)v[f][u][1], (int)v[f][u][2], (int)v[f][u][3]};
-          __builtin_amdgcn_raw_buffer_store_b128(
-              out, ro, (int)(at + (uint32_t)(32 * m + 16 * u + 8 * f) * o_pitch), 0, kCpolNT);
-        }
-      }
-    }
+    store_lines<kCpolNT>(acc, ro, o_lane + (uint32_t)(mt * TM) * o_pitch, o_pitch);
   };
   if (rows == 0) {  // an expert without rows: zeros
     clear_acc(acc);
@@ -536,7 +554,7 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
   int ik = 0, dk = 0, dt = 0, islot = 0, dslot = 0, dids = 0;
   uint32_t a_lane[2];
   auto set_tile = [&] {
-    const int c = (mt0 + dt) * WM + 8 * a_chunk;
+    const int c = (mt0 + dt) * TM + 8 * a_chunk;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       a_lane[i] = (uint32_t)(c < p.a_cols ? c : 0) * 2u +
@@ -568,7 +586,8 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
     const i32x4_t rb = GATHER == kB ? buffer_at(b_base, g_bytes)
                                     : buffer_at(b_base + row * (int64_t)b_pitch, left * b_pitch);
     const int at = dslot * kWSlot;
-    dma_2_4(ra, a, at + wp * 2048, rb, b, at + kWaBytes + wp * 4096);
+    dma_2(ra, a, at + wp * 2048);
+    dma_4(rb, b, 0u, at + kWaBytes + wp * 4096);
     dslot = dslot == kWSlots - 1 ? 0 : dslot + 1;
     dids = (dids + 1) & (kIdsSlots - 1);
     if (++dk == nk) {
@@ -644,13 +663,12 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
 // blocks of one XCD read at a time (one or two experts' rows of x and dG | dU,
 // or of dy and s H) then stays in its L2.
 __global__ __launch_bounds__(256, 2) void weights_kernel(WeightsLaunch w) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   int64_t b = blockIdx.x;
   for (int i = 0; i < w.n_dense; ++i) {
     const int t = w.dense[i].tiles_m * w.dense[i].tiles_n;
     if (b < t) {
       weights_tiles<kNeither>(w.dense[i], 0, (int)b / w.dense[i].tiles_n, 1,
-                              (int)b % w.dense[i].tiles_n, lds);
+                              (int)b % w.dense[i].tiles_n);
       return;
     }
     b -= t;
@@ -673,10 +691,10 @@ __global__ __launch_bounds__(256, 2) void weights_kernel(WeightsLaunch w) {
   if (!up_down) {
     const int n = r / (2 * gm), g = r % (2 * gm);  // the tiles of one column tile of x together
     const int m = g % gm * kWGroup;
-    weights_tiles<kB>(w.expert[g / gm], e, m, min(kWGroup, gu.tiles_m - m), n, lds);
+    weights_tiles<kB>(w.expert[g / gm], e, m, min(kWGroup, gu.tiles_m - m), n);
   } else {
     const int m = r / dn.tiles_n * kWGroup;
-    weights_tiles<kA>(dn, e, m, min(kWGroup, dn.tiles_m - m), r % dn.tiles_n, lds);
+    weights_tiles<kA>(dn, e, m, min(kWGroup, dn.tiles_m - m), r % dn.tiles_n);
   }
 }
 
@@ -833,7 +851,7 @@ static hipError_t start_rows(const RowsProblem& t, const RowsProblem& r, int64_t
   static std::atomic<uint32_t> configured{0};
   const hipError_t e = set_lds_limit_once((const void*)rows_kernel<F32>, kRowsLds, configured);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rows_kernel<F32>, dim3((unsigned)blocks), dim3(512), kRowsLds, stream, t, r,
+  hipLaunchKernelGGL(rows_kernel<F32>, dim3((unsigned)blocks), dim3(256), kRowsLds, stream, t, r,
                      token_blocks);
   return hipGetLastError();
 }
@@ -857,7 +875,7 @@ hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
   if (e != hipSuccess) return e;
   int64_t blocks = 0;
   auto set_tiles = [](WeightsProblem& q) {
-    q.tiles_m = (q.a_cols + WM - 1) / WM;
+    q.tiles_m = (q.a_cols + TM - 1) / TM;
     q.tiles_n = (q.b_cols + TN - 1) / TN;
   };
   for (int i = 0; i < w.n_dense; ++i) {
