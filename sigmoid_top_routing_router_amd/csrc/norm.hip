@@ -104,13 +104,27 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
          (__uint_as_float(readlane_u32(u, 32)) + __uint_as_float(readlane_u32(u, 48)));
 }
 
-// Sums of NS values over the TPR threads of a row.  `part` holds NS floats per
-// wave of the block; it is not written again before the next barrier.
+// Sums of NS values over the TPR threads of a row (0: all of the block's).
+// `part` holds NS floats per wave of the block; it is not written again before
+// the next barrier.
 template <int TPR, int NS>
 __device__ __forceinline__ void row_sums(float (&v)[NS], float* part) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) v[i] = wave_sum_f32(v[i]);
-  if constexpr (TPR > 64) {
+  if constexpr (TPR == 0) {
+    const int wave = threadIdx.x >> 6, W = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) part[wave * NS + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = 0.0f;
+    for (int w = 0; w < W; ++w) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) v[i] += part[w * NS + i];
+    }
+  } else if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -271,81 +285,74 @@ struct NormGradArgs {
   float* part_w;     // [blocks][d] partial sums of dw, then (POST) of dw_post
 };
 
-// Grid-stride over the rows; a thread keeps the sums of its own columns over
-// the block's rows, and every block leaves one partial row of them (its
+// Grid-stride over the rows; a thread keeps the sums of its own eight columns
+// over the block's rows, and every block leaves one partial row of them (its
 // rows' groups added in order through LDS), so the result does not depend on
-// the order in which blocks run.
-template <int TPR, int NV, int VEC, bool POST>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGradArgs a) {
-  constexpr int BT = TPR < 256 ? 256 : TPR;
-  constexpr int RPB = BT / TPR;
-  __shared__ float part[2][2][3 * (BT / 64)];
-  const int t = threadIdx.x % TPR;
-  const int sub = threadIdx.x / TPR;
+// the order in which blocks run.  A row belongs to one wave (WAVE, four rows
+// to a block of 256) or to the whole block, as many waves as its columns need;
+// everything it reads is asked for before the first sum: the passes over memory
+// bound it (16384 x 2560, fp32 stream, sandwich: 755 MB in 139 us, 5.4 TB/s; a
+// wave per row, forty columns a lane and two waves a SIMD, took 250 us).
+template <bool WAVE, int VEC, bool POST>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int NV = 8 / VEC;
+  constexpr int TPR = WAVE ? 64 : 0;
+  constexpr int RPB = WAVE ? 4 : 1;
+  __shared__ float part[2][2][2 * 16];
+  const int threads = WAVE ? 64 : blockDim.x;  // of a row
+  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int sub = WAVE ? threadIdx.x >> 6 : 0;
   const int d = a.d;
   const float inv_d = 1.0f / (float)d;
-  float dw[NV][VEC], dp[POST ? NV : 1][VEC];
+  float dw[NV][VEC], dp[NV][VEC], w[NV][VEC], pw[NV][VEC];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * threads + t) * VEC;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      dw[j][i] = 0.0f;
-      if (POST) dp[j][i] = 0.0f;
+    for (int i = 0; i < VEC; ++i) dw[j][i] = dp[j][i] = w[j][i] = pw[j][i] = 0.0f;
+    if (c < d) {
+      load_any<VEC>(a.w, c, a.weight_f32, w[j]);
+      if (POST) load_any<VEC>(a.post_w, c, a.weight_f32, pw[j]);
     }
+  }
   int flip = 0;
-  // a block of one row at a time (RPB = 1) has one loop count, for the barriers
+  // a block of one row at a time has one loop count, for the barriers
   for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.n;
        row += (int64_t)gridDim.x * RPB, flip ^= 1) {
     const int64_t base = row * d;
-    float r[NV][VEC], g[NV][VEC];
-    float s[2] = {0.0f, 0.0f};
+    float r[NV][VEC], g[NV][VEC], q[NV][VEC], xs[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
+      const int c = (j * threads + t) * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) r[j][i] = g[j][i] = q[j][i] = xs[j][i] = 0.0f;
       if (c < d) {
         load_any<VEC>(a.r, base + c, a.stream_f32, r[j]);
         load_bf16<VEC>(a.dy + base + c, g[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) r[j][i] = g[j][i] = 0.0f;
+        if (a.dres) load_any<VEC>(a.dres, base + c, a.stream_f32, q[j]);
+        if (POST) load_bf16<VEC>(a.x + base + c, xs[j]);
       }
     }
+    float s[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
-      float w[VEC];
-      if (c < d) {
-        load_any<VEC>(a.w, c, a.weight_f32, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = 0.0f;
-      }
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         s[0] += r[j][i] * r[j][i];
-        s[1] += g[j][i] * w[i] * r[j][i];
+        s[1] += g[j][i] * w[j][i] * r[j][i];
       }
-    }
     row_sums<TPR>(s, part[flip][0]);
     const float ra = rsqrtf(s[0] * inv_d + a.eps);
     const float k1 = ra * ra * ra * s[1] * inv_d;  // a n mean(h n) = r k1
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
+      const int c = (j * threads + t) * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        dw[j][i] += g[j][i] * (r[j][i] * ra);
+        r[j][i] = q[j][i] + (ra * (g[j][i] * w[j][i]) - r[j][i] * k1);  // dr from here on
+      }
       if (c < d) {
-        float w[VEC], q[VEC];
-        load_any<VEC>(a.w, c, a.weight_f32, w);
-        if (a.dres) {
-          load_any<VEC>(a.dres, base + c, a.stream_f32, q);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) q[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          dw[j][i] += g[j][i] * (r[j][i] * ra);
-          r[j][i] = q[i] + (ra * (g[j][i] * w[i]) - r[j][i] * k1);  // dr from here on
-        }
         if (a.dr_out) {
           if (a.stream_f32) store_f32<VEC>(reinterpret_cast<float*>(a.dr_out) + base + c, r[j]);
           else store_bf16<VEC>(reinterpret_cast<uint16_t*>(a.dr_out) + base + c, r[j]);
@@ -354,68 +361,55 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
       }
     }
     if constexpr (POST) {
-      float xs[NV][VEC];
       float p[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + t) * VEC;
-        if (c < d) {
-          float w[VEC];
-          load_bf16<VEC>(a.x + base + c, xs[j]);
-          load_any<VEC>(a.post_w, c, a.weight_f32, w);
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            p[0] += xs[j][i] * xs[j][i];
-            p[1] += r[j][i] * w[i] * xs[j][i];
-          }
+        for (int i = 0; i < VEC; ++i) {
+          p[0] += xs[j][i] * xs[j][i];
+          p[1] += r[j][i] * pw[j][i] * xs[j][i];
         }
-      }
       row_sums<TPR>(p, part[flip][1]);
       const float rb = rsqrtf(p[0] * inv_d + a.eps);
       const float k2 = rb * rb * rb * p[1] * inv_d;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + t) * VEC;
-        if (c < d) {
-          float w[VEC], o[VEC];
-          load_any<VEC>(a.post_w, c, a.weight_f32, w);
+        const int c = (j * threads + t) * VEC;
+        float o[VEC];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            dp[j][i] += r[j][i] * (xs[j][i] * rb);
-            o[i] = rb * (r[j][i] * w[i]) - xs[j][i] * k2;
-          }
-          if (a.dx) store_bf16<VEC>(a.dx + base + c, o);
+        for (int i = 0; i < VEC; ++i) {
+          dp[j][i] += r[j][i] * (xs[j][i] * rb);
+          o[i] = rb * (r[j][i] * pw[j][i]) - xs[j][i] * k2;
         }
+        if (c < d && a.dx) store_bf16<VEC>(a.dx + base + c, o);
       }
     }
   }
   // the block's partial row
   float* out = a.part_w + (int64_t)blockIdx.x * (POST ? 2 : 1) * d;
-  if constexpr (RPB == 1) {
+  if constexpr (!WAVE) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
+      const int c = (j * threads + t) * VEC;
       if (c < d) {
         store_f32<VEC>(out + c, dw[j]);
         if (POST) store_f32<VEC>(out + d + c, dp[j]);
       }
     }
   } else {
-    // four waves of one block: added in order, one column set at a time
-    __shared__ float red[RPB][TPR * VEC];
+    // the four waves' sums in order
+    __shared__ float red[RPB][512];
 #pragma unroll
     for (int q = 0; q < (POST ? 2 : 1); ++q) {
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        __syncthreads();
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) red[sub][t * VEC + i] = q ? dp[POST ? j : 0][i] : dw[j][i];
-        __syncthreads();
-        for (int k = threadIdx.x; k < TPR * VEC; k += BT) {
-          const int c = j * TPR * VEC + k;
-          if (c < d) out[q * d + c] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
-        }
-      }
+        for (int i = 0; i < VEC; ++i)
+          red[sub][(j * 64 + t) * VEC + i] = q ? dp[j][i] : dw[j][i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < d; c += 256)
+        out[q * d + c] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
     }
   }
 }
@@ -430,6 +424,7 @@ __global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict_
   const int c = blockIdx.x * 32 + cx;
   float s = 0.0f;
   if (c < cols)
+#pragma unroll 8
     for (int r = gy; r < rows; r += 32) s += part[(int64_t)r * cols + c];
   red[gy][cx] = s;
   __syncthreads();
@@ -441,6 +436,8 @@ __global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict_
     else if (out1) out1[c - d] = v;
   }
 }
+
+constexpr int kWaveD = 512;  // widest row of a wave in norm_grad_kernel
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -454,14 +451,14 @@ void start_norm(const NormArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((norm_kernel<TPR, NV, VEC, false>), dim3(blocks), dim3(BT), 0, stream, a);
 }
 
-template <int TPR, int NV, int VEC>
+template <bool WAVE, int VEC>
 void start_norm_grad(const NormGradArgs& a, int blocks, hipStream_t stream) {
-  constexpr int BT = TPR < 256 ? 256 : TPR;
+  const int threads = WAVE ? 256 : (a.d + 511) / 512 * 64;
   if (a.post_w)
-    hipLaunchKernelGGL((norm_grad_kernel<TPR, NV, VEC, true>), dim3((unsigned)blocks), dim3(BT), 0,
-                       stream, a);
+    hipLaunchKernelGGL((norm_grad_kernel<WAVE, VEC, true>), dim3((unsigned)blocks), dim3(threads),
+                       0, stream, a);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<TPR, NV, VEC, false>), dim3((unsigned)blocks), dim3(BT),
+    hipLaunchKernelGGL((norm_grad_kernel<WAVE, VEC, false>), dim3((unsigned)blocks), dim3(threads),
                        0, stream, a);
 }
 
@@ -497,10 +494,16 @@ hipError_t launch_rms_norm(const uint16_t* x, const void* residual, const void* 
   return hipGetLastError();
 }
 
+// Blocks, and so partial rows.  Rows of a block: some twelve waves a CU in a
+// whole number of blocks (16384 x 2560, sandwich, five waves a row: 138 us with
+// 512 blocks, 161 with 1024, 176 with 256), two rows each or more (256 x 2560:
+// 7 us, with four rows 10, with eight 16).  Rows of a wave: up to four blocks a
+// CU (65536 x 256: 27 us with 1024 blocks, 38 with 512, 28 with 2048).
 int rms_norm_grad_blocks(int64_t n, int d) {
-  // enough blocks for every CU; more rows per block, fewer partial rows
-  const int64_t most = d <= 2560 ? 1024 : 512;
-  const int64_t per = d <= 2560 ? 4 : 1;  // rows a block of waves takes at once
+  const bool wave = d <= kWaveD;
+  const int waves = (d + 511) / 512;
+  const int64_t most = 256 * (wave ? 4 : waves < 12 ? 12 / waves : 1);
+  const int64_t per = wave ? 4 : 2;
   const int64_t need = (n + per - 1) / per;
   return (int)(need < 1 ? 1 : need < most ? need : most);
 }
@@ -515,18 +518,11 @@ hipError_t launch_rms_norm_grad(const uint16_t* dy, const void* r, const uint16_
   const NormGradArgs a{dy, r, x, dres, w, post_w, n, d, eps, stream_f32, weight_f32, dx, dr_out, part};
   const bool vec = d % 8 == 0 && al16(dy) && al16(r) && al16(x) && al16(dres) && al16(w) &&
                    al16(post_w) && al16(dx) && al16(dr_out);
-  if (vec) {
-    if (d <= 512) start_norm_grad<64, 1, 8>(a, blocks, stream);
-    else if (d <= 1024) start_norm_grad<64, 2, 8>(a, blocks, stream);
-    else if (d <= 2048) start_norm_grad<64, 4, 8>(a, blocks, stream);
-    else if (d <= 2560) start_norm_grad<64, 5, 8>(a, blocks, stream);
-    else if (d <= 4096) start_norm_grad<256, 2, 8>(a, blocks, stream);
-    else start_norm_grad<256, 4, 8>(a, blocks, stream);
-  } else {
-    if (d <= 1024) start_norm_grad<64, 16, 1>(a, blocks, stream);
-    else if (d <= 4096) start_norm_grad<256, 16, 1>(a, blocks, stream);
-    else start_norm_grad<256, 32, 1>(a, blocks, stream);
-  }
+  const bool wave = d <= kWaveD;
+  if (vec && wave) start_norm_grad<true, 8>(a, blocks, stream);
+  else if (vec) start_norm_grad<false, 8>(a, blocks, stream);
+  else if (wave) start_norm_grad<true, 1>(a, blocks, stream);
+  else start_norm_grad<false, 1>(a, blocks, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (!dw && !dw_post) return hipSuccess;
