@@ -225,6 +225,7 @@ __global__ __launch_bounds__(64 * kCombWaves) void balance_combine_kernel(
     uint32_t c = 0u;
     if (lo < hi && e < E) {
       const int b0 = lo / R, b1 = (hi - 1) / R;
+#pragma unroll 8
       for (int b = b0 + w; b <= b1; b += kCombWaves) {
         const int64_t at = ((int64_t)b + g) * E + e;
         s += (double)sums[at];

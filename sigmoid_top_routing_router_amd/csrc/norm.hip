@@ -16,9 +16,12 @@
 // the forward pass keeps nothing for it.
 //
 // All statistics, sums and the row itself are fp32; a row is read once and
-// kept in registers.  TPR threads own a row (a wave or a block of 256), each
-// NV pieces of VEC consecutive columns: VEC = 8 (16-byte loads of bf16) when
-// the width is a multiple of 8 and every pointer 16-byte aligned, else VEC = 1.
+// kept in registers, eight columns a thread, so that all of a row's loads are
+// in flight at once: rows of up to 512 columns belong to one wave (WAVE; four
+// rows to a block of 256, no barrier), wider ones to a block of as many waves
+// as they need.  A thread's columns are consecutive (VEC = 8: 16-byte loads of
+// bf16) when the width is a multiple of 8 and every pointer 16-byte aligned,
+// else a row's threads apart (VEC = 1).
 #include "common.h"
 #include "kernels.h"
 
@@ -104,14 +107,13 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
          (__uint_as_float(readlane_u32(u, 32)) + __uint_as_float(readlane_u32(u, 48)));
 }
 
-// Sums of NS values over the TPR threads of a row (0: all of the block's).
-// `part` holds NS floats per wave of the block; it is not written again before
-// the next barrier.
-template <int TPR, int NS>
+// Sums of NS values over a row's wave, or the block's.  `part` holds NS floats
+// per wave of the block; it is not written again before the next barrier.
+template <bool WAVE, int NS>
 __device__ __forceinline__ void row_sums(float (&v)[NS], float* part) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) v[i] = wave_sum_f32(v[i]);
-  if constexpr (TPR == 0) {
+  if constexpr (!WAVE) {
     const int wave = threadIdx.x >> 6, W = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -124,22 +126,13 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float* part) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) v[i] += part[w * NS + i];
     }
-  } else if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) part[(threadIdx.x >> 6) * NS + i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) s += part[w * NS + i];
-      v[i] = s;
-    }
   }
 }
+
+constexpr int kWaveD = 512;  // widest row of one wave
+// Blocks along x of norm_kernel's grid: a grid's threads along x stay below
+// 2^32.
+constexpr int64_t kGridX = 1 << 20;
 
 constexpr float kE4M3Max = 448.0f;
 
@@ -158,26 +151,34 @@ struct NormArgs {
   float* scales;
 };
 
-template <int TPR, int NV, int VEC, bool POST>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
-  constexpr int BT = TPR < 256 ? 256 : TPR;
-  __shared__ float part[2][BT / 64];
-  const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * (BT / TPR) + threadIdx.x / TPR;
-  // a wave past the last row leaves whole (TPR = 64: no barrier below)
-  if (row >= a.n) return;
+// Bound by its passes over memory: 65536 x 2560, fp32 stream, sandwich, bf16
+// and E4M3 outputs, 2.18 GB in 427 us, 5.1 TB/s.  16384 x 2560, bf16 with an
+// fp32 stream: 87 us; with one wave a row (forty columns a lane) 104 us, and
+// 64 such rows 3.2 us against 5.8.  512 columns: a wave and a block of one
+// wave took the same.
+template <bool WAVE, int VEC, bool POST>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
+  constexpr int NV = 8 / VEC;
+  __shared__ float part[2][16];
+  const int threads = WAVE ? 64 : blockDim.x;  // of a row
+  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t block = (int64_t)blockIdx.y * kGridX + blockIdx.x;
+  const int64_t row = WAVE ? block * 4 + (threadIdx.x >> 6) : block;
+  if (row >= a.n) return;  // a whole wave (WAVE: no barrier below)
   const int d = a.d;
   const int64_t base = row * d;
   const float inv_d = 1.0f / (float)d;
-  float v[NV][VEC];
+  float v[NV][VEC], q[NV][VEC], w[NV][VEC], pw[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + t) * VEC;
+    const int c = (j * threads + t) * VEC;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[j][i] = q[j][i] = w[j][i] = pw[j][i] = 0.0f;
     if (c < d) {
       load_bf16<VEC>(a.x + base + c, v[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[j][i] = 0.0f;
+      if (a.residual) load_any<VEC>(a.residual, base + c, a.stream_f32, q[j]);
+      if (POST) load_any<VEC>(a.post_w, c, a.weight_f32, pw[j]);
+      load_any<VEC>(a.w, c, a.weight_f32, w[j]);
     }
   }
   if constexpr (POST) {
@@ -186,35 +187,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) ss[0] += v[j][i] * v[j][i];
-    row_sums<TPR>(ss, part[0]);
+    row_sums<WAVE>(ss, part[0]);
     const float b = rsqrtf(ss[0] * inv_d + a.eps);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
-      if (c < d) {
-        float w[VEC];
-        load_any<VEC>(a.post_w, c, a.weight_f32, w);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * b * w[i];
-      }
-    }
+      for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * b * pw[j][i];
   }
   if (a.residual) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
-      if (c < d) {
-        float q[VEC];
-        load_any<VEC>(a.residual, base + c, a.stream_f32, q);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[j][i] += q[i];
-      }
-    }
+      for (int i = 0; i < VEC; ++i) v[j][i] += q[j][i];
   }
   if (a.r_out) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + t) * VEC;
+      const int c = (j * threads + t) * VEC;
       if (c < d) {
         if (a.stream_f32) store_f32<VEC>(reinterpret_cast<float*>(a.r_out) + base + c, v[j]);
         else store_bf16<VEC>(reinterpret_cast<uint16_t*>(a.r_out) + base + c, v[j]);
@@ -226,18 +215,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) ss[0] += v[j][i] * v[j][i];
-  row_sums<TPR>(ss, part[1]);
+  row_sums<WAVE>(ss, part[1]);
   const float s = rsqrtf(ss[0] * inv_d + a.eps);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + t) * VEC;
-    if (c < d) {
-      float w[VEC];
-      load_any<VEC>(a.w, c, a.weight_f32, w);
+    const int c = (j * threads + t) * VEC;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * s * w[i];
-      if (a.y) store_bf16<VEC>(a.y + base + c, v[j]);
-    }
+    for (int i = 0; i < VEC; ++i) v[j][i] = v[j][i] * s * w[j][i];
+    if (c < d && a.y) store_bf16<VEC>(a.y + base + c, v[j]);
     if constexpr (VEC == 8) {
       // 16 neighbouring lanes hold one 1 x 128 group (d % 128 == 0 here), all
       // of them inside the row or none
@@ -296,7 +281,6 @@ struct NormGradArgs {
 template <bool WAVE, int VEC, bool POST>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
   constexpr int NV = 8 / VEC;
-  constexpr int TPR = WAVE ? 64 : 0;
   constexpr int RPB = WAVE ? 4 : 1;
   __shared__ float part[2][2][2 * 16];
   const int threads = WAVE ? 64 : blockDim.x;  // of a row
@@ -341,7 +325,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
         s[0] += r[j][i] * r[j][i];
         s[1] += g[j][i] * w[j][i] * r[j][i];
       }
-    row_sums<TPR>(s, part[flip][0]);
+    row_sums<WAVE>(s, part[flip][0]);
     const float ra = rsqrtf(s[0] * inv_d + a.eps);
     const float k1 = ra * ra * ra * s[1] * inv_d;  // a n mean(h n) = r k1
 #pragma unroll
@@ -369,7 +353,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
           p[0] += xs[j][i] * xs[j][i];
           p[1] += r[j][i] * pw[j][i] * xs[j][i];
         }
-      row_sums<TPR>(p, part[flip][1]);
+      row_sums<WAVE>(p, part[flip][1]);
       const float rb = rsqrtf(p[0] * inv_d + a.eps);
       const float k2 = rb * rb * rb * p[1] * inv_d;
 #pragma unroll
@@ -437,23 +421,25 @@ __global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict_
   }
 }
 
-constexpr int kWaveD = 512;  // widest row of a wave in norm_grad_kernel
-
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-template <int TPR, int NV, int VEC>
+int row_threads(int d) { return (d + 511) / 512 * 64; }
+
+template <bool WAVE, int VEC>
 void start_norm(const NormArgs& a, hipStream_t stream) {
-  constexpr int BT = TPR < 256 ? 256 : TPR;
-  const unsigned blocks = (unsigned)((a.n + BT / TPR - 1) / (BT / TPR));
+  const int64_t blocks = WAVE ? (a.n + 3) / 4 : a.n;
+  const dim3 grid((unsigned)(blocks < kGridX ? blocks : kGridX),
+                  (unsigned)((blocks + kGridX - 1) / kGridX));
+  const int threads = WAVE ? 256 : row_threads(a.d);
   if (a.post_w)
-    hipLaunchKernelGGL((norm_kernel<TPR, NV, VEC, true>), dim3(blocks), dim3(BT), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<WAVE, VEC, true>), grid, dim3(threads), 0, stream, a);
   else
-    hipLaunchKernelGGL((norm_kernel<TPR, NV, VEC, false>), dim3(blocks), dim3(BT), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<WAVE, VEC, false>), grid, dim3(threads), 0, stream, a);
 }
 
 template <bool WAVE, int VEC>
 void start_norm_grad(const NormGradArgs& a, int blocks, hipStream_t stream) {
-  const int threads = WAVE ? 256 : (a.d + 511) / 512 * 64;
+  const int threads = WAVE ? 256 : row_threads(a.d);
   if (a.post_w)
     hipLaunchKernelGGL((norm_grad_kernel<WAVE, VEC, true>), dim3((unsigned)blocks), dim3(threads),
                        0, stream, a);
@@ -475,22 +461,11 @@ hipError_t launch_rms_norm(const uint16_t* x, const void* residual, const void* 
                    al16(r_out) && al16(codes);
   // a 1 x 128 group is 16 lanes of 8 columns
   if (codes && (!vec || d % 128)) return hipErrorInvalidValue;
-  // Few rows: a block per row, so that a row's loads are in flight at once;
-  // many rows: a wave per row, no barrier.
-  const bool few = n < 2048;
-  if (vec) {
-    if (d <= 512 && !few) start_norm<64, 1, 8>(a, stream);
-    else if (d <= 1024 && !few) start_norm<64, 2, 8>(a, stream);
-    else if (d <= 2048 && !few) start_norm<64, 4, 8>(a, stream);
-    else if (d <= 2560 && !few) start_norm<64, 5, 8>(a, stream);
-    else if (d <= 2048) start_norm<256, 1, 8>(a, stream);
-    else if (d <= 4096) start_norm<256, 2, 8>(a, stream);
-    else start_norm<256, 4, 8>(a, stream);
-  } else {
-    if (d <= 1024) start_norm<64, 16, 1>(a, stream);
-    else if (d <= 4096) start_norm<256, 16, 1>(a, stream);
-    else start_norm<256, 32, 1>(a, stream);
-  }
+  const bool wave = d <= kWaveD;
+  if (vec && wave) start_norm<true, 8>(a, stream);
+  else if (vec) start_norm<false, 8>(a, stream);
+  else if (wave) start_norm<true, 1>(a, stream);
+  else start_norm<false, 1>(a, stream);
   return hipGetLastError();
 }
 

@@ -272,3 +272,18 @@ def test_streams_and_graph(M):
             assert bool((a == b).all()), rep
         M.rms_norm(s["x"], s["w"], EPS, s["res"], s["post"])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n,d", [(4 * 2 ** 20 + 3, 8), (2 ** 20 + 2, 520)])
+def test_more_rows_than_one_line_of_blocks(M, n, d):
+    """Row n - 1 belongs to a block behind 2^20 others, and its elements lie
+    past 2^25 (2^29) of them."""
+    import torch
+    torch.manual_seed(5)
+    x = torch.empty(n, d, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    y, _ = M.rms_norm(x, w, EPS)[:2]
+    for rows in (slice(0, 5), slice(2 ** 20 - 3, 2 ** 20 + 2), slice(n - 5, n)):
+        a = f64(x[rows])
+        ref = a / np.sqrt((a * a).mean(axis=1, keepdims=True) + EPS)
+        assert (np.abs(f64(y[rows]) - ref) <= (STAT + BF16) * np.abs(ref)).all()
