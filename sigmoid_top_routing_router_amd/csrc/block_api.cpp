@@ -107,8 +107,8 @@ struct GradLayout {
   int32_t *ids, *counts, *offsets, *sorted_src, *src_pos, *tiles, *n_tiles, *row_tiles, *n_row_tiles;
   uint32_t* tok;
   uint32_t* block_counts;
-  float *S, *Q, *Qs, *dscore;
-  uint16_t *hid, *dXp, *hids, *dzb, *base;
+  float *S, *Q, *Qs, *dscore, *dXp, *base;
+  uint16_t *hid, *hids, *dzb;
   int64_t ld, lds;  // row pitch of hid and of hids (the shared expert's)
   int64_t max_tiles, max_row_tiles;
   int ldb;
@@ -143,9 +143,7 @@ GradLayout carve_grad(void* ws, const moe_problem_t& p) {
   l.n_row_tiles = (int32_t*)take(16);
   l.tok = (uint32_t*)take(pairs * 4);
   // Q is read for the last time before the pairs' part of grad_x is written
-  void* q = take(pairs * (size_t)(p.h * 4 > p.d * 2 ? p.h * 4 : p.d * 2));
-  l.Q = (float*)q;
-  l.dXp = (uint16_t*)q;
+  l.Q = l.dXp = (float*)take(pairs * (size_t)(p.h > p.d ? p.h : p.d) * 4);
   l.ld = hidden_pitch(p.h);
   l.lds = hidden_pitch((int)hs);
   l.hid = (uint16_t*)take(pairs * l.ld * 2);
@@ -153,7 +151,7 @@ GradLayout carve_grad(void* ws, const moe_problem_t& p) {
   l.Qs = (float*)take(N * hs * 4);
   l.hids = (uint16_t*)take(hs ? N * l.lds * 2 : 0);
   l.dzb = (uint16_t*)take(N * (size_t)l.ldb * 2);
-  l.base = (uint16_t*)take(N * p.d * 2);
+  l.base = (float*)take(N * p.d * 4);
   l.bytes = off;
   return l;
 }
@@ -229,7 +227,7 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
       t.out = l.Qs;
       t.ldo = hs;
     }
-    MOE_TRY(moe::launch_rows(shared ? &t : nullptr, r, true, st), "hidden gradient");
+    MOE_TRY(moe::launch_rows(shared ? &t : nullptr, r, st), "hidden gradient");
   }
   // G, U again; dG, dU, s H and the score gradients
   MOE_TRY(moe::launch_gateup_grad(x, N, l.sorted_src, K, l.tiles, l.n_tiles, l.max_tiles, 0,
@@ -260,7 +258,7 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     t.ncols = d;
     t.out = l.base;
     t.ldo = d;
-    MOE_TRY(moe::launch_rows(t.n_seg ? &t : nullptr, r, false, st), "x gradient");
+    MOE_TRY(moe::launch_rows(t.n_seg ? &t : nullptr, r, st), "x gradient");
     MOE_TRY(moe::launch_sum_pairs(t.n_seg ? l.base : nullptr, l.dXp, l.src_pos, N, K, d, g.x, st),
             "x gradient sum");
   }

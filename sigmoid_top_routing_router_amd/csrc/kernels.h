@@ -224,10 +224,10 @@ hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int3
 // Gathered operands (x, dy) and the tiles' rows of direct ones are smaller
 // than this.
 constexpr uint32_t kGradMaxOperandBytes = 0xFFFE0000u;
-// C[row, n] = sum over the segments of sum_k A[row, k] B[k, n].  Pairs: rows
-// from the tile table (expert, first row, rows, offset); with an fp32 result
-// A's rows are gathered (gather[row]: byte offset; a_rows rows in all).
-// Tokens: rows 0 .. rows_dense - 1.
+// C[row, n] = sum over the segments of sum_k A[row, k] B[k, n] in fp32.  Pairs:
+// rows from the tile table (expert, first row, rows, offset); with gather A's
+// rows are at these byte offsets (gather[row]; a_rows rows in all).  Tokens:
+// rows 0 .. rows_dense - 1.
 struct RowsSegment {
   const uint16_t* A;
   int64_t lda;             // elements
@@ -244,14 +244,13 @@ struct RowsProblem {
   const int32_t* n_tiles;
   int64_t max_tiles;
   int64_t rows_dense;
-  int ncols;               // multiple of 8 (bf16 out) or 4
+  int ncols;               // multiple of 8
   int n_tiles_n;           // set by the launcher
-  void* out;               // fp32 or bf16
+  float* out;
   int64_t ldo;
 };
 int grad_tile_rows();      // rows of a tile in the table of launch_grouped_rows
-hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool out_f32,
-                       hipStream_t stream);
+hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, hipStream_t stream);
 // C[m, n] = sum_row A[row, m] B[row, n] in bf16, rows offsets[e] ..
 // offsets[e + 1] - 1 (dense: all rows_dense).  The expert problems are gate,
 // up (rows of B, x, at byte offset tok[row], of tok_rows rows) and down (A, dy).
@@ -286,7 +285,7 @@ hipError_t launch_logits_grad(const float* Z, const int32_t* ids, const int32_t*
                               const float* dscore_part, int parts, int64_t N, int E, int K,
                               const float* grad_in, float* grad_out, uint16_t* dzb, int ldb,
                               hipStream_t stream);
-hipError_t launch_sum_pairs(const uint16_t* base, const uint16_t* Y, const int32_t* src_pos,
+hipError_t launch_sum_pairs(const float* base, const float* Y, const int32_t* src_pos,
                             int64_t N, int K, int d, uint16_t* out, hipStream_t stream);
 
 // ---------------------------------------------------------------- FP8

@@ -266,8 +266,8 @@ __host__ __device__ __forceinline__ int64_t xcd_blocks(int64_t work) {
 }
 
 // ---------------------------------------------------------------- rows
-// PAIR: rows of the tile table, else tokens.  F32: the fp32 result (Q), whose
-// pairs gather their rows of A; else bf16 (parts of dx).
+// PAIR: rows of the tile table, else tokens.  The results are fp32: Q, and the
+// parts of dx, which are summed before they are rounded.
 //
 // The segments' stages are one stream.  Half-stage h (32 k) opens with a wait
 // for the wave's own loads of it and the barrier that shows them to all waves
@@ -275,9 +275,8 @@ __host__ __device__ __forceinline__ int64_t xcd_blocks(int64_t work) {
 // and, when h is the first half of stage j, A of stage j + 1.  Rows past the
 // tile repeat its last row and columns past the result column 0 (what they
 // give is not stored); k past a segment reads zeros of both.
-template <bool PAIR, bool F32>
+template <bool PAIR, bool GATHER>
 __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item) {
-  constexpr bool GATHER = PAIR && F32;
   const int64_t mt = item / p.n_tiles_n;
   const int n0 = (int)(item % p.n_tiles_n) * TN;
   int expert = 0, rows;
@@ -413,65 +412,59 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item) {
   wait_vmcnt<0>();  // nothing may still write the LDS when another block has it
   if (!live) return;
 
-  if constexpr (F32) {
-    // Thirty-two stores of 16 rows x 64 bytes: two register groups of four
-    // columns trade the rows of their 16 lanes.
-    const uint32_t pitch = (uint32_t)p.ldo * 4u;
-    const __amdgpu_buffer_rsrc_t out =
-        make_rsrc(reinterpret_cast<float*>(p.out) + row0 * p.ldo, (uint32_t)rows * pitch);
-    const int col = n0 + wp * 64 + 8 * ((lane >> 4) & 1) + 4 * (lane >> 5);
+  // Thirty-two stores of 8 rows x 128 bytes, as store_lines makes them: the
+  // four register groups of a block trade rows until eight lanes hold one
+  // row's 32 columns.  Q is read by the next launch; the parts of dx pass the
+  // caches (non-temporal).
+  const uint32_t pitch = (uint32_t)p.ldo * 4u;
+  const __amdgpu_buffer_rsrc_t out = make_rsrc(p.out + row0 * p.ldo, (uint32_t)rows * pitch);
+  const int col = n0 + wp * 64 + 16 * ((lane >> 3) & 1) + 8 * ((lane >> 4) & 1) + 4 * (lane >> 5);
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < 2; ++f) {
+    const int c = col + 32 * f;
+    const uint32_t at = c < p.ncols ? (uint32_t)(lane & 7) * pitch + (uint32_t)c * 4u : kNoStore;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = col + 32 * f + 16 * u;
-        const uint32_t at = c < p.ncols ? (uint32_t)(lane & 15) * pitch + (uint32_t)c * 4u : kNoStore;
+    for (int m = 0; m < 4; ++m) {
+      uint32_t v[4][4];  // rows 0, 16, 8, 24 .. + 7 of the block after the trades
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          uint32_t v[2][4];
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[0][j] = __float_as_uint(acc[m][f][8 * u + j]);
-            v[1][j] = __float_as_uint(acc[m][f][8 * u + 4 + j]);
-            swap_rows16(v[0][j], v[1][j]);
-          }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const i32x4_t w = {(int)v[g][0], (int)v[g][1], (int)v[g][2], (int)v[g][3]};
-            __builtin_amdgcn_raw_buffer_store_b128(w, out, (int)(at + (uint32_t)(32 * m + 16 * g) * pitch),
-                                                   0, 0);
-          }
-        }
+        for (int q = 0; q < 4; ++q) v[q][j] = __float_as_uint(acc[m][f][4 * q + j]);
+        swap_rows16(v[0][j], v[1][j]);
+        swap_rows16(v[2][j], v[3][j]);
+        swap_rows8(v[0][j], v[2][j]);
+        swap_rows8(v[1][j], v[3][j]);
       }
-  } else {
-    const uint32_t pitch = (uint32_t)p.ldo * 2u;
-    const __amdgpu_buffer_rsrc_t out =
-        make_rsrc(reinterpret_cast<uint16_t*>(p.out) + row0 * p.ldo, (uint32_t)rows * pitch);
-    const int col = n0 + wp * 64 + line_col(lane);
-    store_lines<0>(acc, out,
-                   col < p.ncols ? (uint32_t)line_row(lane) * pitch + (uint32_t)col * 2u : kNoStore,
-                   pitch);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const i32x4_t w = {(int)v[q][0], (int)v[q][1], (int)v[q][2], (int)v[q][3]};
+        const int row = 32 * m + 16 * (q & 1) + 8 * (q >> 1);
+        __builtin_amdgcn_raw_buffer_store_b128(w, out, (int)(at + (uint32_t)row * pitch), 0,
+                                               GATHER ? 0 : kCpolNT);
+      }
+    }
   }
 }
 
 // The work item of block b of a problem's share of the grid.
-template <bool PAIR, bool F32>
+template <bool PAIR, bool GATHER>
 __device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b) {
   const int64_t m_tiles = PAIR ? (int64_t)*p.n_tiles : (p.rows_dense + TM - 1) / TM;
   const int64_t work = m_tiles * p.n_tiles_n;
   const int64_t share = (work + kXcds - 1) / kXcds;
   if (b / kXcds >= share) return;
   const int64_t item = xcd_item(b, share);
-  if (item < work) rows_tile<PAIR, F32>(p, item);
+  if (item < work) rows_tile<PAIR, GATHER>(p, item);
 }
 
 // The tokens' blocks first (fewer items), then the pairs'.
-template <bool F32>
+// GATHER: the pairs' rows of A come from p.gather.
+template <bool GATHER>
 __global__ __launch_bounds__(256, 2) void rows_kernel(RowsProblem token, RowsProblem pair,
                                                       int64_t token_blocks) {
   const int64_t b = blockIdx.x;
-  if (b < token_blocks) rows_block<false, F32>(token, b);
-  else rows_block<true, F32>(pair, b - token_blocks);
+  if (b < token_blocks) rows_block<false, false>(token, b);
+  else rows_block<true, GATHER>(pair, b - token_blocks);
 }
 
 // ---------------------------------------------------------------- weights
@@ -782,42 +775,33 @@ __global__ __launch_bounds__(256) void logits_grad_kernel(
   }
 }
 
-// dx[t] = base[t] + sum_k Y[src_pos[t, k]] in fp32, slot order, 8 columns a
-// thread (base NULL: zero).
+// dx[t] = base[t] + sum_k Y[src_pos[t, k]], slot order, 4 columns a thread
+// (base NULL: zero), rounded once.
 template <int K>
-__global__ __launch_bounds__(256) void sum_pairs_kernel(const uint16_t* __restrict__ base,
-                                                        const uint16_t* __restrict__ Y,
+__global__ __launch_bounds__(256) void sum_pairs_kernel(const float* __restrict__ base,
+                                                        const float* __restrict__ Y,
                                                         const int32_t* __restrict__ src_pos,
                                                         int64_t N, int d,
                                                         uint16_t* __restrict__ out) {
-  typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-  const int cpr = d / 8;
+  typedef float f32x4_t __attribute__((ext_vector_type(4)));
+  const int cpr = d / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= N * cpr) return;
   const int64_t t = i / cpr;
-  const int c = (int)(i % cpr) * 8;
-  u32x4_t v[K + 1];
+  const int c = (int)(i % cpr) * 4;
+  f32x4_t v[K + 1];
 #pragma unroll
   for (int k = 0; k < K; ++k)
     v[k] = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4_t*>(Y + (int64_t)src_pos[t * K + k] * d + c));
-  v[K] = base ? *reinterpret_cast<const u32x4_t*>(base + t * d + c) : u32x4_t{0u, 0u, 0u, 0u};
-  float s[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    s[2 * j] = __uint_as_float(v[K][j] << 16);
-    s[2 * j + 1] = __uint_as_float(v[K][j] & 0xFFFF0000u);
-  }
+        reinterpret_cast<const f32x4_t*>(Y + (int64_t)src_pos[t * K + k] * d + c));
+  v[K] = base ? __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(base + t * d + c))
+              : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      s[2 * j] += __uint_as_float(v[k][j] << 16);
-      s[2 * j + 1] += __uint_as_float(v[k][j] & 0xFFFF0000u);
-    }
-  const u32x4_t o = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]),
-                     pack_bf16(s[6], s[7])};
-  *reinterpret_cast<u32x4_t*>(out + t * d + c) = o;
+    for (int j = 0; j < 4; ++j) v[K][j] += v[k][j];
+  *reinterpret_cast<uint2*>(out + t * d + c) =
+      make_uint2(pack_bf16(v[K][0], v[K][1]), pack_bf16(v[K][2], v[K][3]));
 }
 
 }  // namespace
@@ -845,19 +829,18 @@ static int64_t rows_blocks(const RowsProblem& p) {
   return xcd_blocks(m_tiles * p.n_tiles_n);
 }
 
-template <bool F32>
+template <bool GATHER>
 static hipError_t start_rows(const RowsProblem& t, const RowsProblem& r, int64_t token_blocks,
                              int64_t blocks, hipStream_t stream) {
   static std::atomic<uint32_t> configured{0};
-  const hipError_t e = set_lds_limit_once((const void*)rows_kernel<F32>, kRowsLds, configured);
+  const hipError_t e = set_lds_limit_once((const void*)rows_kernel<GATHER>, kRowsLds, configured);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rows_kernel<F32>, dim3((unsigned)blocks), dim3(256), kRowsLds, stream, t, r,
+  hipLaunchKernelGGL(rows_kernel<GATHER>, dim3((unsigned)blocks), dim3(256), kRowsLds, stream, t, r,
                      token_blocks);
   return hipGetLastError();
 }
 
-hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool out_f32,
-                       hipStream_t stream) {
+hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, hipStream_t stream) {
   RowsProblem t{}, r = pair;
   if (token) t = *token;
   t.n_tiles_n = (t.ncols + TN - 1) / TN;
@@ -865,8 +848,8 @@ hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, bool o
   const int64_t tb = token ? rows_blocks(t) : 0;
   const int64_t blocks = tb + rows_blocks(r);
   if (blocks > 0x7FFFFFF0LL) return hipErrorInvalidConfiguration;
-  return out_f32 ? start_rows<true>(t, r, tb, blocks, stream)
-                 : start_rows<false>(t, r, tb, blocks, stream);
+  return r.gather ? start_rows<true>(t, r, tb, blocks, stream)
+                  : start_rows<false>(t, r, tb, blocks, stream);
 }
 
 hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
@@ -899,9 +882,9 @@ hipError_t launch_logits_grad(const float* Z, const int32_t* ids, const int32_t*
   return hipGetLastError();
 }
 
-hipError_t launch_sum_pairs(const uint16_t* base, const uint16_t* Y, const int32_t* src_pos,
+hipError_t launch_sum_pairs(const float* base, const float* Y, const int32_t* src_pos,
                             int64_t N, int K, int d, uint16_t* out, hipStream_t stream) {
-  const dim3 grid((unsigned)((N * (d / 8) + 255) / 256));
+  const dim3 grid((unsigned)((N * (d / 4) + 255) / 256));
 #define MOE_K(n)                                                                              \
   case n:                                                                                     \
     hipLaunchKernelGGL(sum_pairs_kernel<n>, grid, dim3(256), 0, stream, base, Y, src_pos, N,  \
