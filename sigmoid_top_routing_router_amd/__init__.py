@@ -531,6 +531,7 @@ def forward_fp8(x, weights: Fp8ExpertWeights, K: int, beta_in=None,
     if x_quant is not None:
         _dev(x_quant[0], "x_quant codes", u8, (N, d))
         _dev(x_quant[1], "x_quant scales", f32, (N, d // 128))
+        _one_device(x, codes=x_quant[0], scales=x_quant[1])
     wg = _dev(weights.w_gate, "w_gate", u8)
     if weights.packed:
         if wg.dim() != 4 or wg.shape[1] * 128 != d or wg.shape[3] != 128:
