@@ -434,7 +434,7 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  * y leaves in bf16 and / or as E4M3 codes with one fp32 scale per 1 x 128
  * group, by the rule of moe_fp8_quantize_rows applied to the fp32 y (not to
  * its bf16 rounding): the x and the codes that moe_forward_fp8_quantized
- * takes.  r is rounded once, to the stream's type; y is formed from the
+ * takes.  A group with a NaN has a NaN scale.  r is rounded once, to the stream's type; y is formed from the
  * unrounded r.
  *
  *  x            [n,d] bf16 bits.
@@ -446,7 +446,7 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *               itself.
  *  codes        [n,d] out or NULL, scales [n,d/128] out (both or neither):
  *               d % 128 == 0 and every buffer except scales 16-byte aligned.
- * At least one output.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
+ * At least one output, no two the same.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
  * row of zeros with eps = 0 has no norm).  bf16 buffers 2-byte, fp32 buffers
  * 4-byte aligned; 16-byte aligned buffers and d % 8 == 0 take the fast path.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
@@ -471,7 +471,7 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *               post_weight only).  n = 0 gives zeros.
  *  workspace    moe_rms_norm_backward_workspace_bytes(n, d) bytes, 256-byte
  *               aligned; 0 from the query means n or d out of range.
- * No output may alias an input.
+ * No output may alias an input or another output.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, WORKSPACE_TOO_SMALL, HIP.
  */
 #define MOE_NORM_STREAM_F32 0x1u  /* residual, residual_out, r and their gradients are fp32 */
@@ -564,8 +564,8 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  *   grad W_r = grad_logits_out^T x,
  * the shared expert with s = 1.  Q, G, U, H and the score gradients are fp32;
  * dG, dU, s H and, for the router's two products, grad_logits_out are rounded
- * to bf16 as matrix operands, a pair's part of grad_x once more; every sum is
- * fp32, every gradient but the logits' leaves in bf16.
+ * to bf16 as matrix operands; every sum is fp32, every gradient but the
+ * logits' leaves in bf16.
  *
  *  p            problem; sizes as moe_forward, and N*d*2 bytes and N*K*h*2
  *               bytes each at most 4 GiB - 128 KiB.  The routing flags are not

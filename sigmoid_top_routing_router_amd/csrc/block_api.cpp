@@ -1,6 +1,7 @@
 // C ABI of the operators around the layer (the residual norm and the balance
-// loss, forward and backward) and of the layer's backward pass.  Argument checks, workspace carving and the
-// launches on the caller's stream; nothing else.
+// loss, forward and backward) and of the layer's backward pass.  Argument
+// checks, workspace carving and the launches on the caller's stream; nothing
+// else.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -58,6 +59,14 @@ moe_status_t check_aligned(const void* const* p, int count, size_t a, const char
   for (int i = 0; i < count; ++i)
     if (p[i] && !aligned(p[i], a))
       return fail(MOE_ERR_INVALID_ARGUMENT, "%s must be %zu-byte aligned", what, a);
+  return MOE_OK;
+}
+
+moe_status_t check_distinct(const void* const* out, int count) {
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < i; ++j)
+      if (out[i] && out[i] == out[j])
+        return fail(MOE_ERR_INVALID_ARGUMENT, "two outputs are the same buffer");
   return MOE_OK;
 }
 
@@ -337,6 +346,7 @@ moe_status_t moe_backward(const moe_problem_t* p, const moe_weights_t* w, const 
       if (i && i == o) return fail(MOE_ERR_INVALID_ARGUMENT, "a gradient aliases an input");
   const GradLayout need = carve_grad(nullptr, *p);
   if ((s = check_workspace(workspace, workspace_bytes, need.bytes)) != MOE_OK) return s;
+  if ((s = check_distinct(out, 8)) != MOE_OK) return s;
   return backward_launches(*p, *w, x, grad_y, logits, topk_ids, grad_logits, *g,
                            carve_grad(workspace, *p), (hipStream_t)stream);
 }
@@ -374,6 +384,7 @@ moe_status_t moe_rms_norm(const uint16_t* x, const void* residual, const void* p
     for (int j = 0; j < 4; ++j)
       if (in[i] && in[i] == out[j] && !(in[i] == residual && out[j] == residual_out))
         return fail(MOE_ERR_INVALID_ARGUMENT, "an output aliases an input");
+  if ((s = check_distinct(out, 4)) != MOE_OK) return s;
   return done(moe::launch_rms_norm(x, residual, post_weight, weight, n, d, eps, sf, wf, y,
                                    residual_out, codes, scales, (hipStream_t)stream),
               "moe_rms_norm");
@@ -414,6 +425,7 @@ moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const 
   for (const void* i : in)
     for (const void* o : out)
       if (i && i == o) return fail(MOE_ERR_INVALID_ARGUMENT, "an output aliases an input");
+  if ((s = check_distinct(out, 4)) != MOE_OK) return s;
   s = check_workspace(workspace, workspace_bytes, moe_rms_norm_backward_workspace_bytes(n, d));
   if (s != MOE_OK) return s;
   return done(moe::launch_rms_norm_grad(grad_y, r, x, grad_residual, weight, post_weight, n, d,

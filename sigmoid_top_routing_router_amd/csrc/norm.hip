@@ -227,10 +227,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
       // 16 neighbouring lanes hold one 1 x 128 group (d % 128 == 0 here), all
       // of them inside the row or none
       if (a.codes) {
-        float m = 0.0f;
+        // as integers the magnitudes keep their order and a NaN comes last, so
+        // that a group with a NaN gets a NaN scale and not the others' codes
+        uint32_t mb = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
-        m = row16_max_f32(m);
+        for (int i = 0; i < 8; ++i) mb = max(mb, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+        const float m = __uint_as_float(row16_max_u32(mb));
         const float sc = m / kE4M3Max;
         u32x2_t q = {0u, 0u};
         if (m != 0.0f) {

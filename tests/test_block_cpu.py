@@ -275,3 +275,17 @@ def test_layer_gradient_formula():
         assert np.abs(got - _differences(value, t[name], 1e-5)).max() < 1e-6, name
         if key != "x":  # the sizes bound the sums
             assert np.all(np.abs(out[key]) <= mag[key] + 1e-12)
+
+
+@built
+def test_outputs_that_are_one_buffer(lib, mem):
+    """Two outputs in one buffer are refused before any HIP call."""
+    assert lib.moe_rms_norm(mem, mem + 4096, None, mem + 8192, 4, 128, 1e-6, 0, mem + 12288,
+                            mem + 12288, None, None, None) == 1
+    need = lib.moe_rms_norm_backward_workspace_bytes(4, 128)
+    assert lib.moe_rms_norm_backward(mem, mem + 4096, mem + 20480, None, mem + 8192, mem + 24576,
+                                     4, 128, 1e-6, 0, mem + 12288, mem + 12288, None, None,
+                                     mem + 65536, need, None) == 1
+    assert lib.moe_rms_norm_backward(mem, mem + 4096, mem + 20480, None, mem + 8192, mem + 24576,
+                                     4, 128, 1e-6, 0, None, None, mem + 12288, mem + 12288,
+                                     mem + 65536, need, None) == 1

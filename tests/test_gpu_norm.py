@@ -287,3 +287,18 @@ def test_more_rows_than_one_line_of_blocks(M, n, d):
         a = f64(x[rows])
         ref = a / np.sqrt((a * a).mean(axis=1, keepdims=True) + EPS)
         assert (np.abs(f64(y[rows]) - ref) <= (STAT + BF16) * np.abs(ref)).all()
+
+
+def test_nan_rows_show_in_the_codes(M):
+    """A NaN in a row makes the row's y NaN; its codes carry it in their scale,
+    and the rows beside it stay as they were."""
+    import torch
+    say("rms_norm, NaN rows")
+    s = make(12, 6, 512, "f32", False, "bf16")
+    y0, _, (c0, s0) = M.rms_norm(s["x"], s["w"], EPS, s["res"], quantize=True)
+    s["res"][2, 300] = float("nan")
+    y1, _, (c1, s1) = M.rms_norm(s["x"], s["w"], EPS, s["res"], quantize=True)
+    keep = [0, 1, 3, 4, 5]
+    assert bool(y1[2].isnan().all()) and bool(s1[2].isnan().all())
+    assert torch.equal(y0[keep], y1[keep]) and torch.equal(c0[keep], c1[keep])
+    assert torch.equal(s0[keep], s1[keep])
