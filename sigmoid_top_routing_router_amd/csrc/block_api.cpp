@@ -123,9 +123,8 @@ struct GradLayout {
   int ldb;
   size_t bytes;
 };
-// Rows of dG | dU | s H: an odd number of 128-byte lines, so that the same
-// columns of neighbouring rows lie in different channels of the cache.
-int64_t hidden_pitch(int h) { return ((3 * (int64_t)h + 63) / 64 | 1) * 64; }
+// Rows of dG | dU | s H in whole 128-byte lines.
+int64_t hidden_pitch(int h) { return (3 * (int64_t)h + 63) / 64 * 64; }
 GradLayout carve_grad(void* ws, const moe_problem_t& p) {
   char* const base = (char*)ws;
   size_t off = 0;
