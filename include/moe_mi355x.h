@@ -575,7 +575,8 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  *  x, grad_y    [N,d] bf16 bits.
  *  logits       [N,E] fp32, as the forward call used them (aux.logits).
  *  topk_ids     [N,K] int32 (aux.topk_ids).  A pair whose id lies outside
- *               [0,E) contributes nothing.
+ *               [0,E) contributes nothing, whatever its rows of x, grad_y and
+ *               logits hold (the shared expert and the router read every row).
  *  grad_logits  [N,E] fp32 or NULL (zero): the logits' gradient from
  *               elsewhere (moe_lei_backward, moe_balance_loss_backward).
  *  g            the gradients, all required: x [N,d] bf16, logits [N,E] fp32

@@ -202,7 +202,7 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   pw.n_tiles = l.n_tiles;
   MOE_TRY(moe::launch_permute(l.ids, N, E, K, moe::gemm_bm(), moe::gemm_xrows(), pw, st),
           "grouping");
-  MOE_TRY(moe::launch_grouped_rows(l.sorted_src, pairs, K, (uint32_t)d * 2u, l.offsets, E, l.tok,
+  MOE_TRY(moe::launch_grouped_rows(l.sorted_src, l.S, pairs, K, (uint32_t)d * 2u, l.offsets, E, l.tok,
                                    l.row_tiles, l.n_row_tiles, st),
           "grouped rows");
 

@@ -70,7 +70,7 @@ struct GemmArgs {
   int64_t shared_row0;
   // Backward gate/up only (kGateUpGrad), rows as the output rows of gate/up:
   const float* q_in;       // Q = dy W_d [rows][h] fp32
-  const float* row_scale;  // s of pair sorted_src[row], or NULL (1)
+  const float* row_scale;  // s of pair sorted_src[row] (< 0: dropped), or NULL (1)
   uint16_t* hid_out;       // [rows][hid_ld]: dG, dU, s H, h columns each
   int64_t hid_ld;
   float* dscore_part;      // [rows][n_tiles_n]: Q . H over the tile's columns, or NULL

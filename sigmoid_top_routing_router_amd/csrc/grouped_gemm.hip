@@ -356,7 +356,8 @@ __device__ __forceinline__ void router_tile_select(const GemmArgs& a, int nt, in
 
 // Epilogue of the backward gate/up tile ("Kolibri 1 im Detail", SwiGLU
 // paragraph, differentiated): with G and U of a row in the accumulators,
-// Q = dy W_d from memory and the row's weight s, sg = sigma(G),
+// Q = dy W_d from memory and the row's weight s (below 0: a dropped row, all
+// zeros whatever G and U are), sg = sigma(G),
 //   H = G sg U,  dU = s Q G sg,  dG = s Q U sg (1 + G (1 - sg)),
 // and the row's score gradient Q . H over the tile's columns, added over the
 // four column quarters in order.  dG, dU and s H leave in bf16 (they are the
@@ -386,7 +387,9 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& a, floatx16_t (&ac
     float part = 0.0f;
     if (rr < rows && cols) {
       const int64_t orow = row0 + rr;
-      const float s = a.row_scale ? a.row_scale[a.gather[orow]] : 1.0f;
+      const float weight = a.row_scale ? a.row_scale[a.gather[orow]] : 1.0f;
+      const bool drop = weight < 0.0f;  // Q is zero there already
+      const float s = drop ? 0.0f : weight;
       const float* q = a.q_in + orow * h + col0 + ocol_l;
       uint16_t* dg = a.hid_out + orow * a.hid_ld + col0 + ocol_l;
 #pragma unroll
@@ -396,7 +399,7 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& a, floatx16_t (&ac
         float o0[4], o1[4], o2[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float g = g_of(4 * k + j), u = u_of(4 * k + j);
+          const float g = drop ? 0.0f : g_of(4 * k + j), u = drop ? 0.0f : u_of(4 * k + j);
           const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
           const float gs = g * sg;
           const float hv = gs * u;

@@ -278,9 +278,9 @@ struct WeightsLaunch {
 hipError_t launch_weights(WeightsLaunch w, hipStream_t stream);
 hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E, int K,
                         int32_t* ids_out, float* S, hipStream_t stream);
-hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K, uint32_t pitch,
-                               const int32_t* offsets, int E, uint32_t* tok, int32_t* tiles,
-                               int32_t* n_tiles, hipStream_t stream);
+hipError_t launch_grouped_rows(const int32_t* sorted_src, const float* S, int64_t pairs, int K,
+                               uint32_t pitch, const int32_t* offsets, int E, uint32_t* tok,
+                               int32_t* tiles, int32_t* n_tiles, hipStream_t stream);
 hipError_t launch_logits_grad(const float* Z, const int32_t* ids, const int32_t* src_pos,
                               const float* dscore_part, int parts, int64_t N, int E, int K,
                               const float* grad_in, float* grad_out, uint16_t* dzb, int ldb,

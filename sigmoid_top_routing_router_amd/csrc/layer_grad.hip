@@ -693,7 +693,10 @@ __global__ __launch_bounds__(256, 2) void weights_kernel(WeightsLaunch w) {
 
 // ---------------------------------------------------------------- small kernels
 // One thread per pair: the id kept inside [0, E), and the pair's weight
-// sigma(z), 0 for an id outside the range (such a pair has no gradient).
+// sigma(z), -1 for an id outside the range: such a pair is dropped.  It stays
+// a row of expert 0's segment, all zeros whatever its token holds: x and dy
+// are gathered from no address, and the epilogue of G and U puts zeros in
+// their place.
 __global__ __launch_bounds__(256) void pairs_kernel(const int32_t* __restrict__ ids,
                                                     const float* __restrict__ Z, int64_t pairs,
                                                     int E, int K, int32_t* __restrict__ ids_out,
@@ -703,19 +706,22 @@ __global__ __launch_bounds__(256) void pairs_kernel(const int32_t* __restrict__ 
   const uint32_t e = (uint32_t)ids[p];
   const bool in = e < (uint32_t)E;
   ids_out[p] = in ? (int32_t)e : 0;
-  S[p] = in ? sigmoid_weight(Z[p / K * E + e]) : 0.0f;
+  S[p] = in ? sigmoid_weight(Z[p / K * E + e]) : -1.0f;
 }
 
 // Of the grouped pairs: the byte offset of every row's token in x (pitch bytes
-// a token; the same in dy); block 0 also makes the m-tiles of
-// rows_kernel from the segment offsets (thread e counts its expert's tiles, a
-// scan places them).
+// a token; the same in dy), kNoAddr for a dropped pair; block 0 also makes the
+// m-tiles of rows_kernel from the segment offsets (thread e counts its
+// expert's tiles, a scan places them).
 __global__ __launch_bounds__(512) void grouped_rows_kernel(
-    const int32_t* __restrict__ sorted_src, int64_t pairs, int K, uint32_t pitch,
-    const int32_t* __restrict__ offsets, int E, uint32_t* __restrict__ tok,
+    const int32_t* __restrict__ sorted_src, const float* __restrict__ S, int64_t pairs, int K,
+    uint32_t pitch, const int32_t* __restrict__ offsets, int E, uint32_t* __restrict__ tok,
     int32_t* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
   const int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x;
-  if (i < pairs) tok[i] = (uint32_t)(sorted_src[i] / K) * pitch;
+  if (i < pairs) {
+    const int32_t p = sorted_src[i];
+    tok[i] = S[p] < 0.0f ? kNoAddr : (uint32_t)(p / K) * pitch;
+  }
   if (blockIdx.x != 0) return;
   __shared__ uint32_t wsum[8];
   const int e = threadIdx.x, w = e >> 6;
@@ -814,11 +820,11 @@ hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_rows(const int32_t* sorted_src, int64_t pairs, int K, uint32_t pitch,
-                               const int32_t* offsets, int E, uint32_t* tok, int32_t* tiles,
-                               int32_t* n_tiles, hipStream_t stream) {
+hipError_t launch_grouped_rows(const int32_t* sorted_src, const float* S, int64_t pairs, int K,
+                               uint32_t pitch, const int32_t* offsets, int E, uint32_t* tok,
+                               int32_t* tiles, int32_t* n_tiles, hipStream_t stream) {
   hipLaunchKernelGGL(grouped_rows_kernel, dim3((unsigned)((pairs + 511) / 512)), dim3(512), 0,
-                     stream, sorted_src, pairs, K, pitch, offsets, E, tok, tiles, n_tiles);
+                     stream, sorted_src, S, pairs, K, pitch, offsets, E, tok, tiles, n_tiles);
   return hipGetLastError();
 }
 

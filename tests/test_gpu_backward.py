@@ -159,6 +159,31 @@ def test_ids_outside_and_twice(M):
     check(L, Z, ids, run(M, L, Z, ids))
 
 
+def test_padded_rows_that_hold_nan(M):
+    """Rows with no expert, NaN and infinities in their x, dy and logits, at the
+    start, inside and at the end: the other gradients are the bits of the
+    batch with zeros there, and theirs are zeros."""
+    import torch
+    L, Z, ids = make(25, 300, 128, 6, 2, 96, 0, router=False)
+    pad = np.r_[0:9, 100:140, 290:300]
+    ids[pad] = -1
+    for k in ("x", "dy"):
+        L[k][pad] = 0
+    Z[pad] = 0
+    say("backward, padded rows")
+    want = run(M, L, Z, ids)
+    check(L, Z, ids, want)
+    for k in ("x", "dy"):
+        L[k][pad] = 0x7FC0                               # NaN
+        L[k][pad[::3]] = 0x7F80                          # inf
+    Z[pad] = np.nan
+    got = run(M, L, Z, ids)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not got[0][torch.from_numpy(pad).cuda()].any()
+    for k in ("w_gate", "w_up", "w_down"):
+        assert torch.equal(getattr(got[2], k), getattr(want[2], k)), k
+
+
 def test_agrees_with_the_forward_pass(M):
     """Differences of the layer's own output: dy . (y(x + v) - y(x - v)) / 2 for
     a direction v, with the selection held by a bias.  y leaves in bf16, so the
