@@ -238,13 +238,13 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
     MOE_TRY(moe::launch_rows(shared ? &t : nullptr, r, st), "hidden gradient");
   }
   // G, U again; dG, dU, s H and the score gradients
-  MOE_TRY(moe::launch_gateup_grad(x, N, l.sorted_src, K, l.tiles, l.n_tiles, l.max_tiles, 0,
-                                  w.w_gate, w.w_up, d, h, l.Q, l.S, l.hid, l.ld, l.dscore, st),
-          "gate/up gradient");
-  if (shared)
-    MOE_TRY(moe::launch_gateup_grad(x, N, nullptr, 1, nullptr, nullptr, 0, N, w.ws_gate, w.ws_up,
-                                    d, hs, l.Qs, nullptr, l.hids, l.lds, nullptr, st),
-            "shared gate/up gradient");
+  {
+    const moe::GateUpGrad r{w.w_gate, w.w_up, h, l.Q, l.hid, l.ld};
+    const moe::GateUpGrad t{w.ws_gate, w.ws_up, hs, l.Qs, l.hids, l.lds};
+    MOE_TRY(moe::launch_gateup_grad(x, N, l.sorted_src, K, l.tiles, l.n_tiles, l.max_tiles, d, l.S,
+                                    l.dscore, r, shared ? &t : nullptr, st),
+            "gate/up gradient");
+  }
   MOE_TRY(moe::launch_logits_grad(Z, ids, l.src_pos, l.dscore, moe::gateup_col_tiles(h), N, E, K,
                                   grad_logits, g.logits, router ? l.dzb : nullptr, l.ldb, st),
           "logits gradient");

@@ -95,12 +95,15 @@ __device__ __forceinline__ uint16_t f32_to_bf16_u16(float v) {
 // Logical tile of this block: workgroups are dealt round-robin to the XCDs,
 // so block b takes tile (b % 8) * share + b / 8 and each XCD walks a
 // contiguous run.  Returns false for surplus blocks.
-__device__ __forceinline__ bool xcd_tile(int64_t work, int64_t& logical) {
+__device__ __forceinline__ bool xcd_tile(int64_t block, int64_t work, int64_t& logical) {
   const int64_t share = (work + kXcd - 1) / kXcd;
-  const int64_t local = blockIdx.x / kXcd;
+  const int64_t local = block / kXcd;
   if (local >= share) return false;
-  logical = (int64_t)(blockIdx.x % kXcd) * share + local;
+  logical = block % kXcd * share + local;
   return logical < work;
+}
+__device__ __forceinline__ bool xcd_tile(int64_t work, int64_t& logical) {
+  return xcd_tile((int64_t)blockIdx.x, work, logical);
 }
 
 // Quantised H of the E4M3 gate/up tile: the tile's fp32 values are staged in
@@ -362,8 +365,8 @@ __device__ __forceinline__ void router_tile_select(const GemmArgs& a, int nt, in
 // and the row's score gradient Q . H over the tile's columns, added over the
 // four column quarters in order.  dG, dU and s H leave in bf16 (they are the
 // operands of the next products); everything else is fp32.  Four consecutive
-// columns per lane go out as 8-byte stores.  98304 rows, 384 experts, 2560 x
-// 512: 0.71 ms for 515 GFLOP, 730 TFLOP/s, the weights (2 GB) read once.
+// columns per lane go out as 8-byte stores.  98304 rows of 384 experts and
+// 16384 of the shared one, 2560 x 512: 0.80 ms for 601 GFLOP, 750 TFLOP/s.
 template <int XR>
 __device__ __forceinline__ void epilogue_grad(const GemmArgs& a, floatx16_t (&acc)[4][2],
                                               floatx16_t& accx, int nt, int64_t row0, int rows,
@@ -1392,6 +1395,41 @@ static hipError_t launch_mode(const GemmArgs& a, dim3 grid, hipStream_t stream) 
   return hipGetLastError();
 }
 
+static dim3 xcd_grid(int64_t work) {
+  const int64_t share = (work + kXcd - 1) / kXcd;
+  return dim3((unsigned)(share * kXcd));
+}
+
+// The backward pass's gate/up products in one launch: the shared expert's
+// tiles (t, all tokens; the first token_blocks blocks), then the pairs' (r).
+// Two launches left the CUs to the shared expert's few tiles alone: 4096
+// tokens of 2048, 128 experts of 768, eight a token, and a shared one, 0.33 +
+// 0.07 ms against 0.36 (16384 of 2560, 384 of 512, six: 0.80 ms either way).
+__global__ __launch_bounds__(512, 2) void gemm_gateup_grad_kernel(GemmArgs t, GemmArgs r,
+                                                                  int64_t token_blocks) {
+  extern __shared__ __attribute__((aligned(16))) char lds_raw[];
+  const int64_t b = blockIdx.x;
+  int64_t logical;
+  if (b < token_blocks) {
+    if (!xcd_tile(b, (t.rows_dense + BM - 1) / BM * t.n_tiles_n, logical)) return;
+    gemm_tile<kGateUpGrad, false>(t, logical / t.n_tiles_n, (int)(logical % t.n_tiles_n), lds_raw);
+    return;
+  }
+  const int64_t m_tiles = *r.n_tiles;
+  if (!xcd_tile(b - token_blocks, m_tiles * r.n_tiles_n, logical)) return;
+  const int64_t mt = logical / r.n_tiles_n;
+  const int nt = (int)(logical % r.n_tiles_n);
+  const int4 ent = reinterpret_cast<const int4*>(r.tiles)[mt];
+  const bool once = single_tile_segment(r, ent, mt, m_tiles);
+  if (ent.z > BM) {
+    if (once) gemm_tile<kGateUpGrad, true, kXRows, true>(r, mt, nt, lds_raw);
+    else gemm_tile<kGateUpGrad, true, kXRows>(r, mt, nt, lds_raw);
+  } else {
+    if (once) gemm_tile<kGateUpGrad, true, 0, true>(r, mt, nt, lds_raw);
+    else gemm_tile<kGateUpGrad, true>(r, mt, nt, lds_raw);
+  }
+}
+
 static hipError_t launch_gemm(int mode, const GemmArgs& a, int64_t max_m_tiles,
                               hipStream_t stream) {
   const int64_t work = max_m_tiles * a.n_tiles_n;
@@ -1405,9 +1443,6 @@ static hipError_t launch_gemm(int mode, const GemmArgs& a, int64_t max_m_tiles,
     case kGateUp:
       return grouped ? launch_mode<kGateUp, true>(a, grid, stream)
                      : launch_mode<kGateUp, false>(a, grid, stream);
-    case kGateUpGrad:
-      return grouped ? launch_mode<kGateUpGrad, true>(a, grid, stream)
-                     : launch_mode<kGateUpGrad, false>(a, grid, stream);
     case kDown:
       return grouped ? launch_mode<kDown, true>(a, grid, stream)
                      : launch_mode<kDown, false>(a, grid, stream);
@@ -1458,21 +1493,39 @@ hipError_t launch_gateup(const uint16_t* x, int64_t x_rows, const int32_t* sorte
   return launch_gemm(kGateUp, a, mt, stream);
 }
 
-hipError_t launch_gateup_grad(const uint16_t* x, int64_t x_rows, const int32_t* sorted_src, int K,
+hipError_t launch_gateup_grad(const uint16_t* x, int64_t N, const int32_t* sorted_src, int K,
                               const int32_t* tiles, const int32_t* n_tiles, int64_t max_tiles,
-                              int64_t rows_dense, const uint16_t* w_gate, const uint16_t* w_up,
-                              int d, int h, const float* Q, const float* row_scale,
-                              uint16_t* hid, int64_t hid_ld, float* dscore_part,
+                              int d, const float* row_scale, float* dscore_part,
+                              const GateUpGrad& routed, const GateUpGrad* shared,
                               hipStream_t stream) {
-  GemmArgs a = gateup_args(x, x_rows, sorted_src, K, tiles, n_tiles, rows_dense, w_gate, w_up, d,
-                           h, nullptr);
-  a.q_in = Q;
-  a.row_scale = row_scale;
-  a.hid_out = hid;
-  a.hid_ld = hid_ld;
-  a.dscore_part = dscore_part;
-  const int64_t mt = tiles ? max_tiles : (rows_dense + BM - 1) / BM;
-  return launch_gemm(kGateUpGrad, a, mt, stream);
+  auto set = [](GemmArgs& a, const GateUpGrad& g) {
+    a.q_in = g.Q;
+    a.hid_out = g.hid;
+    a.hid_ld = g.hid_ld;
+  };
+  GemmArgs r = gateup_args(x, N, sorted_src, K, tiles, n_tiles, 0, routed.w_gate, routed.w_up, d,
+                           routed.h, nullptr);
+  set(r, routed);
+  r.row_scale = row_scale;
+  r.dscore_part = dscore_part;
+  GemmArgs t{};
+  int64_t token_blocks = 0;
+  if (shared) {
+    t = gateup_args(x, N, nullptr, 1, nullptr, nullptr, N, shared->w_gate, shared->w_up, d,
+                    shared->h, nullptr);
+    set(t, *shared);
+    token_blocks = xcd_grid((N + BM - 1) / BM * t.n_tiles_n).x;
+  }
+  const int64_t work = max_tiles * r.n_tiles_n;
+  const int64_t blocks = token_blocks + (work + kXcd - 1) / kXcd * kXcd;
+  if (blocks > 0x7FFFFF0LL) return hipErrorInvalidConfiguration;
+  static std::atomic<uint32_t> configured{0};
+  const hipError_t e =
+      set_lds_limit_once((const void*)gemm_gateup_grad_kernel, LDS_BYTES, configured);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(gemm_gateup_grad_kernel, dim3((unsigned)blocks), dim3(512), LDS_BYTES, stream,
+                     t, r, token_blocks);
+  return hipGetLastError();
 }
 
 hipError_t launch_down(const uint16_t* H, int64_t h_rows, const int32_t* tiles, const int32_t* n_tiles,
@@ -1481,11 +1534,6 @@ hipError_t launch_down(const uint16_t* H, int64_t h_rows, const int32_t* tiles, 
   const GemmArgs a = down_args(H, h_rows, tiles, n_tiles, rows_dense, w_down, d, h, Y);
   const int64_t mt = tiles ? max_tiles : (rows_dense + BM - 1) / BM;
   return launch_gemm(kDown, a, mt, stream);
-}
-
-static dim3 xcd_grid(int64_t work) {
-  const int64_t share = (work + kXcd - 1) / kXcd;
-  return dim3((unsigned)(share * kXcd));
 }
 
 hipError_t launch_router_shared_gateup(const uint16_t* x, int64_t N, int d,

@@ -117,19 +117,27 @@ hipError_t launch_gateup(const uint16_t* x, int64_t x_rows, const int32_t* sorte
                          int64_t rows_dense, const uint16_t* w_gate,
                          const uint16_t* w_up, int d, int h, uint16_t* H,
                          hipStream_t stream, bool kblock_major = false);
-// Grouped down projection: Y rows = H rows W_d^T (bf16 out).  H has h_rows
-// rows; h_rows * h * 2 < 4 GiB.
-// The gate/up product of the backward pass over the same rows (see the
-// kernel's epilogue): from Q [rows][h] fp32 and the pairs' weights row_scale
-// [N*K] (NULL: 1) it writes hid [rows][hid_ld] = dG | dU | s H and, when given,
-// the score gradients' partial sums [rows][gateup_col_tiles(h)].
-hipError_t launch_gateup_grad(const uint16_t* x, int64_t x_rows, const int32_t* sorted_src, int K,
+// The gate/up products of the backward pass over the same rows (see the
+// kernel's epilogue), the pairs' and the shared expert's over all tokens (or
+// NULL): from Q [rows][h] fp32 and the pairs' weights row_scale [N*K] they
+// write hid [rows][hid_ld] = dG | dU | s H, and the pairs the score gradients'
+// partial sums [rows][gateup_col_tiles(h)].
+struct GateUpGrad {
+  const uint16_t* w_gate;
+  const uint16_t* w_up;
+  int h;
+  const float* Q;
+  uint16_t* hid;
+  int64_t hid_ld;
+};
+hipError_t launch_gateup_grad(const uint16_t* x, int64_t N, const int32_t* sorted_src, int K,
                               const int32_t* tiles, const int32_t* n_tiles, int64_t max_tiles,
-                              int64_t rows_dense, const uint16_t* w_gate, const uint16_t* w_up,
-                              int d, int h, const float* Q, const float* row_scale,
-                              uint16_t* hid, int64_t hid_ld, float* dscore_part,
+                              int d, const float* row_scale, float* dscore_part,
+                              const GateUpGrad& routed, const GateUpGrad* shared,
                               hipStream_t stream);
 inline int gateup_col_tiles(int h) { return (h + 127) / 128; }
+// Grouped down projection: Y rows = H rows W_d^T (bf16 out).  H has h_rows
+// rows; h_rows * h * 2 < 4 GiB.
 hipError_t launch_down(const uint16_t* H, int64_t h_rows, const int32_t* tiles, const int32_t* n_tiles,
                        int64_t max_tiles, int64_t rows_dense, const uint16_t* w_down,
                        int d, int h, uint16_t* Y, hipStream_t stream);
