@@ -70,9 +70,9 @@ __device__ __forceinline__ void load_f32(const float* p, float* v) {
     v[0] = *p;
   }
 }
-template <int VEC>
-__device__ __forceinline__ void load_any(const void* base, int64_t at, bool f32, float* v) {
-  if (f32) load_f32<VEC>(reinterpret_cast<const float*>(base) + at, v);
+template <int VEC, bool F32>
+__device__ __forceinline__ void load_any(const void* base, int64_t at, float* v) {
+  if constexpr (F32) load_f32<VEC>(reinterpret_cast<const float*>(base) + at, v);
   else load_bf16<VEC>(reinterpret_cast<const uint16_t*>(base) + at, v);
 }
 template <int VEC>
@@ -156,7 +156,7 @@ struct NormArgs {
 // fp32 stream: 87 us; with one wave a row (forty columns a lane) 104 us, and
 // 64 such rows 3.2 us against 5.8.  512 columns: a wave and a block of one
 // wave took the same.
-template <bool WAVE, int VEC, bool POST>
+template <bool WAVE, int VEC, bool POST, bool SF32, bool WF32>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
   constexpr int NV = 8 / VEC;
   __shared__ float part[2][16];
@@ -168,19 +168,30 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
   const int d = a.d;
   const int64_t base = row * d;
   const float inv_d = 1.0f / (float)d;
+  // columns past the row load column 0 and count as 0: a load under a branch
+  // would be waited for inside it
+  auto inside = [&](int j) { return (j * threads + t) * VEC < d; };
+  auto column = [&](int j) { return inside(j) ? (j * threads + t) * VEC : 0; };
   float v[NV][VEC], q[NV][VEC], w[NV][VEC], pw[NV][VEC];
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_any<VEC, SF32>(a.residual, base + column(j), q[j]);
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * threads + t) * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[j][i] = q[j][i] = w[j][i] = pw[j][i] = 0.0f;
-    if (c < d) {
-      load_bf16<VEC>(a.x + base + c, v[j]);
-      if (a.residual) load_any<VEC>(a.residual, base + c, a.stream_f32, q[j]);
-      if (POST) load_any<VEC>(a.post_w, c, a.weight_f32, pw[j]);
-      load_any<VEC>(a.w, c, a.weight_f32, w[j]);
-    }
+    const int c = column(j);
+    load_bf16<VEC>(a.x + base + c, v[j]);
+    if constexpr (POST) load_any<VEC, WF32>(a.post_w, c, pw[j]);
+    load_any<VEC, WF32>(a.w, c, w[j]);
   }
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      v[j][i] = inside(j) ? v[j][i] : 0.0f;
+      w[j][i] = inside(j) ? w[j][i] : 0.0f;
+      if constexpr (POST) pw[j][i] = inside(j) ? pw[j][i] : 0.0f;
+    }
   if constexpr (POST) {
     float ss[1] = {0.0f};
 #pragma unroll
@@ -198,14 +209,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[j][i] += q[j][i];
+      for (int i = 0; i < VEC; ++i) v[j][i] += inside(j) ? q[j][i] : 0.0f;
   }
   if (a.r_out) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * threads + t) * VEC;
       if (c < d) {
-        if (a.stream_f32) store_f32<VEC>(reinterpret_cast<float*>(a.r_out) + base + c, v[j]);
+        if constexpr (SF32) store_f32<VEC>(reinterpret_cast<float*>(a.r_out) + base + c, v[j]);
         else store_bf16<VEC>(reinterpret_cast<uint16_t*>(a.r_out) + base + c, v[j]);
       }
     }
@@ -280,7 +291,7 @@ struct NormGradArgs {
 // everything it reads is asked for before the first sum: the passes over memory
 // bound it (16384 x 2560, fp32 stream, sandwich: 755 MB in 139 us, 5.4 TB/s; a
 // wave per row, forty columns a lane and two waves a SIMD, took 250 us).
-template <bool WAVE, int VEC, bool POST>
+template <bool WAVE, int VEC, bool POST, bool SF32, bool WF32>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
   constexpr int NV = 8 / VEC;
   constexpr int RPB = WAVE ? 4 : 1;
@@ -290,15 +301,20 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
   const int sub = WAVE ? threadIdx.x >> 6 : 0;
   const int d = a.d;
   const float inv_d = 1.0f / (float)d;
+  // as in norm_kernel
+  auto inside = [&](int j) { return (j * threads + t) * VEC < d; };
+  auto column = [&](int j) { return inside(j) ? (j * threads + t) * VEC : 0; };
   float dw[NV][VEC], dp[NV][VEC], w[NV][VEC], pw[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * threads + t) * VEC;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) dw[j][i] = dp[j][i] = w[j][i] = pw[j][i] = 0.0f;
-    if (c < d) {
-      load_any<VEC>(a.w, c, a.weight_f32, w[j]);
-      if (POST) load_any<VEC>(a.post_w, c, a.weight_f32, pw[j]);
+    for (int i = 0; i < VEC; ++i) dw[j][i] = dp[j][i] = 0.0f;
+    load_any<VEC, WF32>(a.w, column(j), w[j]);
+    if constexpr (POST) load_any<VEC, WF32>(a.post_w, column(j), pw[j]);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      w[j][i] = inside(j) ? w[j][i] : 0.0f;
+      if constexpr (POST) pw[j][i] = inside(j) ? pw[j][i] : 0.0f;
     }
   }
   int flip = 0;
@@ -309,16 +325,29 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
     float r[NV][VEC], g[NV][VEC], q[NV][VEC], xs[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * threads + t) * VEC;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) r[j][i] = g[j][i] = q[j][i] = xs[j][i] = 0.0f;
-      if (c < d) {
-        load_any<VEC>(a.r, base + c, a.stream_f32, r[j]);
-        load_bf16<VEC>(a.dy + base + c, g[j]);
-        if (a.dres) load_any<VEC>(a.dres, base + c, a.stream_f32, q[j]);
-        if (POST) load_bf16<VEC>(a.x + base + c, xs[j]);
-      }
+      const int c = column(j);
+      load_any<VEC, SF32>(a.r, base + c, r[j]);
+      load_bf16<VEC>(a.dy + base + c, g[j]);
+      if constexpr (POST) load_bf16<VEC>(a.x + base + c, xs[j]);
     }
+    if (a.dres) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_any<VEC, SF32>(a.dres, base + column(j), q[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) q[j][i] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        r[j][i] = inside(j) ? r[j][i] : 0.0f;
+        g[j][i] = inside(j) ? g[j][i] : 0.0f;
+        q[j][i] = inside(j) ? q[j][i] : 0.0f;
+        if constexpr (POST) xs[j][i] = inside(j) ? xs[j][i] : 0.0f;
+      }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -340,7 +369,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
       }
       if (c < d) {
         if (a.dr_out) {
-          if (a.stream_f32) store_f32<VEC>(reinterpret_cast<float*>(a.dr_out) + base + c, r[j]);
+          if constexpr (SF32) store_f32<VEC>(reinterpret_cast<float*>(a.dr_out) + base + c, r[j]);
           else store_bf16<VEC>(reinterpret_cast<uint16_t*>(a.dr_out) + base + c, r[j]);
         }
         if (!POST && a.dx) store_bf16<VEC>(a.dx + base + c, r[j]);
@@ -427,28 +456,38 @@ bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 int row_threads(int d) { return (d + 511) / 512 * 64; }
 
-template <bool WAVE, int VEC>
-void start_norm(const NormArgs& a, hipStream_t stream) {
-  const int64_t blocks = WAVE ? (a.n + 3) / 4 : a.n;
-  const dim3 grid((unsigned)(blocks < kGridX ? blocks : kGridX),
-                  (unsigned)((blocks + kGridX - 1) / kGridX));
-  const int threads = WAVE ? 256 : row_threads(a.d);
-  if (a.post_w)
-    hipLaunchKernelGGL((norm_kernel<WAVE, VEC, true>), grid, dim3(threads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_kernel<WAVE, VEC, false>), grid, dim3(threads), 0, stream, a);
-}
-
-template <bool WAVE, int VEC>
-void start_norm_grad(const NormGradArgs& a, int blocks, hipStream_t stream) {
-  const int threads = WAVE ? 256 : row_threads(a.d);
-  if (a.post_w)
-    hipLaunchKernelGGL((norm_grad_kernel<WAVE, VEC, true>), dim3((unsigned)blocks), dim3(threads),
-                       0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_grad_kernel<WAVE, VEC, false>), dim3((unsigned)blocks), dim3(threads),
-                       0, stream, a);
-}
+// The kernels are built for every form (row of a wave or a block, vector width,
+// sandwich or not, types of the stream and of the weights): a type chosen at
+// run time inside them puts a branch around every load, which the compiler
+// then waits for one by one (1025 x 1001, sandwich, backward: 18.8 us, 15.2
+// without those branches, 9 without the ones on the row's end too).
+#define MOE_NORM_TYPES(kernel, wave, vec, post)                                             \
+  do {                                                                                      \
+    if (a.stream_f32 && a.weight_f32)                                                       \
+      hipLaunchKernelGGL((kernel<wave, vec, post, true, true>), grid, dim3(threads), 0,     \
+                         stream, a);                                                        \
+    else if (a.stream_f32)                                                                  \
+      hipLaunchKernelGGL((kernel<wave, vec, post, true, false>), grid, dim3(threads), 0,    \
+                         stream, a);                                                        \
+    else if (a.weight_f32)                                                                  \
+      hipLaunchKernelGGL((kernel<wave, vec, post, false, true>), grid, dim3(threads), 0,    \
+                         stream, a);                                                        \
+    else                                                                                    \
+      hipLaunchKernelGGL((kernel<wave, vec, post, false, false>), grid, dim3(threads), 0,   \
+                         stream, a);                                                        \
+  } while (0)
+#define MOE_NORM_FORM(kernel, wave, vec)                          \
+  do {                                                            \
+    if (a.post_w) MOE_NORM_TYPES(kernel, wave, vec, true);        \
+    else MOE_NORM_TYPES(kernel, wave, vec, false);                \
+  } while (0)
+#define MOE_NORM_LAUNCH(kernel)                                   \
+  do {                                                            \
+    if (wave && vec) MOE_NORM_FORM(kernel, true, 8);              \
+    else if (vec) MOE_NORM_FORM(kernel, false, 8);                \
+    else if (wave) MOE_NORM_FORM(kernel, true, 1);                \
+    else MOE_NORM_FORM(kernel, false, 1);                         \
+  } while (0)
 
 }  // namespace
 
@@ -464,10 +503,11 @@ hipError_t launch_rms_norm(const uint16_t* x, const void* residual, const void* 
   // a 1 x 128 group is 16 lanes of 8 columns
   if (codes && (!vec || d % 128)) return hipErrorInvalidValue;
   const bool wave = d <= kWaveD;
-  if (vec && wave) start_norm<true, 8>(a, stream);
-  else if (vec) start_norm<false, 8>(a, stream);
-  else if (wave) start_norm<true, 1>(a, stream);
-  else start_norm<false, 1>(a, stream);
+  const int64_t blocks = wave ? (n + 3) / 4 : n;
+  const dim3 grid((unsigned)(blocks < kGridX ? blocks : kGridX),
+                  (unsigned)((blocks + kGridX - 1) / kGridX));
+  const int threads = wave ? 256 : row_threads(d);
+  MOE_NORM_LAUNCH(norm_kernel);
   return hipGetLastError();
 }
 
@@ -496,10 +536,9 @@ hipError_t launch_rms_norm_grad(const uint16_t* dy, const void* r, const uint16_
   const bool vec = d % 8 == 0 && al16(dy) && al16(r) && al16(x) && al16(dres) && al16(w) &&
                    al16(post_w) && al16(dx) && al16(dr_out);
   const bool wave = d <= kWaveD;
-  if (vec && wave) start_norm_grad<true, 8>(a, blocks, stream);
-  else if (vec) start_norm_grad<false, 8>(a, blocks, stream);
-  else if (wave) start_norm_grad<true, 1>(a, blocks, stream);
-  else start_norm_grad<false, 1>(a, blocks, stream);
+  const int threads = wave ? 256 : row_threads(d);
+  const dim3 grid((unsigned)blocks);
+  MOE_NORM_LAUNCH(norm_grad_kernel);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (!dw && !dw_post) return hipSuccess;
