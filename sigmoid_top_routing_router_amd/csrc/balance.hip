@@ -12,9 +12,9 @@
 //   normalised:  dz = w (s (1 - s) / D) (f - sum_e f p)
 //   softmax:     dz = w p (f - sum_e f p)
 //
-// Rows are read 16 lanes each, four to a wave: a lane holds 4 consecutive
-// columns out of every 64, so a row's reductions stay inside a DPP row and a
-// wave reads four contiguous rows.  Both passes are bound by memory: 65536 x
+// Rows are read 16 lanes each, four to a wave: a lane holds four columns out
+// of every 64, so a row's reductions stay inside a DPP row and a wave reads
+// four contiguous rows.  Both passes are bound by memory: 65536 x
 // 384 logits in 16 segments, 100 MB read in 27 us (3.7 TB/s, what a plain
 // reduction reaches); the gradient added to one that is there, 302 MB in 67 us
 // (4.5 TB/s, a copy's rate).
@@ -60,22 +60,47 @@ struct Segs {
   }
 };
 
+// The column of a lane's value (j, i).  QUADS: E is a multiple of 4; a lane has
+// four consecutive columns, and its loads are 16 bytes wide where the array is
+// aligned (vec).  Else neighbouring lanes have neighbouring columns (65536 x
+// 383, gradient: 87 us in quads).
+template <bool QUADS>
+__device__ __forceinline__ int column(int j, int i, int l16) {
+  return 64 * j + (QUADS ? 4 * l16 + i : 16 * i + l16);
+}
+
 // The NC x 4 columns of row t that this lane holds; columns past E give fill.
-template <int NC>
+template <int NC, bool QUADS>
 __device__ __forceinline__ void load_row(const float* __restrict__ Z, int64_t t, int E, int l16,
                                          bool vec, float fill, float (&v)[NC][4]) {
   const float* p = Z + t * E;
+  if constexpr (QUADS) {
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = 64 * j + 4 * l16;
-    if (vec) {
-      const float4 q = c < E ? *reinterpret_cast<const float4*>(p + c)
-                             : make_float4(fill, fill, fill, fill);
-      v[j][0] = q.x; v[j][1] = q.y; v[j][2] = q.z; v[j][3] = q.w;
-    } else {
+    for (int j = 0; j < NC; ++j) {
+      const int c = column<QUADS>(j, 0, l16);
+      if (vec) {
+        const float4 q = c < E ? *reinterpret_cast<const float4*>(p + c)
+                               : make_float4(fill, fill, fill, fill);
+        v[j][0] = q.x; v[j][1] = q.y; v[j][2] = q.z; v[j][3] = q.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = c + i < E ? p[c + i] : fill;
+        for (int i = 0; i < 4; ++i) v[j][i] = c < E ? p[c + i] : fill;
+      }
     }
+  } else {
+    // columns past E load column 0: a load under a branch of its own would be
+    // waited for inside it
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = column<QUADS>(j, i, l16);
+        v[j][i] = p[c < E ? c : 0];
+      }
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = column<QUADS>(j, i, l16) < E ? v[j][i] : fill;
   }
 }
 
@@ -133,7 +158,7 @@ __device__ __forceinline__ void scores(float (&v)[NC][4], float (&slope)[NC][4])
 
 constexpr int kFwdWaves = 4;
 
-template <int SCORE, int NC>
+template <int SCORE, int NC, bool QUADS>
 __global__ __launch_bounds__(64 * kFwdWaves) void balance_partial_kernel(
     const float* __restrict__ Z, const int32_t* __restrict__ ids, Segs sg, int E, int K, int R,
     bool vec, float* __restrict__ sums, uint32_t* __restrict__ loads, uint32_t* ticket) {
@@ -175,7 +200,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void balance_partial_kernel(
       const int32_t t = t0 + 4 * w + sub;
       if (t < hi) {  // whole DPP rows
         float v[NC][4], slope[NC][4];
-        load_row<NC>(Z, t, E, l16, vec, -INFINITY, v);
+        load_row<NC, QUADS>(Z, t, E, l16, vec, -INFINITY, v);
         scores<SCORE, NC>(v, slope);
 #pragma unroll
         for (int j = 0; j < NC; ++j)
@@ -190,7 +215,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void balance_partial_kernel(
       for (int i = 0; i < 4; ++i) {
         acc[j][i] += __shfl_xor(acc[j][i], 16);
         acc[j][i] += __shfl_xor(acc[j][i], 32);
-        const int c = 64 * j + 4 * l16 + i;
+        const int c = column<QUADS>(j, i, l16);
         if (sub == 0 && c < E) red[w][c] = acc[j][i];
       }
     }
@@ -296,7 +321,7 @@ __global__ __launch_bounds__(64 * kCombWaves) void balance_combine_kernel(
 
 // Each wave takes four consecutive rows at a time, 16 lanes a row; f of the
 // row's segment stays in registers until a row of another segment comes.
-template <int SCORE, int NC>
+template <int SCORE, int NC, bool QUADS>
 __global__ __launch_bounds__(256) void balance_grad_kernel(
     const float* __restrict__ Z, const int32_t* __restrict__ counts, Segs sg, int E, int RW,
     bool vec, float coef, const float* __restrict__ grad_loss, const float* G, float* out) {
@@ -329,7 +354,7 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(
         for (int j = 0; j < NC; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int c = 64 * j + 4 * l16 + i;
+            const int c = column<QUADS>(j, i, l16);
             const int32_t n = c < E ? counts[(int64_t)gcur * E + c] : 0;
             f[j][i] = (float)n;
             total += (double)n;
@@ -348,7 +373,7 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(
     const bool inside = gcur >= 0;
     if (inside) {
       float v[NC][4], slope[NC][4];
-      load_row<NC>(Z, t, E, l16, vec, -INFINITY, v);
+      load_row<NC, QUADS>(Z, t, E, l16, vec, -INFINITY, v);
       scores<SCORE, NC>(v, slope);
       float dot = 0.0f;
       if constexpr (SCORE != kSigmoid) {
@@ -371,7 +396,7 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(
     }
     if (G) {
       float q[NC][4];
-      load_row<NC>(G, t, E, l16, vec, 0.0f, q);
+      load_row<NC, QUADS>(G, t, E, l16, vec, 0.0f, q);
 #pragma unroll
       for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -380,14 +405,16 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(
     float* p = out + (int64_t)t * E;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int c = 64 * j + 4 * l16;
-      if (vec) {
+      if (QUADS && vec) {
+        const int c = column<QUADS>(j, 0, l16);
         if (c < E)
           *reinterpret_cast<float4*>(p + c) = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < E) p[c + i] = o[j][i];
+        for (int i = 0; i < 4; ++i) {
+          const int c = column<QUADS>(j, i, l16);
+          if (c < E) p[c] = o[j][i];
+        }
       }
     }
   }
@@ -415,8 +442,13 @@ static void start_partial(int nc, dim3 grid, hipStream_t stream, const float* Z,
                           const BalanceWork& w) {
 #define MOE_NC(n)                                                                              \
   case n:                                                                                      \
-    hipLaunchKernelGGL((balance_partial_kernel<SCORE, n>), grid, dim3(64 * kFwdWaves), 0,      \
-                       stream, Z, ids, sg, E, K, R, vec, w.sums, w.loads, w.ticket);           \
+    if (E % 4 == 0)                                                                            \
+      hipLaunchKernelGGL((balance_partial_kernel<SCORE, n, true>), grid, dim3(64 * kFwdWaves), \
+                         0, stream, Z, ids, sg, E, K, R, vec, w.sums, w.loads, w.ticket);      \
+    else                                                                                       \
+      hipLaunchKernelGGL((balance_partial_kernel<SCORE, n, false>), grid,                      \
+                         dim3(64 * kFwdWaves), 0, stream, Z, ids, sg, E, K, R, vec, w.sums,    \
+                         w.loads, w.ticket);                                                   \
     break;
   switch (nc) { MOE_NC(1) MOE_NC(2) MOE_NC(3) MOE_NC(4) MOE_NC(5) MOE_NC(6) }
 #undef MOE_NC
@@ -450,8 +482,12 @@ static void start_grad(int nc, dim3 grid, hipStream_t stream, const float* Z,
                        const float* gl, const float* G, float* out) {
 #define MOE_NC(n)                                                                              \
   case n:                                                                                      \
-    hipLaunchKernelGGL((balance_grad_kernel<SCORE, n>), grid, dim3(256), 0, stream, Z, counts, \
-                       sg, E, RW, vec, coef, gl, G, out);                                      \
+    if (E % 4 == 0)                                                                            \
+      hipLaunchKernelGGL((balance_grad_kernel<SCORE, n, true>), grid, dim3(256), 0, stream, Z, \
+                         counts, sg, E, RW, vec, coef, gl, G, out);                            \
+    else                                                                                       \
+      hipLaunchKernelGGL((balance_grad_kernel<SCORE, n, false>), grid, dim3(256), 0, stream,   \
+                         Z, counts, sg, E, RW, vec, coef, gl, G, out);                         \
     break;
   switch (nc) { MOE_NC(1) MOE_NC(2) MOE_NC(3) MOE_NC(4) MOE_NC(5) MOE_NC(6) }
 #undef MOE_NC
