@@ -233,9 +233,10 @@ hipError_t launch_balance_grad(const float* Z, const int32_t* counts, const int3
 // than this.
 constexpr uint32_t kGradMaxOperandBytes = 0xFFFE0000u;
 // C[row, n] = sum over the segments of sum_k A[row, k] B[k, n] in fp32.  Pairs:
-// rows from the tile table (expert, first row, rows, offset); with gather A's
-// rows are at these byte offsets (gather[row]; a_rows rows in all).  Tokens:
-// rows 0 .. rows_dense - 1.
+// rows from the tile table (expert, first row, rows + 256 * the tile's index
+// among the expert's, how many those are); with gather A's rows are at these
+// byte offsets (gather[row]; a_rows rows in all).  Tokens: rows 0 ..
+// rows_dense - 1.
 struct RowsSegment {
   const uint16_t* A;
   int64_t lda;             // elements

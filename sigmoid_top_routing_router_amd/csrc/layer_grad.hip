@@ -41,16 +41,16 @@
 //
 // Measured at 16384 tokens of 2560, 384 experts of 512, six a token, a shared
 // expert of 512 (256 rows an expert, 6 GB of routed weights and gradients):
-//   Q          301 GFLOP   0.40 ms   750 TFLOP/s, 2.4 GB read + written
-//   dx parts   633 GFLOP   0.89 ms   710 TFLOP/s, 4.5 GB, 5.1 TB/s
-//   weights    934 GFLOP   1.49 ms   625 TFLOP/s, 5.5 GB, 3.7 TB/s
-// dx is bound by memory: every expert's gate and up matrices are read again,
-// and the parts are fp32.  The weights' gradients are bound by the CU's path
-// to the caches, which loads (48 KB a stage pair) and results (64 KB a tile)
-// share: MFMAs and LDS reads alone take 0.60 ms, without stores 0.77, loads
-// and stores without MFMAs 1.3.  128 x 256 tiles, two blocks, against one
-// block of eight waves and 256 x 256: weights 1.49 ms against 1.67, Q 0.40
-// against 0.43 (bf16 parts: dx 0.80 against 0.84).
+//   Q          301 GFLOP   0.39 ms   770 TFLOP/s, 2.3 GB read + written
+//   dx parts   633 GFLOP   0.88 ms   720 TFLOP/s, 3.8 GB, 4.3 TB/s
+//   weights    934 GFLOP   1.47 ms   635 TFLOP/s, 5.5 GB, 3.7 TB/s
+// All are bound by the CU's path to the caches, which loads into LDS and
+// results share: dx loads 7.3 GB into LDS and stores 1.2 (9.7 TB/s; loads
+// alone reach some 12), the weights' gradients load 10.7 GB and store 3.0 (9.3
+// TB/s).  Of the latter, MFMAs and LDS reads alone take 0.60 ms, without stores
+// 0.77, loads and stores without MFMAs 1.3.  128 x 256 tiles, two blocks,
+// against one block of eight waves and 256 x 256: weights 1.48 ms against 1.67,
+// Q 0.40 against 0.43 (bf16 parts: dx 0.80 against 0.84).
 #include <type_traits>
 
 #include "common.h"
@@ -293,16 +293,15 @@ __host__ __device__ __forceinline__ int64_t xcd_blocks(int64_t work) {
 // tile repeat its last row and columns past the result column 0 (what they
 // give is not stored); k past a segment reads zeros of both.
 template <bool PAIR, bool GATHER>
-__device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item) {
-  const int64_t mt = item / p.n_tiles_n;
-  const int n0 = (int)(item % p.n_tiles_n) * TN;
+__device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t mt, int nt) {
+  const int n0 = nt * TN;
   int expert = 0, rows;
   int64_t row0;
   if constexpr (PAIR) {
     const int4 ent = reinterpret_cast<const int4*>(p.tiles)[mt];
     expert = ent.x;
     row0 = ent.y;
-    rows = ent.z;
+    rows = ent.z & 0xFF;
   } else {
     row0 = mt * TM;
     rows = (int)min((int64_t)TM, p.rows_dense - row0);
@@ -463,7 +462,11 @@ __device__ __forceinline__ void rows_tile(const RowsProblem& p, int64_t item) {
   }
 }
 
-// The work item of block b of a problem's share of the grid.
+// The work item of block b of a problem's share of the grid.  Items run over
+// the row tiles of an expert (of the tokens) four at a time: the four of a
+// column tile follow each other, so that they read the same B within the time
+// that the L2 keeps it, then the next column tile, which reads the same A.
+constexpr int kRowGroup = 4;
 template <bool PAIR, bool GATHER>
 __device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b) {
   const int64_t m_tiles = PAIR ? (int64_t)*p.n_tiles : (p.rows_dense + TM - 1) / TM;
@@ -471,7 +474,18 @@ __device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b) {
   const int64_t share = (work + kXcds - 1) / kXcds;
   if (b / kXcds >= share) return;
   const int64_t item = xcd_item(b, share);
-  if (item < work) rows_tile<PAIR, GATHER>(p, item);
+  if (item >= work) return;
+  const int64_t mt = item / p.n_tiles_n;
+  int64_t index = mt, count = m_tiles;  // of the tile among its expert's
+  if constexpr (PAIR) {
+    const int4 ent = reinterpret_cast<const int4*>(p.tiles)[mt];
+    index = ent.z >> 8;
+    count = ent.w;
+  }
+  const int in_group = (int)(index % kRowGroup);
+  const int group = (int)min((int64_t)kRowGroup, count - (index - in_group));
+  const int l = in_group * p.n_tiles_n + (int)(item % p.n_tiles_n);
+  rows_tile<PAIR, GATHER>(p, mt - in_group + l % group, l / group);
 }
 
 // The tokens' blocks first (fewer items), then the pairs'.
@@ -752,7 +766,8 @@ __global__ __launch_bounds__(512) void grouped_rows_kernel(
   for (int j = 0; j < w; ++j) base += wsum[j];
   uint32_t t = base + inc - nt;
   for (int32_t r = 0; r < cnt; r += TM)
-    reinterpret_cast<int4*>(tiles)[t++] = make_int4(e, off + r, min(TM, cnt - r), r);
+    reinterpret_cast<int4*>(tiles)[t++] =
+        make_int4(e, off + r, min(TM, cnt - r) | (r / TM) << 8, (int)nt);
   if (e == 511) *n_tiles = (int32_t)(base + inc);
 }
 
