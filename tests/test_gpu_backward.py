@@ -184,6 +184,43 @@ def test_padded_rows_that_hold_nan(M):
         assert torch.equal(getattr(got[2], k), getattr(want[2], k)), k
 
 
+def test_hidden_rows_past_four_gigabytes(M):
+    """60,000 x 8 pairs of 2,080: the hidden rows take 6 GB, Q 4.  The last
+    expert's gradients and the last tokens' grad_x against fp64."""
+    import torch
+    N, d, E, K, h = 60000, 64, 9, 8, 2080
+    L, Z, ids = make(26, N, d, E, K, h, 0, router=False)
+    say("backward, hidden rows past 4 GB")
+    dx, dz, G = run(M, L, Z, ids)
+    x, dy = (bf16_dev(L[k]).double() for k in ("x", "dy"))
+    wg, wu, wd = (bf16_dev(L[k]).double() for k in ("w_gate", "w_up", "w_down"))
+    z, sel = dev(Z).double(), dev(ids)
+
+    def pairs(t, e):
+        s = torch.sigmoid(z[t, e])[:, None]
+        g, u, q = x[t] @ wg[e].t(), x[t] @ wu[e].t(), dy[t] @ wd[e]
+        sg = torch.sigmoid(g)
+        return s * q * u * sg * (1 + g * (1 - sg)), s * q * g * sg, s * g * sg * u
+    c = (N / 16 + 20) * 2.0 ** -24
+    e = E - 1
+    t = (sel == e).any(dim=1).nonzero()[:, 0]
+    dg, du, sh = pairs(t, e)
+    for got, a, b in ((G.w_gate, dg, x[t]), (G.w_up, du, x[t]), (G.w_down, dy[t], sh)):
+        want, mag = a.t() @ b, a.abs().t() @ b.abs()
+        tol = (HALF * 1.01 + 2 * c + 2.0 ** -17) * mag + HALF * want.abs()
+        assert bool(((got[e].double() - want).abs() <= tol).all())
+        assert float((got[e].double() - want).norm() / want.norm()) <= HALF
+    tail = torch.arange(N - 40, N, device="cuda")
+    want, mag = torch.zeros(40, d, dtype=torch.float64, device="cuda"), 0.0
+    for e in range(E):
+        on = (sel[tail] == e).any(dim=1)[:, None]
+        dg, du, _ = pairs(tail, e)
+        want += on * (dg @ wg[e] + du @ wu[e])
+        mag = mag + on * (dg.abs() @ wg[e].abs() + du.abs() @ wu[e].abs())
+    tol = (HALF * 1.01 + 2 * c + 2.0 ** -17) * mag + HALF * want.abs()
+    assert bool(((dx[tail].double() - want).abs() <= tol).all())
+
+
 def test_agrees_with_the_forward_pass(M):
     """Differences of the layer's own output: dy . (y(x + v) - y(x - v)) / 2 for
     a direction v, with the selection held by a bias.  y leaves in bf16, so the
