@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 from dataclasses import dataclass, replace
 from typing import Optional
 
@@ -34,9 +35,15 @@ def load_library():
     return _lib.load()
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -94,6 +101,7 @@ def _one_device(first, **others):
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
+@functools.lru_cache(maxsize=None)
 def _bf16():
     torch = _torch()
     return (torch.bfloat16, torch.uint16, torch.int16)
