@@ -249,28 +249,23 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
                                   grad_logits, g.logits, router ? l.dzb : nullptr, l.ldb, st),
           "logits gradient");
   // grad_x: the pairs' parts, and the tokens' (shared expert and router)
-  {
-    moe::RowsProblem r = pair_rows(), t = token_rows();
-    const int64_t es = (int64_t)h * d;
-    r.seg[0] = {l.hid, l.ld, w.w_gate, es, h};
-    r.seg[1] = {l.hid + h, l.ld, w.w_up, es, h};
-    r.n_seg = 2;
-    r.ncols = d;
-    r.out = l.dXp;
-    r.ldo = d;
-    if (shared) {
-      t.seg[t.n_seg++] = {l.hids, l.lds, w.ws_gate, 0, hs};
-      t.seg[t.n_seg++] = {l.hids + hs, l.lds, w.ws_up, 0, hs};
-    }
-    if (router) t.seg[t.n_seg++] = {l.dzb, l.ldb, w.w_router, 0, E};
-    t.ncols = d;
-    t.out = l.base;
-    t.ldo = d;
-    MOE_TRY(moe::launch_rows(t.n_seg ? &t : nullptr, r, st), "x gradient");
-    MOE_TRY(moe::launch_sum_pairs(t.n_seg ? l.base : nullptr, l.dXp, l.src_pos, N, K, d, g.x, st),
-            "x gradient sum");
+  moe::RowsProblem r = pair_rows(), t = token_rows();
+  const int64_t es = (int64_t)h * d;
+  r.seg[0] = {l.hid, l.ld, w.w_gate, es, h};
+  r.seg[1] = {l.hid + h, l.ld, w.w_up, es, h};
+  r.n_seg = 2;
+  r.ncols = d;
+  r.out = l.dXp;
+  r.ldo = d;
+  if (shared) {
+    t.seg[t.n_seg++] = {l.hids, l.lds, w.ws_gate, 0, hs};
+    t.seg[t.n_seg++] = {l.hids + hs, l.lds, w.ws_up, 0, hs};
   }
-  // the weights' gradients, one launch
+  if (router) t.seg[t.n_seg++] = {l.dzb, l.ldb, w.w_router, 0, E};
+  t.ncols = d;
+  t.out = l.base;
+  t.ldo = d;
+  // the weights' gradients
   moe::WeightsLaunch wl{};
   auto problem = [&](const uint16_t* A, int64_t lda, int a_cols, const uint16_t* B, int64_t ldb,
                      int b_cols, uint16_t* out) {
@@ -299,7 +294,9 @@ moe_status_t backward_launches(const moe_problem_t& p, const moe_weights_t& w, c
   wl.expert[1] = problem(l.hid + h, l.ld, h, x, d, d, g.w_up);
   wl.expert[2] = problem(dy, d, d, l.hid + 2 * h, l.ld, h, g.w_down);
   wl.E = E;
-  MOE_TRY(moe::launch_weights(wl, st), "weight gradients");
+  MOE_TRY(moe::launch_gradients(t.n_seg ? &t : nullptr, r, wl, st), "x and weight gradients");
+  MOE_TRY(moe::launch_sum_pairs(t.n_seg ? l.base : nullptr, l.dXp, l.src_pos, N, K, d, g.x, st),
+          "x gradient sum");
   return moe::set_error(MOE_OK, "");
 }
 

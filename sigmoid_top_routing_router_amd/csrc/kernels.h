@@ -259,6 +259,7 @@ struct RowsProblem {
   int64_t ldo;
 };
 int grad_tile_rows();      // rows of a tile in the table of launch_grouped_rows
+// The pairs' problem with gather, and the tokens' (or NULL).
 hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, hipStream_t stream);
 // C[m, n] = sum_row A[row, m] B[row, n] in bf16, rows offsets[e] ..
 // offsets[e + 1] - 1 (dense: all rows_dense).  The expert problems are gate,
@@ -284,7 +285,9 @@ struct WeightsLaunch {
   WeightsProblem expert[3];
   int E;
 };
-hipError_t launch_weights(WeightsLaunch w, hipStream_t stream);
+// The rows' problems (the pairs' without gather) and the weights' gradients.
+hipError_t launch_gradients(const RowsProblem* token, const RowsProblem& pair, WeightsLaunch w,
+                            hipStream_t stream);
 hipError_t launch_pairs(const int32_t* ids, const float* Z, int64_t pairs, int E, int K,
                         int32_t* ids_out, float* S, hipStream_t stream);
 hipError_t launch_grouped_rows(const int32_t* sorted_src, const float* S, int64_t pairs, int K,

@@ -11,17 +11,20 @@
 //   dZ = grad_logits + [e chosen for t] dS s (1 - s).
 // G and U come from the forward pass's tile engine, whose epilogue forms dG,
 // dU, s H and Q . H (grouped_gemm.hip).  Here:
-//  * rows_kernel: Q (fp32) and dx, C[row, n] = sum_k A[row, k] B[k, n]: the
-//    rows are k-contiguous, the weights are read as they are stored, n
-//    contiguous;
-//  * weights_kernel: every weight gradient, C[m, n] = sum_row A[row, m]
+//  * rows_tile: Q and the parts of dx (fp32), C[row, n] = sum_k A[row, k]
+//    B[k, n]: the rows are k-contiguous, the weights are read as they are
+//    stored, n contiguous;
+//  * weights_tiles: every weight gradient, C[m, n] = sum_row A[row, m]
 //    B[row, n] over the rows of an expert's segment: both operands n
 //    contiguous.
+// Q is a launch of its own (rows_kernel); the parts of dx and the weights'
+// gradients share one (gradients_kernel: 333 tokens of 320, 20 experts of 160,
+// 11 us, in two launches 11 + 10).
 // Both multiply 128 x 256 tiles with v_mfma_f32_32x32x16_bf16, four waves of
 // 128 x 64, two blocks to a CU, so that one block's start, loads and stores
-// pass behind the other's MFMAs.  rows_kernel has long sums: A in stages of 64
+// pass behind the other's MFMAs.  rows_tile has long sums: A in stages of 64
 // k (whole 128-byte lines of its rows) kept twice, B in halves of 32 k kept
-// three times.  weights_kernel has short ones (an expert's rows, some 256) and
+// three times.  weights_tiles has short ones (an expert's rows, some 256) and
 // large results: stages of 32 k kept three times, and a block takes two tiles
 // under each other as one stream of stages, so that a tile's first loads and
 // the last tile's stores pass behind MFMAs (one, three or four tiles at a time
@@ -62,14 +65,14 @@ namespace moe {
 namespace {
 
 constexpr int TM = 128, TN = 256;              // rows and columns of a tile
-// rows_kernel
+// rows_tile
 constexpr int TK = 64;
 constexpr int kRaBytes = TM * TK * 2;          // A of one stage, two slots
 constexpr int kRbOff = 2 * kRaBytes;
 constexpr int kRbBytes = TK / 2 * TN * 2;      // B of half a stage, three slots
 constexpr int kRowsLds = kRbOff + 3 * kRbBytes;
 static_assert(2 * kRowsLds <= 160 * 1024, "two blocks share a CU");
-// weights_kernel
+// weights_tiles
 constexpr int WK = 32;
 constexpr int kWaBytes = WK * TM * 2;          // A of one stage, then B
 constexpr int kWSlot = kWaBytes + WK * TN * 2;
@@ -81,6 +84,7 @@ constexpr int kWeightsLds = kIdsOff + kIdsSlots * kIdsSlot;
 constexpr int kWGroup = 2;                     // tiles of a block
 static_assert(2 * kWeightsLds <= 160 * 1024, "two blocks share a CU");
 constexpr int kXcds = 8;
+constexpr int64_t kMaxGradBlocks = (1 << 24) - 8;  // a grid's threads stay below 2^32
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
@@ -488,14 +492,13 @@ __device__ __forceinline__ void rows_block(const RowsProblem& p, int64_t b) {
   rows_tile<PAIR, GATHER>(p, mt - in_group + l % group, l / group);
 }
 
-// The tokens' blocks first (fewer items), then the pairs'.
-// GATHER: the pairs' rows of A come from p.gather.
-template <bool GATHER>
+// Q of the shared expert (token, its token_blocks blocks first) and of the
+// pairs.
 __global__ __launch_bounds__(256, 2) void rows_kernel(RowsProblem token, RowsProblem pair,
                                                       int64_t token_blocks) {
   const int64_t b = blockIdx.x;
   if (b < token_blocks) rows_block<false, false>(token, b);
-  else rows_block<true, GATHER>(pair, b - token_blocks);
+  else rows_block<true, true>(pair, b - token_blocks);
 }
 
 // ---------------------------------------------------------------- weights
@@ -686,8 +689,7 @@ __device__ __forceinline__ void weights_tiles(const WeightsProblem& p, int exper
 // then expert by expert the gate and up tiles, then the down tiles: what the
 // blocks of one XCD read at a time (one or two experts' rows of x and dG | dU,
 // or of dy and s H) then stays in its L2.
-__global__ __launch_bounds__(256, 2) void weights_kernel(WeightsLaunch w) {
-  int64_t b = blockIdx.x;
+__device__ __forceinline__ void weights_block(const WeightsLaunch& w, int64_t b) {
   for (int i = 0; i < w.n_dense; ++i) {
     const int t = w.dense[i].tiles_m * w.dense[i].tiles_n;
     if (b < t) {
@@ -722,6 +724,18 @@ __global__ __launch_bounds__(256, 2) void weights_kernel(WeightsLaunch w) {
   }
 }
 
+// The parts of dx (the tokens' token_blocks blocks, then the pairs', row_blocks
+// in all), then the weights' gradients: one launch, whose second part begins
+// on the CUs that the first has left.
+__global__ __launch_bounds__(256, 2) void gradients_kernel(RowsProblem token, RowsProblem pair,
+                                                           int64_t token_blocks,
+                                                           int64_t row_blocks, WeightsLaunch w) {
+  const int64_t b = blockIdx.x;
+  if (b < token_blocks) rows_block<false, false>(token, b);
+  else if (b < row_blocks) rows_block<true, false>(pair, b - token_blocks);
+  else weights_block(w, b - row_blocks);
+}
+
 // ---------------------------------------------------------------- small kernels
 // One thread per pair: the id kept inside [0, E), and the pair's weight
 // sigma(z), -1 for an id outside the range: such a pair is dropped.  It stays
@@ -742,7 +756,7 @@ __global__ __launch_bounds__(256) void pairs_kernel(const int32_t* __restrict__ 
 
 // Of the grouped pairs: the byte offset of every row's token in x (pitch bytes
 // a token; the same in dy), kNoAddr for a dropped pair; block 0 also makes the
-// m-tiles of rows_kernel from the segment offsets (thread e counts its
+// row tiles of rows_tile from the segment offsets (thread e counts its
 // expert's tiles, a scan places them).
 __global__ __launch_bounds__(512) void grouped_rows_kernel(
     const int32_t* __restrict__ sorted_src, const float* __restrict__ S, int64_t pairs, int K,
@@ -870,34 +884,36 @@ static int64_t rows_blocks(const RowsProblem& p) {
   return xcd_blocks(m_tiles * p.n_tiles_n);
 }
 
-template <bool GATHER>
-static hipError_t start_rows(const RowsProblem& t, const RowsProblem& r, int64_t token_blocks,
-                             int64_t blocks, hipStream_t stream) {
-  static std::atomic<uint32_t> configured{0};
-  const hipError_t e = set_lds_limit_once((const void*)rows_kernel<GATHER>, kRowsLds, configured);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rows_kernel<GATHER>, dim3((unsigned)blocks), dim3(256), kRowsLds, stream, t, r,
-                     token_blocks);
-  return hipGetLastError();
+// Column tiles, and the blocks of the tokens' part and of both.
+static void set_rows(RowsProblem& t, RowsProblem& r, bool token, int64_t& tb, int64_t& blocks) {
+  t.n_tiles_n = (t.ncols + TN - 1) / TN;
+  r.n_tiles_n = (r.ncols + TN - 1) / TN;
+  tb = token ? rows_blocks(t) : 0;
+  blocks = tb + rows_blocks(r);
 }
 
 hipError_t launch_rows(const RowsProblem* token, const RowsProblem& pair, hipStream_t stream) {
-  RowsProblem t{}, r = pair;
-  if (token) t = *token;
-  t.n_tiles_n = (t.ncols + TN - 1) / TN;
-  r.n_tiles_n = (r.ncols + TN - 1) / TN;
-  const int64_t tb = token ? rows_blocks(t) : 0;
-  const int64_t blocks = tb + rows_blocks(r);
-  if (blocks > 0x7FFFFFF0LL) return hipErrorInvalidConfiguration;
-  return r.gather ? start_rows<true>(t, r, tb, blocks, stream)
-                  : start_rows<false>(t, r, tb, blocks, stream);
+  static std::atomic<uint32_t> configured{0};
+  const hipError_t e = set_lds_limit_once((const void*)rows_kernel, kRowsLds, configured);
+  if (e != hipSuccess) return e;
+  RowsProblem t = token ? *token : RowsProblem{}, r = pair;
+  int64_t tb, blocks;
+  set_rows(t, r, token != nullptr, tb, blocks);
+  if (blocks > kMaxGradBlocks) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(rows_kernel, dim3((unsigned)blocks), dim3(256), kRowsLds, stream, t, r, tb);
+  return hipGetLastError();
 }
 
-hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
+hipError_t launch_gradients(const RowsProblem* token, const RowsProblem& pair, WeightsLaunch w,
+                            hipStream_t stream) {
+  constexpr int kLds = kRowsLds > kWeightsLds ? kRowsLds : kWeightsLds;
   static std::atomic<uint32_t> configured{0};
-  hipError_t e = set_lds_limit_once((const void*)weights_kernel, kWeightsLds, configured);
+  const hipError_t e = set_lds_limit_once((const void*)gradients_kernel, kLds, configured);
   if (e != hipSuccess) return e;
-  int64_t blocks = 0;
+  RowsProblem t = token ? *token : RowsProblem{}, r = pair;
+  int64_t tb, rb;
+  set_rows(t, r, token != nullptr, tb, rb);
+  int64_t blocks = rb;
   auto set_tiles = [](WeightsProblem& q) {
     q.tiles_m = (q.a_cols + TM - 1) / TM;
     q.tiles_n = (q.b_cols + TN - 1) / TN;
@@ -909,8 +925,9 @@ hipError_t launch_weights(WeightsLaunch w, hipStream_t stream) {
   for (WeightsProblem& q : w.expert) set_tiles(q);
   auto items = [](const WeightsProblem& q) { return (q.tiles_m + kWGroup - 1) / kWGroup * q.tiles_n; };
   blocks += xcd_blocks((int64_t)w.E * 2 * items(w.expert[0])) + xcd_blocks((int64_t)w.E * items(w.expert[2]));
-  if (blocks > 0x7FFFFFF0LL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(weights_kernel, dim3((unsigned)blocks), dim3(256), kWeightsLds, stream, w);
+  if (blocks > kMaxGradBlocks) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(gradients_kernel, dim3((unsigned)blocks), dim3(256), kLds, stream, t, r, tb,
+                     rb, w);
   return hipGetLastError();
 }
 
