@@ -3,14 +3,14 @@
 Tolerances, worst case per value.  A bf16 rounding is half a step, B = 2^-8
 relative.  Weight gradients: one operand (dG, dU, s H or grad_logits_out) is
 rounded once and the result once: B mag + B |out|, mag being the product of
-the operands' absolute values.  grad_x: the operand, the pair's part (or the
-tokens' part) and the result: 2 B mag + B |out|.  fp32 accumulation: an MFMA
+the operands' absolute values.  grad_x: the same two (its bound here holds one
+rounding of the parts more): 2 B mag + B |out|.  fp32 accumulation: an MFMA
 adds 16 products, so a sum over k has at most k / 16 + 20 roundings of 2^-24
 of at most mag each: C below, with k the longest sum of the path.
 grad_logits: Q, G and U each within C of their terms, H and Q . H a few more
 roundings (2^-18 together with sigma): (C + 2^-18) mag, plus the rounding of
 the sum.  Pooled, errors are independent: a half step is at most B / sqrt(3)
-rms, two of them (three for grad_x) below B."""
+rms, two of them (or three) below or at B."""
 import numpy as np
 import pytest
 

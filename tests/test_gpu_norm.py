@@ -2,8 +2,8 @@
 forms.
 
 Tolerances.  STAT = 2^-18 bounds the relative error of a reciprocal root mean
-square and of a mean over a row in fp32: a thread adds at most 32 squares one
-after the other, then six wave steps and four waves (42 roundings of 2^-24,
+square and of a mean over a row in fp32: a thread adds eight squares one after
+the other, then six wave steps and at most 16 waves (30 roundings of 2^-24,
 halved by the root), the root and two products one to two more each; a gradient
 uses two such factors and their products.  The magnitudes it multiplies are the
 sums of the absolute terms, so that cancelling terms are covered.  A value that
