@@ -446,7 +446,8 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *               itself.
  *  codes        [n,d] out or NULL, scales [n,d/128] out (both or neither):
  *               d % 128 == 0 and every buffer except scales 16-byte aligned.
- * At least one output, no two the same.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
+ * At least one output; none shares memory with an input or another output, but
+ * for residual_out and residual.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
  * row of zeros with eps = 0 has no norm).  bf16 buffers 2-byte, fp32 buffers
  * 4-byte aligned; 16-byte aligned buffers and d % 8 == 0 take the fast path.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
@@ -471,7 +472,8 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *               post_weight only).  n = 0 gives zeros.
  *  workspace    moe_rms_norm_backward_workspace_bytes(n, d) bytes, 256-byte
  *               aligned; 0 from the query means n or d out of range.
- * No output may alias an input or another output.
+ * No output, nor the workspace, may share memory with an input or another
+ * output.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, WORKSPACE_TOO_SMALL, HIP.
  */
 #define MOE_NORM_STREAM_F32 0x1u  /* residual, residual_out, r and their gradients are fp32 */
@@ -520,7 +522,8 @@ moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const 
  *  mean_scores  [n_seg,E] fp32 out or NULL: P.
  *  workspace    moe_balance_workspace_bytes(N, E, n_seg), 256-byte aligned; 0
  *               from the query means a size out of range.
- * 1 <= n_seg <= 2^20.  Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE,
+ * 1 <= n_seg <= 2^20.  No output, nor the workspace, may share memory with an
+ * input or another output.  Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE,
  * WORKSPACE_TOO_SMALL, HIP.
  *
  * moe_balance_loss_backward - grad_logits_out = grad_logits + grad_loss *
@@ -531,7 +534,7 @@ moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const 
  *               (counts_in, or its counts_out).
  *  grad_loss    [1] fp32 in device memory, or NULL (1).
  *  grad_logits  [N,E] fp32 or NULL (zero); grad_logits_out may be the same
- *               buffer.  It must not be logits.
+ *               buffer.  It shares memory with no other input.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
  */
 #define MOE_SCORE_SIGMOID 0
@@ -585,6 +588,8 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  *               ws_* with a shared expert).  Experts without rows get zeros.
  *  workspace    moe_backward_workspace_bytes(p) bytes, 256-byte aligned; 0
  *               from the query means an unsupported problem.
+ * No gradient, nor the workspace, may share memory with an input or another
+ * gradient, but for g->logits and grad_logits, which may be one buffer.
  * Buffers of 16-bit words 16-byte aligned, the others 4-byte.  The first call
  * on a device sets the kernels' LDS attributes: make one uncaptured call
  * before capturing.

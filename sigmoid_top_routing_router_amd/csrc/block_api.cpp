@@ -62,12 +62,35 @@ moe_status_t check_aligned(const void* const* p, int count, size_t a, const char
   return MOE_OK;
 }
 
-moe_status_t check_distinct(const void* const* out, int count) {
-  for (int i = 0; i < count; ++i)
-    for (int j = 0; j < i; ++j)
-      if (out[i] && out[i] == out[j])
-        return fail(MOE_ERR_INVALID_ARGUMENT, "two outputs are the same buffer");
+// A buffer of a call (p NULL: absent).  inplace: the input and the output that
+// may be one buffer.
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool inplace = false;
+};
+
+// No output (the workspace is one) shares memory with an input or another
+// output: a launch would overwrite what a later one still reads.
+moe_status_t check_alias(const Span* in, int n_in, const Span* out, int n_out) {
+  auto share = [](const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (share(in[i], out[o]) && !(in[i].inplace && out[o].inplace && in[i].p == out[o].p))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "an output aliases an input");
+    for (int j = 0; j < o; ++j)
+      if (share(out[j], out[o]))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "two outputs alias each other");
+  }
   return MOE_OK;
+}
+
+template <int I, int O>
+moe_status_t check_alias(const Span (&in)[I], const Span (&out)[O]) {
+  return check_alias(in, I, out, O);
 }
 
 // ---- balance loss
@@ -335,14 +358,18 @@ moe_status_t moe_backward(const moe_problem_t* p, const moe_weights_t* w, const 
   if ((s = check_aligned(in, 9, 16, "bf16 inputs")) != MOE_OK) return s;
   if ((s = check_aligned(out, 8, 16, "bf16 gradients")) != MOE_OK) return s;
   if ((s = check_aligned(f4, 4, 4, "logits and ids")) != MOE_OK) return s;
-  if (g->logits == logits)
-    return fail(MOE_ERR_INVALID_ARGUMENT, "the logits' gradient must not be the logits");
-  for (const void* i : in)
-    for (const void* o : out)
-      if (i && i == o) return fail(MOE_ERR_INVALID_ARGUMENT, "a gradient aliases an input");
   const GradLayout need = carve_grad(nullptr, *p);
   if ((s = check_workspace(workspace, workspace_bytes, need.bytes)) != MOE_OK) return s;
-  if ((s = check_distinct(out, 8)) != MOE_OK) return s;
+  const size_t xb = (size_t)p->N * p->d * 2, zb = (size_t)p->N * p->E * 4;
+  const size_t rb = (size_t)p->E * p->d * 2, eb = rb * p->h;
+  const size_t sb = p->n_shared == 1 ? (size_t)p->h_shared * p->d * 2 : 0;
+  const Span ins[] = {{x, xb}, {grad_y, xb}, {logits, zb}, {topk_ids, (size_t)p->N * p->K * 4},
+                      {grad_logits, zb, true}, {w->w_router, rb}, {w->w_gate, eb}, {w->w_up, eb},
+                      {w->w_down, eb}, {w->ws_gate, sb}, {w->ws_up, sb}, {w->ws_down, sb}};
+  const Span outs[] = {{g->x, xb}, {g->logits, zb, true}, {g->w_router, rb}, {g->w_gate, eb},
+                       {g->w_up, eb}, {g->w_down, eb}, {g->ws_gate, sb}, {g->ws_up, sb},
+                       {g->ws_down, sb}, {workspace, need.bytes}};
+  if ((s = check_alias(ins, outs)) != MOE_OK) return s;
   return backward_launches(*p, *w, x, grad_y, logits, topk_ids, grad_logits, *g,
                            carve_grad(workspace, *p), (hipStream_t)stream);
 }
@@ -374,13 +401,10 @@ moe_status_t moe_rms_norm(const uint16_t* x, const void* residual, const void* p
     const void* all[] = {x, y, residual, residual_out, weight, post_weight, codes};
     if ((s = check_aligned(all, 7, 16, "buffers of a call with codes")) != MOE_OK) return s;
   }
-  const void* in[] = {x, weight, post_weight, residual};
-  const void* out[] = {y, codes, scales, residual_out};
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j)
-      if (in[i] && in[i] == out[j] && !(in[i] == residual && out[j] == residual_out))
-        return fail(MOE_ERR_INVALID_ARGUMENT, "an output aliases an input");
-  if ((s = check_distinct(out, 4)) != MOE_OK) return s;
+  const size_t m = (size_t)n * d, sm = m * (sf ? 4 : 2), wm = (size_t)d * (wf ? 4 : 2);
+  const Span in[] = {{x, m * 2}, {residual, sm, true}, {weight, wm}, {post_weight, wm}};
+  const Span out[] = {{y, m * 2}, {residual_out, sm, true}, {codes, m}, {scales, m / 128 * 4}};
+  if ((s = check_alias(in, out)) != MOE_OK) return s;
   return done(moe::launch_rms_norm(x, residual, post_weight, weight, n, d, eps, sf, wf, y,
                                    residual_out, codes, scales, (hipStream_t)stream),
               "moe_rms_norm");
@@ -416,14 +440,14 @@ moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const 
   if ((s = check_aligned(st, 3, sf ? 4 : 2, "r and the residual's gradients")) != MOE_OK) return s;
   if ((s = check_aligned(wt, 2, wf ? 4 : 2, "weights")) != MOE_OK) return s;
   if ((s = check_aligned(f4, 2, 4, "weight gradients")) != MOE_OK) return s;
-  const void* in[] = {grad_y, r, x, grad_residual, weight, post_weight};
-  const void* out[] = {grad_x, grad_residual_out, grad_weight, grad_post_weight};
-  for (const void* i : in)
-    for (const void* o : out)
-      if (i && i == o) return fail(MOE_ERR_INVALID_ARGUMENT, "an output aliases an input");
-  if ((s = check_distinct(out, 4)) != MOE_OK) return s;
-  s = check_workspace(workspace, workspace_bytes, moe_rms_norm_backward_workspace_bytes(n, d));
-  if (s != MOE_OK) return s;
+  const size_t need = moe_rms_norm_backward_workspace_bytes(n, d);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return s;
+  const size_t m = (size_t)n * d, sm = m * (sf ? 4 : 2), wm = (size_t)d * (wf ? 4 : 2);
+  const Span in[] = {{grad_y, m * 2}, {r, sm}, {x, m * 2}, {grad_residual, sm}, {weight, wm},
+                     {post_weight, wm}};
+  const Span out[] = {{grad_x, m * 2}, {grad_residual_out, sm}, {grad_weight, (size_t)d * 4},
+                      {grad_post_weight, (size_t)d * 4}, {workspace, need}};
+  if ((s = check_alias(in, out)) != MOE_OK) return s;
   return done(moe::launch_rms_norm_grad(grad_y, r, x, grad_residual, weight, post_weight, n, d,
                                         eps, sf, wf, grad_x, grad_residual_out, grad_weight,
                                         grad_post_weight, (float*)workspace, (hipStream_t)stream),
@@ -452,10 +476,13 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_ids,
     return fail(MOE_ERR_INVALID_ARGUMENT, "topk_ids or counts_in is required");
   const void* p4[] = {logits, topk_ids, counts_in, seg_begin, seg_end, loss, counts_out, mean_scores};
   if ((s = check_aligned(p4, 8, 4, "buffers")) != MOE_OK) return s;
-  if (counts_in && counts_in == counts_out)
-    return fail(MOE_ERR_INVALID_ARGUMENT, "counts_out aliases counts_in");
-  s = check_workspace(workspace, workspace_bytes, moe_balance_workspace_bytes(N, E, n_seg));
-  if (s != MOE_OK) return s;
+  const size_t need = moe_balance_workspace_bytes(N, E, n_seg);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return s;
+  const size_t gb = (size_t)n_seg * 4, cb = gb * E;
+  const Span in[] = {{logits, (size_t)N * E * 4}, {topk_ids, (size_t)N * K * 4}, {counts_in, cb},
+                     {seg_begin, gb}, {seg_end, gb}};
+  const Span out[] = {{loss, 4}, {counts_out, cb}, {mean_scores, cb}, {workspace, need}};
+  if ((s = check_alias(in, out)) != MOE_OK) return s;
   size_t bytes;
   const moe::BalanceWork w = carve_balance(workspace, N, E, n_seg, &bytes);
   return done(moe::launch_balance_loss(logits, topk_ids, counts_in, seg_begin, seg_end, N, E, K,
@@ -476,8 +503,11 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
     return fail(MOE_ERR_INVALID_ARGUMENT, "logits, counts and grad_logits_out are required");
   const void* p4[] = {logits, counts, seg_begin, seg_end, grad_loss, grad_logits, grad_logits_out};
   if ((s = check_aligned(p4, 7, 4, "buffers")) != MOE_OK) return s;
-  if (grad_logits_out == logits)
-    return fail(MOE_ERR_INVALID_ARGUMENT, "grad_logits_out must not be logits");
+  const size_t zb = (size_t)N * E * 4, gb = (size_t)n_seg * 4;
+  const Span in[] = {{logits, zb}, {counts, gb * E}, {seg_begin, gb}, {seg_end, gb},
+                     {grad_loss, 4}, {grad_logits, zb, true}};
+  const Span out[] = {{grad_logits_out, zb, true}};
+  if ((s = check_alias(in, out)) != MOE_OK) return s;
   return done(moe::launch_balance_grad(logits, counts, seg_begin, seg_end, N, E, n_seg, score, coef,
                                        grad_loss, grad_logits, grad_logits_out,
                                        (hipStream_t)stream),
