@@ -89,6 +89,36 @@ def test_backward_aliases(lib, page):
     assert refused(lib, call(ws=at["g.w_down"]), "two outputs")
 
 
+def test_backward_refusals_name_their_reason(lib, page):
+    """Every requirement of the header, one at a time."""
+    call, at = backward_call(lib, page)
+    assert call() == OK_TO_LAUNCH
+    for n in ("x", "dy", "z", "ids"):
+        assert refused(lib, call(**{n: None}), "are required"), n
+    for n in ("w_gate", "w_up", "w_down", "g_x", "g_logits", "g_w_gate", "g_w_up", "g_w_down"):
+        assert refused(lib, call(**{n: None}), "routed expert weights and the gradients"), n
+    for n in ("ws_gate", "ws_up", "ws_down"):
+        assert refused(lib, call(**{n: None}), "shared expert weights"), n
+        assert refused(lib, call(**{"g_" + n: None}), "shared expert weights"), n
+    assert refused(lib, call(w_router=None), "both or neither")
+    assert refused(lib, call(g_w_router=None), "both or neither")
+    assert call(w_router=None, g_w_router=None) == OK_TO_LAUNCH
+    for n in ("x", "dy", *WEIGHTS):
+        assert refused(lib, call(**{n: at[n] + 8}), "bf16 inputs must be 16-byte aligned"), n
+    for n in ("x", *WEIGHTS):
+        status = call(**{"g_" + n: at["g." + n] + 8})
+        assert refused(lib, status, "bf16 gradients must be 16-byte aligned"), n
+    for n in ("z", "ids", "gz"):
+        assert refused(lib, call(**{n: at[n] + 2}), "logits and ids must be 4-byte aligned"), n
+    assert refused(lib, call(g_logits=at["g.logits"] + 2), "logits and ids must be 4-byte")
+    assert refused(lib, call(flags=4), "row-major weights only")
+    assert refused(lib, call(flags=16), "unknown flag bits")
+    assert call(flags=11) == OK_TO_LAUNCH                     # the forward call's routing flags
+    assert refused(lib, call(ws=None), "workspace must be non-NULL and 256-byte aligned")
+    assert refused(lib, call(ws=at["ws"] + 4), "workspace must be non-NULL and 256-byte aligned")
+    assert call(wsb=64) == 3
+
+
 # ---------------------------------------------------------------- balance loss
 def balance_calls(lib, page):
     names = ["z", "ids", "cin", "b", "e", "loss", "cout", "mean", "gl", "gin", "out", "ws"]
