@@ -469,7 +469,8 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *  grad_x       [n,d] bf16 out or NULL.
  *  grad_residual_out [n,d] out or NULL, in the stream's type.
  *  grad_weight, grad_post_weight [d] fp32 out or NULL (the latter with
- *               post_weight only).  n = 0 gives zeros.
+ *               post_weight only).  n = 0 gives zeros; without them
+ *               a call of no rows does nothing.
  *  workspace    moe_rms_norm_backward_workspace_bytes(n, d) bytes, 256-byte
  *               aligned; 0 from the query means n or d out of range.
  * No output, nor the workspace, may share memory with an input or another

@@ -429,6 +429,8 @@ moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const 
     return fail(MOE_ERR_INVALID_ARGUMENT, "x belongs to post_weight: both or neither");
   if (grad_post_weight && !post_weight)
     return fail(MOE_ERR_INVALID_ARGUMENT, "grad_post_weight needs post_weight");
+  // the gradients of no rows are empty (and may be NULL); those of the weights are zeros
+  if (n == 0 && !grad_weight && !grad_post_weight) return moe::set_error(MOE_OK, "");
   if (!grad_x && !grad_residual_out && !grad_weight && !grad_post_weight)
     return fail(MOE_ERR_INVALID_ARGUMENT, "an output is required");
   const bool sf = (flags & MOE_NORM_STREAM_F32) != 0, wf = (flags & MOE_NORM_WEIGHT_F32) != 0;

@@ -202,3 +202,20 @@ def test_norm_aliases(lib, page):
             if q != o:
                 assert refused(lib, backward(**{o: at[q]}), "two outputs"), (o, q)
     assert refused(lib, backward(dr=at["dx"] + 256), "two outputs")
+
+
+def test_norm_backward_of_no_rows(lib, page):
+    """n = 0: with weight gradients they are zeros (a launch), without there is
+    nothing to write; an empty tensor's address is NULL."""
+    _, backward, at = norm_calls(lib, page)
+    rows = {k: None for k in ("dy", "r", "x", "dres", "dx", "dr")}
+    assert backward(n=0, **rows, dw=None, dp=None) == 0
+    assert backward(n=0, **rows, dw=None, dp=None, post=None) == 0
+    assert backward(n=0, dw=None, dp=None, post=None, x=None) == 0
+    assert backward(n=0, **rows) == OK_TO_LAUNCH
+    assert backward(n=0, **rows, dp=None) == OK_TO_LAUNCH
+    # what is refused for rows is refused without them
+    assert refused(lib, backward(n=0, **rows, dw=None, dp=None, w=None), "weight is required")
+    assert refused(lib, backward(n=0, **rows, dw=None, post=None), "needs post_weight")
+    assert refused(lib, backward(n=0, **rows, dw=None, dp=None, eps=-1.0), "eps")
+    assert refused(lib, backward(dx=None, dr=None, dw=None, dp=None), "an output is required")
