@@ -448,7 +448,8 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *               d % 128 == 0 and every buffer except scales 16-byte aligned.
  * At least one output; none shares memory with an input or another output, but
  * for residual_out and residual.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
- * row of zeros with eps = 0 has no norm).  bf16 buffers 2-byte, fp32 buffers
+ * row of zeros with eps = 0 has no norm; the mean squares are fp32, which holds
+ * them for rows from 2^-49 to 2^56).  bf16 buffers 2-byte, fp32 buffers
  * 4-byte aligned; 16-byte aligned buffers and d % 8 == 0 take the fast path.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
  *

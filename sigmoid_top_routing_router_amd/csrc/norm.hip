@@ -358,14 +358,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
       }
     row_sums<WAVE>(s, part[flip][0]);
     const float ra = rsqrtf(s[0] * inv_d + a.eps);
-    const float k1 = ra * ra * ra * s[1] * inv_d;  // a n mean(h n) = r k1
+    // the mean first: n and mean(h n) have the sizes of 1 and h at any scale of
+    // r, a^3 leaves fp32 below 1e-13 and above 1e12
+    const float mean1 = ra * s[1] * inv_d;  // mean(h n)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * threads + t) * VEC;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        dw[j][i] += g[j][i] * (r[j][i] * ra);
-        r[j][i] = q[j][i] + (ra * (g[j][i] * w[j][i]) - r[j][i] * k1);  // dr from here on
+        const float n = r[j][i] * ra;
+        dw[j][i] += g[j][i] * n;
+        r[j][i] = q[j][i] + ra * (g[j][i] * w[j][i] - n * mean1);  // dr from here on
       }
       if (c < d) {
         if (a.dr_out) {
@@ -386,15 +389,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_grad_kernel(NormGradAr
         }
       row_sums<WAVE>(p, part[flip][1]);
       const float rb = rsqrtf(p[0] * inv_d + a.eps);
-      const float k2 = rb * rb * rb * p[1] * inv_d;
+      const float mean2 = rb * p[1] * inv_d;  // mean(k m)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * threads + t) * VEC;
         float o[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          dp[j][i] += r[j][i] * (xs[j][i] * rb);
-          o[i] = rb * (r[j][i] * pw[j][i]) - xs[j][i] * k2;
+          const float m = xs[j][i] * rb;
+          dp[j][i] += r[j][i] * m;
+          o[i] = rb * (r[j][i] * pw[j][i] - m * mean2);
         }
         if (c < d && a.dx) store_bf16<VEC>(a.dx + base + c, o);
       }
