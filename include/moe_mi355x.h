@@ -504,7 +504,9 @@ moe_status_t moe_rms_norm_backward(const uint16_t* grad_y, const void* r, const 
  *   p = sigma(z)                     MOE_SCORE_SIGMOID (the layer's scores),
  *   p = sigma(z) / sum_e sigma(z)    MOE_SCORE_SIGMOID_NORM,
  *   p = softmax(z)                   MOE_SCORE_SOFTMAX.
- * An empty segment contributes 0 and still counts in n_seg.
+ * An empty segment contributes 0 and still counts in n_seg.  A logit of -inf has
+ * the score 0; a row with no other has neither of the last two scores (NaN, as
+ * has a row with a NaN or, for softmax, with +inf).
  *
  *  logits       [N,E] fp32; rows outside every segment are not used, whatever
  *               they hold.

@@ -38,9 +38,13 @@ def balance_scores(z, score):
     if score == "softmax":
         e = np.exp(z - z.max(axis=1, keepdims=True))
         return e / e.sum(axis=1, keepdims=True)
-    s = np.where(z >= 0, 1.0 / (1.0 + np.exp(-np.abs(z))),
-                 np.exp(-np.abs(z)) / (1.0 + np.exp(-np.abs(z))))
-    return s / s.sum(axis=1, keepdims=True) if score == "sigmoid_norm" else s
+    if score == "sigmoid_norm":
+        # log sigma relative to the row's largest, so that no row's sum is zero
+        log = np.minimum(z, 0.0) - np.log1p(np.exp(-np.abs(z)))
+        e = np.exp(log - log.max(axis=1, keepdims=True))
+        return e / e.sum(axis=1, keepdims=True)
+    return np.where(z >= 0, 1.0 / (1.0 + np.exp(-np.abs(z))),
+                    np.exp(-np.abs(z)) / (1.0 + np.exp(-np.abs(z))))
 
 
 def segment_counts(ids, E, spans):

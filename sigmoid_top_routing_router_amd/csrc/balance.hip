@@ -129,18 +129,30 @@ __device__ __forceinline__ void scores(float (&v)[NC][4], float (&slope)[NC][4])
 #pragma unroll
       for (int i = 0; i < 4; ++i) slope[j][i] = v[j][i] = v[j][i] * inv;
   } else {
+    // The normalised scores of a row below zero are taken exp(-m) times as large
+    // (m: its largest logit): far below, every sigma of it would be zero.
+    float m = 0.0f;
+    if constexpr (SCORE == kSigmoidNorm) {
+      m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, v[j][i]);
+      m = fminf(row16_max_f32(m), 0.0f);
+    }
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // e = exp(-|z|) keeps sigma and sigma (1 - sigma) = e / (1 + e)^2
-        // exact to a few ulp for either sign
+        // exact to a few ulp for either sign; n is e, or where m < 0, exp(z - m)
         const float z = v[j][i];
         const float e = __expf(-fabsf(z));
+        const float n = SCORE == kSigmoidNorm ? __expf(-fabsf(z) - m) : e;
         const float q = __builtin_amdgcn_rcpf(1.0f + e);
-        v[j][i] = z >= 0.0f ? q : e * q;
-        slope[j][i] = e * q * q;
+        v[j][i] = z >= 0.0f ? q : n * q;
+        slope[j][i] = n * q * q;
         s += v[j][i];
       }
     if constexpr (SCORE == kSigmoidNorm) {
