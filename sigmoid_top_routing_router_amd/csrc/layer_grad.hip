@@ -121,17 +121,21 @@ constexpr uint32_t kNoAddr = kGradMaxOperandBytes;
 // LDS-DMA: 16 (dma4: 4) bytes per lane from a buffer to LDS at `at` + 16 (4) *
 // lane.  Counted on vmcnt; the waits are this file's own (wait_vmcnt).  m0 (the
 // LDS address) is set and used inside; nothing else in these kernels uses it.
+// The first load of a block waits for m0 (one wait state) and for the scalar
+// registers that v_readfirstlane may have written right in front of it (five):
+// the compiler counts these for its own instructions only.
+#define MOE_DMA_OPEN "s_mov_b32 m0, %0\n\ts_nop 3\n\t"
 #define MOE_DMA16_NEXT(v, r) "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 " v ", " r
 __device__ __forceinline__ void dma4(i32x4_t r, uint32_t off, int at) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know these operands
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile(MOE_DMA_OPEN "buffer_load_dword %1, %2, 0 offen lds"
                :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(r) : "memory");
 #endif
 }
 // Four loads, each 1 KB after the other in LDS, at off + soff of the buffer.
 __device__ __forceinline__ void dma_4(i32x4_t r, const uint32_t (&v)[4], uint32_t soff, int at) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
+  asm volatile(MOE_DMA_OPEN "buffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
                MOE_DMA16_NEXT("%2", "%5, %6 offen lds\n\t")
                MOE_DMA16_NEXT("%3", "%5, %6 offen lds\n\t")
                MOE_DMA16_NEXT("%4", "%5, %6 offen lds")
@@ -143,7 +147,7 @@ __device__ __forceinline__ void dma_4(i32x4_t r, const uint32_t (&v)[4], uint32_
 // Two loads of one buffer.
 __device__ __forceinline__ void dma_2(i32x4_t r, const uint32_t (&v)[2], int at) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+  asm volatile(MOE_DMA_OPEN "buffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
                MOE_DMA16_NEXT("%2", "%3, 0 offen lds")
                :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(v[0]), "v"(v[1]), "s"(r)
                : "memory", "scc");
