@@ -67,11 +67,15 @@ def _dev(t, name, dtype=None, shape=None):
 
 def _stream(stream):
     torch = _torch()
-    if stream is not None:
-        return C.c_void_p(stream.cuda_stream)
-    # the handle of torch.cuda.current_stream() without its object (0.5 us a
-    # call instead of 2.9, of the 13 that a small call takes on the host)
-    return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if stream is None:
+        # the handle of torch.cuda.current_stream() without its object (0.5 us a
+        # call instead of 2.9, of the 13 that a small call takes on the host);
+        # not a public name of torch's, so it may be missing
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return C.c_void_p(raw(torch.cuda.current_device()))
+        stream = torch.cuda.current_stream()
+    return C.c_void_p(stream.cuda_stream)
 
 
 def _on(stream):
