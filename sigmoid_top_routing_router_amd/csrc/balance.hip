@@ -104,10 +104,12 @@ __device__ __forceinline__ void load_row(const float* __restrict__ Z, int64_t t,
   }
 }
 
-// Logits -> scores p in place; a column past E holds -inf and gets 0.
+// The scores p of row t; a column past E gets 0.
 // slope: dp/dz without the sum over the row (see the formulas above).
-template <int SCORE, int NC>
-__device__ __forceinline__ void scores(float (&v)[NC][4], float (&slope)[NC][4]) {
+template <int SCORE, int NC, bool QUADS>
+__device__ __forceinline__ void scores(const float* __restrict__ Z, int64_t t, int E, int l16,
+                                       bool vec, float (&v)[NC][4], float (&slope)[NC][4]) {
+  load_row<NC, QUADS>(Z, t, E, l16, vec, -INFINITY, v);
   if constexpr (SCORE == kSoftmax) {
     float m = -INFINITY;
 #pragma unroll
@@ -129,34 +131,46 @@ __device__ __forceinline__ void scores(float (&v)[NC][4], float (&slope)[NC][4])
 #pragma unroll
       for (int i = 0; i < 4; ++i) slope[j][i] = v[j][i] = v[j][i] * inv;
   } else {
-    // The normalised scores of a row below zero are taken exp(-m) times as large
-    // (m: its largest logit): far below, every sigma of it would be zero.
-    float m = 0.0f;
-    if constexpr (SCORE == kSigmoidNorm) {
-      m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = fmaxf(m, v[j][i]);
-      m = fminf(row16_max_f32(m), 0.0f);
-    }
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // e = exp(-|z|) keeps sigma and sigma (1 - sigma) = e / (1 + e)^2
-        // exact to a few ulp for either sign; n is e, or where m < 0, exp(z - m)
+        // exact to a few ulp for either sign
         const float z = v[j][i];
         const float e = __expf(-fabsf(z));
-        const float n = SCORE == kSigmoidNorm ? __expf(-fabsf(z) - m) : e;
         const float q = __builtin_amdgcn_rcpf(1.0f + e);
-        v[j][i] = z >= 0.0f ? q : n * q;
-        slope[j][i] = n * q * q;
+        v[j][i] = z >= 0.0f ? q : e * q;
+        slope[j][i] = e * q * q;
         s += v[j][i];
       }
     if constexpr (SCORE == kSigmoidNorm) {
-      const float inv = 1.0f / row16_sum_f32(s);
+      s = row16_sum_f32(s);
+      // A sum below 1/2: every logit is below zero (far below, every sigma would
+      // be 0).  The row is read again and its scores are taken exp(-m) times as
+      // large, m being its largest logit: sigma exp(-m) = exp(z - m) / (1 + e).
+      if (s < 0.5f) {
+        load_row<NC, QUADS>(Z, t, E, l16, vec, -INFINITY, v);
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = fmaxf(m, v[j][i]);
+        m = row16_max_f32(m);
+        s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float q = __builtin_amdgcn_rcpf(1.0f + __expf(v[j][i]));
+            v[j][i] = __expf(v[j][i] - m) * q;
+            slope[j][i] = v[j][i] * q;
+            s += v[j][i];
+          }
+        s = row16_sum_f32(s);
+      }
+      const float inv = 1.0f / s;
 #pragma unroll
       for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -212,8 +226,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void balance_partial_kernel(
       const int32_t t = t0 + 4 * w + sub;
       if (t < hi) {  // whole DPP rows
         float v[NC][4], slope[NC][4];
-        load_row<NC, QUADS>(Z, t, E, l16, vec, -INFINITY, v);
-        scores<SCORE, NC>(v, slope);
+        scores<SCORE, NC, QUADS>(Z, t, E, l16, vec, v, slope);
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -385,8 +398,7 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(
     const bool inside = gcur >= 0;
     if (inside) {
       float v[NC][4], slope[NC][4];
-      load_row<NC, QUADS>(Z, t, E, l16, vec, -INFINITY, v);
-      scores<SCORE, NC>(v, slope);
+      scores<SCORE, NC, QUADS>(Z, t, E, l16, vec, v, slope);
       float dot = 0.0f;
       if constexpr (SCORE != kSigmoid) {
 #pragma unroll
