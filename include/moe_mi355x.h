@@ -434,8 +434,8 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  * y leaves in bf16 and / or as E4M3 codes with one fp32 scale per 1 x 128
  * group, by the rule of moe_fp8_quantize_rows applied to the fp32 y (not to
  * its bf16 rounding): the x and the codes that moe_forward_fp8_quantized
- * takes.  A group with a NaN has a NaN scale.  r is rounded once, to the stream's type; y is formed from the
- * unrounded r.
+ * takes.  A group with a NaN has a NaN scale.  r is rounded once, to the
+ * stream's type; y is formed from the unrounded r.
  *
  *  x            [n,d] bf16 bits.
  *  residual     [n,d] or NULL: bf16 bits, or fp32 with MOE_NORM_STREAM_F32.
@@ -447,10 +447,11 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_weights_t* w,
  *  codes        [n,d] out or NULL, scales [n,d/128] out (both or neither):
  *               d % 128 == 0 and every buffer except scales 16-byte aligned.
  * At least one output; none shares memory with an input or another output, but
- * for residual_out and residual.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0 finite (a
- * row of zeros with eps = 0 has no norm; the mean squares are fp32, which holds
- * them for rows from 2^-49 to 2^56).  bf16 buffers 2-byte, fp32 buffers
- * 4-byte aligned; 16-byte aligned buffers and d % 8 == 0 take the fast path.
+ * for residual_out and residual.  0 <= n <= 2^27, 1 <= d <= 8192, eps >= 0
+ * finite (a row of zeros with eps = 0 has no norm; the mean squares are fp32,
+ * which holds them for rows from 2^-49 to 2^56).  bf16 buffers 2-byte, fp32
+ * buffers 4-byte aligned; 16-byte aligned buffers and d % 8 == 0 take the fast
+ * path.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
  *
  * moe_rms_norm_backward - gradients of the same function at the stored r:

@@ -15,7 +15,7 @@
 // Rows are read 16 lanes each, four to a wave: a lane holds four columns out
 // of every 64, so a row's reductions stay inside a DPP row and a wave reads
 // four contiguous rows.  Both passes are bound by memory: 65536 x
-// 384 logits in 16 segments, 100 MB read in 27 us (3.7 TB/s, what a plain
+// 384 logits in 16 segments, 100 MB read in 25 us (4.0 TB/s, what a plain
 // reduction reaches); the gradient added to one that is there, 302 MB in 67 us
 // (4.5 TB/s, a copy's rate).
 //

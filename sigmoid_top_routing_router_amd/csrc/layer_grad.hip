@@ -51,9 +51,11 @@
 // results share: dx loads 7.3 GB into LDS and stores 1.2 (9.7 TB/s; loads
 // alone reach some 12), the weights' gradients load 10.7 GB and store 3.0 (9.3
 // TB/s).  Of the latter, MFMAs and LDS reads alone take 0.60 ms, without stores
-// 0.77, loads and stores without MFMAs 1.3.  128 x 256 tiles, two blocks,
-// against one block of eight waves and 256 x 256: weights 1.48 ms against 1.67,
-// Q 0.40 against 0.43 (bf16 parts: dx 0.80 against 0.84).
+// 0.77, loads and stores without MFMAs 1.3.  Two blocks of 128 x 256 a CU came
+// together with a sixth of the address work, non-temporal stores and this order
+// of items, in the place of one block of 256 x 256: weights 1.48 ms after 1.67, Q
+// 0.40 after 0.43 (bf16 parts: dx 0.80 after 0.84).  What the tile's shape alone
+// gives was not measured; 256 x 256 would load two thirds as much into LDS.
 #include <type_traits>
 
 #include "common.h"

@@ -519,7 +519,8 @@ hipError_t launch_rms_norm(const uint16_t* x, const void* residual, const void* 
 // whole number of blocks (16384 x 2560, sandwich, five waves a row: 138 us with
 // 512 blocks, 161 with 1024, 176 with 256), two rows each or more (256 x 2560:
 // 7 us, with four rows 10, with eight 16).  Rows of a wave: up to four blocks a
-// CU (65536 x 256: 27 us with 1024 blocks, 38 with 512, 28 with 2048).
+// CU (65536 x 256: 27 us with 1024 blocks, 38 with 512, 28 with 2048).  Measured
+// at these two widths only; the others follow from the waves a CU holds.
 int rms_norm_grad_blocks(int64_t n, int d) {
   const bool wave = d <= kWaveD;
   const int waves = (d + 511) / 512;
