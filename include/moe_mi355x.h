@@ -618,6 +618,135 @@ moe_status_t moe_backward(const moe_problem_t* p, const moe_weights_t* w, const 
                           size_t workspace_bytes, void* stream);
 
 /*
+ * The layer taken apart: tokens sorted by expert and back, for callers whose
+ * experts are their own or lie on several GPUs ([K1D] "Routing": tokens are
+ * brought to their experts with no per-expert capacity), with the gradients,
+ * and with activations kept in 8 bits for the backward pass.
+ *
+ * moe_group - the stable grouping of the N*K pairs (t,k) by expert that
+ * moe_forward makes (aux counts, offsets, sorted_src, src_pos), for ids that may
+ * lie outside [0,E): such a pair (an expert on another GPU, a dropped one) is
+ * not counted and has no place.  An expert may occur twice in a token.
+ *
+ *  topk_ids     [N,K] int32.
+ *  counts       [E] int32 out: the loads.
+ *  offsets      [E+1] int32 out: exclusive sums of counts; offsets[E] is the
+ *               number of sorted rows.
+ *  sorted_src   [N*K] int32 out: pair index t*K+k, grouped by expert, ascending;
+ *               -1 from offsets[E] on.
+ *  src_pos      [N,K] int32 out: every pair's place among the sorted rows, or -1.
+ *  workspace    moe_group_workspace_bytes(N, E, K) bytes, 256-byte aligned; 0
+ *               from the query means a size out of range.
+ * 0 <= N <= 2^24, 1 <= E <= 384, 1 <= K <= 8 (K may exceed E).
+ *
+ * The four calls below take that src_pos; a place outside [0, N*K) means no
+ * place, and places must not repeat.  Rows are bf16, or fp32 with MOE_ROWS_F32
+ * (x, rows, y, base and their gradients alike).  0 <= N <= 2^24, 1 <= d <= 8192,
+ * 1 <= K <= 8.  Rows that no pair has (from offsets[E] on) are neither read
+ * nor written.  Sums are fp32 and rounded once.  bf16 buffers 2-byte, fp32
+ * buffers 4-byte aligned; 16-byte aligned buffers and rows of whole 16-byte
+ * words take the fast path.
+ *
+ * Rows kept in 8 bits are E4M3 codes [n,d] with fp32 scales [n,d/128], as
+ * moe_fp8_quantize_rows and moe_rms_norm write them: d % 128 == 0, not with
+ * MOE_ROWS_F32, every buffer but scales, weights and src_pos 16-byte aligned.
+ *
+ * moe_permute - rows[src_pos[t,k]] = x[t].
+ *  x            [N,d]; with x_scales (else NULL) its E4M3 codes: the experts'
+ *               inputs formed again in the backward pass, rounded to bf16.
+ *  rows         [N*K,d] out.
+ *
+ * moe_permute_backward - grad_x[t] = sum_k grad_rows[src_pos[t,k]].
+ *
+ * moe_unpermute - y[t] = base[t] + sum_k weights[t,k] rows[src_pos[t,k]] (the
+ * combine of [KPT] §6.1).
+ *  weights      [N,K] fp32 or NULL (1); base [N,d] or NULL (0).
+ *  codes, scales  [N*K,d] and [N*K,d/128] out, or both NULL: the rows that were
+ *               read, kept in 8 bits for moe_unpermute_backward.  A group with
+ *               an infinity or a NaN has a scale that is not finite.
+ *
+ * moe_unpermute_backward - grad_rows[src_pos[t,k]] = weights[t,k] grad_y[t],
+ * grad_weights[t,k] = <grad_y[t], rows[src_pos[t,k]]> (0 without a place); the
+ * gradient of base is grad_y.
+ *  rows         [N*K,d], with row_scales (else NULL) their codes; needed for
+ *               grad_weights only.
+ *  grad_rows, grad_weights  [N*K,d] and [N,K] fp32 out, either may be NULL.
+ *
+ * No output, nor the workspace, may share memory with an input or another
+ * output.  Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, WORKSPACE_TOO_SMALL,
+ * HIP.
+ */
+#define MOE_ROWS_F32 0x1u
+size_t moe_group_workspace_bytes(int64_t N, int32_t E, int32_t K);
+moe_status_t moe_group(const int32_t* topk_ids, int64_t N, int32_t E, int32_t K, int32_t* counts,
+                       int32_t* offsets, int32_t* sorted_src, int32_t* src_pos, void* workspace,
+                       size_t workspace_bytes, void* stream);
+moe_status_t moe_permute(const void* x, const float* x_scales, const int32_t* src_pos, int64_t N,
+                         int32_t d, int32_t K, uint32_t flags, void* rows, void* stream);
+moe_status_t moe_permute_backward(const void* grad_rows, const int32_t* src_pos, int64_t N,
+                                  int32_t d, int32_t K, uint32_t flags, void* grad_x,
+                                  void* stream);
+moe_status_t moe_unpermute(const void* rows, const int32_t* src_pos, const float* weights,
+                           const void* base, int64_t N, int32_t d, int32_t K, uint32_t flags,
+                           void* y, uint8_t* codes, float* scales, void* stream);
+moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const float* row_scales,
+                                    const int32_t* src_pos, const float* weights, int64_t N,
+                                    int32_t d, int32_t K, uint32_t flags, void* grad_rows,
+                                    float* grad_weights, void* stream);
+
+/*
+ * 8-bit integer products with a scale for each row and each output channel
+ * (beside the E4M3 path: one scale a row instead of one per 128 values, sums
+ * that are exact), dense or over the sorted rows of the experts.
+ *
+ * moe_int8_quantize_rows - bf16 rows x [n,cols] -> integers codes [n,cols] and
+ * scales [n]: s = fp32(amax) / 127, code = x / s rounded to nearest even, in
+ * [-127, 127]; a row of zeros has s = 0 and zeros.  A row with an infinity or
+ * a NaN has the scale NaN and zeros.  Weights [E,cols,k] are quantised as
+ * E*cols rows of k: a scale for each output channel.  n >= 0, cols % 16 == 0
+ * (16 <= cols <= 65536); x and codes 16-byte aligned.
+ *
+ * moe_int8_matmul - out[r,c] = a_scales[s] w_scales[e,c] sum_k a[s,k] w[e,c,k],
+ * rounded to bf16; with w_up silu(out) times the same of w_up, formed in fp32.
+ *  a            [a_rows,k] integers (-128 too), a_scales [a_rows] fp32.
+ *  w            [E,cols,k] integers, w_scales [E,cols] fp32; w_up, w_up_scales
+ *               the same or both NULL.
+ *  offsets      [E+1] int32 (moe_group): rows offsets[e] .. offsets[e+1]-1 are
+ *               expert e's; rows outside are not written.  NULL: E = 1, every
+ *               row is its.  Bounds are clamped to [0, rows]; offsets that do
+ *               not ascend give unspecified rows and no access out of range.
+ *  sorted_src   [rows] int32 (moe_group; with offsets only): row r multiplies
+ *               a's row sorted_src[r] / K (clamped to a's rows).  NULL: a's row
+ *               r, and a_rows = rows.
+ *  out          [rows,cols] bf16 bits.
+ * 0 <= rows <= 2^27, a_rows likewise; 1 <= E <= 384; k % 16 == 0 (16 <= k <=
+ * 65536); cols % 8 == 0 (8 <= cols <= 65536); 1 <= K <= 8.  a, w, w_up and out
+ * 16-byte aligned, the others 4-byte.  The output shares memory with no input.
+ * The first call on a device sets the kernels' LDS attributes: make one
+ * uncaptured call before capturing.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.
+ */
+typedef struct {
+  int64_t a_rows;
+  int64_t rows;
+  int32_t k;
+  int32_t cols;
+  int32_t E;
+  int32_t K;
+  const int8_t* a;
+  const float* a_scales;
+  const int8_t* w;
+  const float* w_scales;
+  const int8_t* w_up;
+  const float* w_up_scales;
+  const int32_t* offsets;
+  const int32_t* sorted_src;
+} moe_int8_matmul_t;
+moe_status_t moe_int8_quantize_rows(const uint16_t* x, int64_t n, int32_t cols, int8_t* codes,
+                                    float* scales, void* stream);
+moe_status_t moe_int8_matmul(const moe_int8_matmul_t* p, uint16_t* out, void* stream);
+
+/*
  * Stage timing (a profiling aid).  moe_stage_timing(1): every moe_forward
  * call records a HIP timing event on its stream at each stage boundary;
  * moe_stage_timing(2): only the two events around stage 3 (the routed

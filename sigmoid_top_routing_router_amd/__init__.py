@@ -26,7 +26,9 @@ __all__ = ["route", "eqb_bias", "eqb_workspace_bytes", "EqbState", "eqb_bias_par
            "ExpertWeights", "MoeError", "load_library", "stage_timing", "stage_times",
            "forward_noalloc", "pack_gateup", "pack_gateup_weights", "rms_norm",
            "rms_norm_backward", "balance_loss", "balance_loss_backward", "backward",
-           "backward_workspace_bytes"]
+           "backward_workspace_bytes", "Grouping", "group_tokens", "permute",
+           "permute_backward", "unpermute", "unpermute_backward", "int8_quantize_rows",
+           "int8_matmul"]
 
 AUX_FIELDS = [f for f, _ in MoeAux._fields_]
 
@@ -825,6 +827,275 @@ def balance_loss_backward(logits, counts, coef: float = 1e-2, score: str = "sigm
         _lib.check(lib.moe_balance_loss_backward(
             _ptr(logits), _ptr(counts), _ptr(begin), _ptr(end), N, E, n_seg, which, coef,
             _ptr(grad_loss), _ptr(grad_logits), _ptr(out), _stream(stream)))
+    return out
+
+
+@dataclass
+class Grouping:
+    """The (token, slot) pairs of a batch grouped by expert (int32 torch tensors
+    on the GPU), from ``group_tokens`` or the aux outputs of ``forward``."""
+    counts: object      # [E] loads
+    offsets: object     # [E + 1] first row of every expert; offsets[E]: sorted rows
+    sorted_src: object  # [N*K] pair t*K + k of every sorted row, -1 behind the last
+    src_pos: object     # [N, K] sorted row of every pair, -1 without one
+
+
+def group_tokens(topk_ids, E: int, workspace=None, stream=None) -> Grouping:
+    """Stable grouping of the pairs of topk_ids (int32 [N, K]) by expert
+    (moe_group).  Ids outside [0, E) (experts on other GPUs, dropped pairs) have
+    no place."""
+    torch = _torch()
+    lib = _lib.load()
+    topk_ids = _dev(topk_ids, "topk_ids", torch.int32)
+    if topk_ids is None or topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [N, K]")
+    N, K = topk_ids.shape
+    _one_device(topk_ids, workspace=workspace)
+    with _on_device(topk_ids, stream):
+        dev = topk_ids.device
+        counts = torch.empty((E,), dtype=torch.int32, device=dev)
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        sorted_src = torch.empty((N * K,), dtype=torch.int32, device=dev)
+        src_pos = torch.empty((N, K), dtype=torch.int32, device=dev)
+        if workspace is None:
+            need = int(lib.moe_group_workspace_bytes(N, E, K))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _lib.check(lib.moe_group(_ptr(topk_ids), N, E, K, _ptr(counts), _ptr(offsets),
+                                 _ptr(sorted_src), _ptr(src_pos), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+    return Grouping(counts, offsets, sorted_src, src_pos)
+
+
+def _places(grouping):
+    pos = _dev(grouping.src_pos, "src_pos", _torch().int32)
+    if pos is None or pos.dim() != 2:
+        raise ValueError("src_pos must be [N, K]")
+    return pos
+
+
+def _row_types():
+    return (*_bf16(), _torch().float32)
+
+
+def _kept(pair, name, shape):
+    """(codes, scales) of rows kept in 8 bits."""
+    torch = _torch()
+    n, d = shape
+    codes = _dev(pair[0], f"{name} codes", torch.uint8, shape)
+    scales = _dev(pair[1], f"{name} scales", torch.float32, (n, d // 128))
+    if codes is None or scales is None:
+        raise ValueError(f"{name}: codes and scales, both")
+    return codes, scales
+
+
+def _rows_flag(t):
+    return _lib.MOE_ROWS_F32 if t.dtype == _torch().float32 else 0
+
+
+def permute(x, grouping: Grouping, out=None, stream=None):
+    """Rows of tokens sorted by expert (moe_permute): rows[src_pos[t, k]] = x[t].
+    x: [N, d] bf16 or fp32, or (codes, scales) of tokens kept in 8 bits
+    (``fp8_quantize_rows``, ``rms_norm(..., quantize=True)``), which gives bf16
+    rows.  Returns rows [N*K, d]; those from offsets[E] on keep what ``out``
+    held (without it they are unspecified)."""
+    torch = _torch()
+    lib = _lib.load()
+    pos = _places(grouping)
+    N, K = pos.shape
+    scales, flags = None, 0
+    if isinstance(x, (tuple, list)):
+        if not isinstance(x[0], torch.Tensor) or x[0].dim() != 2 or x[0].shape[0] != N:
+            raise ValueError(f"x codes must be [{N}, d]")
+        x, scales = _kept(x, "x", tuple(x[0].shape))
+        dtype = (torch.bfloat16, torch.uint16, torch.int16)
+    else:
+        x = _dev(x, "x", _row_types())
+        if x is None or x.dim() != 2 or x.shape[0] != N:
+            raise ValueError(f"x must be [{N}, d]")
+        flags, dtype = _rows_flag(x), x.dtype
+    d = x.shape[1]
+    out = _dev(out, "out", dtype, (N * K, d))
+    _one_device(x, src_pos=pos, x_scales=scales, out=out)
+    with _on_device(x, stream):
+        if out is None:
+            out = torch.empty((N * K, d), dtype=torch.bfloat16 if scales is not None else dtype,
+                              device=x.device)
+        _lib.check(lib.moe_permute(_ptr(x), _ptr(scales), _ptr(pos), N, d, K, flags, _ptr(out),
+                                   _stream(stream)))
+    return out
+
+
+def permute_backward(grad_rows, grouping: Grouping, stream=None):
+    """Gradient of permute (moe_permute_backward): grad_x[t] = sum_k
+    grad_rows[src_pos[t, k]], [N, d] in the type of grad_rows [N*K, d]."""
+    torch = _torch()
+    lib = _lib.load()
+    pos = _places(grouping)
+    N, K = pos.shape
+    grad_rows = _dev(grad_rows, "grad_rows", _row_types())
+    if grad_rows is None or grad_rows.dim() != 2 or grad_rows.shape[0] != N * K:
+        raise ValueError(f"grad_rows must be [{N * K}, d]")
+    d = grad_rows.shape[1]
+    _one_device(grad_rows, src_pos=pos)
+    with _on_device(grad_rows, stream):
+        grad_x = torch.empty((N, d), dtype=grad_rows.dtype, device=grad_rows.device)
+        _lib.check(lib.moe_permute_backward(_ptr(grad_rows), _ptr(pos), N, d, K,
+                                            _rows_flag(grad_rows), _ptr(grad_x),
+                                            _stream(stream)))
+    return grad_x
+
+
+def unpermute(rows, grouping: Grouping, weights=None, base=None, checkpoint: bool = False,
+              stream=None):
+    """The experts' rows back to their tokens (moe_unpermute): y[t] = base[t] +
+    sum_k weights[t, k] rows[src_pos[t, k]].  rows: [N*K, d] bf16 or fp32; base
+    [N, d] of that type or None; weights fp32 [N, K] or None (1).
+
+    Returns (y [N, d], kept): with ``checkpoint`` (bf16 rows, d % 128 == 0)
+    kept = (codes uint8 [N*K, d], scales fp32 [N*K, d/128]), the rows in 8 bits
+    for unpermute_backward, else None."""
+    torch = _torch()
+    lib = _lib.load()
+    pos = _places(grouping)
+    N, K = pos.shape
+    rows = _dev(rows, "rows", _row_types())
+    if rows is None or rows.dim() != 2 or rows.shape[0] != N * K:
+        raise ValueError(f"rows must be [{N * K}, d]")
+    d = rows.shape[1]
+    weights = _dev(weights, "weights", torch.float32, (N, K))
+    base = _dev(base, "base", rows.dtype, (N, d))
+    _one_device(rows, src_pos=pos, weights=weights, base=base)
+    with _on_device(rows, stream):
+        dev = rows.device
+        y = torch.empty((N, d), dtype=rows.dtype, device=dev)
+        codes = scales = None
+        if checkpoint:
+            codes = torch.empty((N * K, d), dtype=torch.uint8, device=dev)
+            scales = torch.empty((N * K, d // 128), dtype=torch.float32, device=dev)
+        _lib.check(lib.moe_unpermute(_ptr(rows), _ptr(pos), _ptr(weights), _ptr(base), N, d, K,
+                                     _rows_flag(rows), _ptr(y), _ptr(codes), _ptr(scales),
+                                     _stream(stream)))
+    return y, (codes, scales) if checkpoint else None
+
+
+def unpermute_backward(grad_y, grouping: Grouping, weights=None, rows=None, out=None,
+                       stream=None):
+    """Gradients of unpermute (moe_unpermute_backward).  grad_y: [N, d] bf16 or
+    fp32 (it is base's gradient as it is); rows: the forward call's [N*K, d], or
+    the (codes, scales) that it kept; None: no gradient of the weights.
+
+    Returns (grad_rows [N*K, d] in the type of grad_y, grad_weights fp32 [N, K]
+    or None); grad_rows from offsets[E] on keep what ``out`` held (without it
+    they are unspecified)."""
+    torch = _torch()
+    lib = _lib.load()
+    pos = _places(grouping)
+    N, K = pos.shape
+    grad_y = _dev(grad_y, "grad_y", _row_types())
+    if grad_y is None or grad_y.dim() != 2 or grad_y.shape[0] != N:
+        raise ValueError(f"grad_y must be [{N}, d]")
+    d = grad_y.shape[1]
+    weights = _dev(weights, "weights", torch.float32, (N, K))
+    scales = None
+    if isinstance(rows, (tuple, list)):
+        rows, scales = _kept(rows, "rows", (N * K, d))
+    else:
+        rows = _dev(rows, "rows", grad_y.dtype, (N * K, d))
+    out = _dev(out, "out", grad_y.dtype, (N * K, d))
+    _one_device(grad_y, src_pos=pos, weights=weights, rows=rows, row_scales=scales, out=out)
+    with _on_device(grad_y, stream):
+        dev = grad_y.device
+        if out is None:
+            out = torch.empty((N * K, d), dtype=grad_y.dtype, device=dev)
+        dw = None if rows is None else torch.empty((N, K), dtype=torch.float32, device=dev)
+        _lib.check(lib.moe_unpermute_backward(_ptr(grad_y), _ptr(rows), _ptr(scales), _ptr(pos),
+                                              _ptr(weights), N, d, K, _rows_flag(grad_y),
+                                              _ptr(out), _ptr(dw), _stream(stream)))
+    return out, dw
+
+
+def int8_quantize_rows(x, stream=None):
+    """bf16 [..., C] (C % 16 == 0) -> (codes int8 of the same shape, fp32 scales
+    [...]), one scale per row (moe_int8_quantize_rows): tokens [n, C], or
+    weights [E, cols, k] with a scale for each output channel."""
+    torch = _torch()
+    x = _dev(x, "x", _bf16())
+    if x is None or x.dim() < 2:
+        raise ValueError("x must be [..., C]")
+    n, Cc = x.shape[:-1].numel(), x.shape[-1]
+    with _on_device(x, stream):
+        codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _lib.check(_lib.load().moe_int8_quantize_rows(_ptr(x), n, Cc, _ptr(codes), _ptr(scales),
+                                                      _stream(stream)))
+    return codes, scales
+
+
+def _int8_weight(w, name, shape):
+    torch = _torch()
+    codes = _dev(w[0], f"{name} codes", torch.int8, shape)
+    if codes is None or codes.dim() not in (2, 3):
+        raise ValueError(f"{name} codes must be [cols, k] or [E, cols, k]")
+    scales = _dev(w[1], f"{name} scales", torch.float32, tuple(codes.shape[:-1]))
+    if scales is None:
+        raise ValueError(f"{name} scales are required")
+    return codes, scales
+
+
+def int8_matmul(x, w, w_up=None, grouping: Grouping = None, gather: bool = False, out=None,
+                stream=None):
+    """Product in 8-bit integers with a scale for each row and each output
+    channel (moe_int8_matmul), in bf16.  x: (codes int8 [n, k], scales [n]) and
+    w: (codes [cols, k], scales [cols]), as int8_quantize_rows gives them:
+    out = x w^T [n, cols].  With ``w_up``, of w's shape: silu(x w^T) * (x w_up^T).
+
+    With ``grouping`` w is [E, cols, k] and out [N*K, cols]: sorted row r is
+    multiplied with its expert's weight.  x then holds the sorted rows
+    [N*K, k], or with ``gather`` the tokens [N, k], which the product picks by
+    itself.  Rows from offsets[E] on keep what ``out`` held (without it they
+    are unspecified)."""
+    torch = _torch()
+    lib = _lib.load()
+    a = _dev(x[0], "x codes", torch.int8)
+    if a is None or a.dim() != 2:
+        raise ValueError("x codes must be [n, k]")
+    n, k = a.shape
+    sa = _dev(x[1], "x scales", torch.float32, (n,))
+    if sa is None:
+        raise ValueError("x scales are required")
+    wc, ws = _int8_weight(w, "w", None)
+    uc = us = None
+    if w_up is not None:
+        uc, us = _int8_weight(w_up, "w_up", tuple(wc.shape))
+    if wc.dim() != (2 if grouping is None else 3) or wc.shape[-1] != k:
+        raise ValueError(f"w codes have shape {tuple(wc.shape)}, expected "
+                         + (f"(cols, {k})" if grouping is None else f"(E, cols, {k})"))
+    E, cols = (1 if grouping is None else wc.shape[0]), wc.shape[-2]
+    rows, K, offsets, src = n, 1, None, None
+    if grouping is not None:
+        pos = _places(grouping)
+        N, K = pos.shape
+        rows = N * K
+        offsets = _dev(grouping.offsets, "offsets", torch.int32, (E + 1,))
+        if offsets is None:
+            raise ValueError("offsets are required")
+        if n != (N if gather else rows):
+            raise ValueError(f"x codes have {n} rows, expected {N if gather else rows}")
+        if gather:
+            src = _dev(grouping.sorted_src, "sorted_src", torch.int32, (rows,))
+            if src is None:
+                raise ValueError("gather needs sorted_src")
+    elif gather:
+        raise ValueError("gather needs grouping")
+    out = _dev(out, "out", _bf16(), (rows, cols))
+    _one_device(a, x_scales=sa, w=wc, w_scales=ws, w_up=uc, w_up_scales=us, offsets=offsets,
+                sorted_src=src, out=out)
+    with _on_device(a, stream):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=a.device)
+        p = _lib.MoeInt8Matmul(n, rows, k, cols, E, K, _ptr(a), _ptr(sa), _ptr(wc), _ptr(ws),
+                               _ptr(uc), _ptr(us), _ptr(offsets), _ptr(src))
+        _lib.check(lib.moe_int8_matmul(C.byref(p), _ptr(out), _stream(stream)))
     return out
 
 

@@ -19,6 +19,7 @@ MOE_PACKED_GATEUP = 0x4
 MOE_ROUTE_FUSED = 0x8
 MOE_NORM_STREAM_F32 = 0x1
 MOE_NORM_WEIGHT_F32 = 0x2
+MOE_ROWS_F32 = 0x1
 SCORES = {"sigmoid": 0, "sigmoid_norm": 1, "softmax": 2}  # MOE_SCORE_*
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
@@ -34,6 +35,9 @@ EXPORTED = ["moe_route", "moe_eqb_workspace_bytes", "moe_eqb_bias", "moe_eqb_sta
             "moe_rms_norm", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
             "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
             "moe_backward_workspace_bytes", "moe_backward",
+            "moe_group_workspace_bytes", "moe_group", "moe_permute", "moe_permute_backward",
+            "moe_unpermute", "moe_unpermute_backward", "moe_int8_quantize_rows",
+            "moe_int8_matmul",
             "moe_status_string",
             "moe_last_error_message", "moe_abi_version", "moe_stage_timing",
             "moe_stage_times", "moe_stage_name"]
@@ -75,6 +79,14 @@ class MoeGrads(C.Structure):
     _fields_ = [("x", C.c_void_p), ("logits", C.c_void_p), ("w_router", C.c_void_p),
                 ("w_gate", C.c_void_p), ("w_up", C.c_void_p), ("w_down", C.c_void_p),
                 ("ws_gate", C.c_void_p), ("ws_up", C.c_void_p), ("ws_down", C.c_void_p)]
+
+
+class MoeInt8Matmul(C.Structure):
+    _fields_ = [("a_rows", C.c_int64), ("rows", C.c_int64), ("k", C.c_int32),
+                ("cols", C.c_int32), ("E", C.c_int32), ("K", C.c_int32), ("a", C.c_void_p),
+                ("a_scales", C.c_void_p), ("w", C.c_void_p), ("w_scales", C.c_void_p),
+                ("w_up", C.c_void_p), ("w_up_scales", C.c_void_p), ("offsets", C.c_void_p),
+                ("sorted_src", C.c_void_p)]
 
 
 class MoeRouteStats(C.Structure):
@@ -168,6 +180,22 @@ def load(path: str = LIB_PATH):
     lib.moe_backward.argtypes = [C.POINTER(MoeProblem), C.POINTER(MoeWeights), vp, vp, vp, vp, vp,
                                  C.POINTER(MoeGrads), vp, C.c_size_t, vp]
     lib.moe_backward.restype = C.c_int
+    lib.moe_group_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.moe_group_workspace_bytes.restype = C.c_size_t
+    lib.moe_group.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.moe_group.restype = C.c_int
+    lib.moe_permute.argtypes = [vp, vp, vp, i64, i32, i32, u32, vp, vp]
+    lib.moe_permute.restype = C.c_int
+    lib.moe_permute_backward.argtypes = [vp, vp, i64, i32, i32, u32, vp, vp]
+    lib.moe_permute_backward.restype = C.c_int
+    lib.moe_unpermute.argtypes = [vp, vp, vp, vp, i64, i32, i32, u32, vp, vp, vp, vp]
+    lib.moe_unpermute.restype = C.c_int
+    lib.moe_unpermute_backward.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, u32, vp, vp, vp]
+    lib.moe_unpermute_backward.restype = C.c_int
+    lib.moe_int8_quantize_rows.argtypes = [vp, i64, i32, vp, vp, vp]
+    lib.moe_int8_quantize_rows.restype = C.c_int
+    lib.moe_int8_matmul.argtypes = [C.POINTER(MoeInt8Matmul), vp, vp]
+    lib.moe_int8_matmul.restype = C.c_int
     lib.moe_status_string.argtypes = [C.c_int]
     lib.moe_status_string.restype = C.c_char_p
     lib.moe_last_error_message.argtypes = []

@@ -97,6 +97,12 @@ int64_t perm_max_tiles(int64_t pairs, int E, int bm);
 // (the shared expert folded into the weight-streaming products).
 hipError_t launch_permute(const int32_t* ids, int64_t N, int E, int K, int bm, int xr,
                           const PermWork& w, hipStream_t stream, int shared_rows = 0);
+// The public grouping: pairs whose id lies outside [0, E) come last, with
+// sorted_src and src_pos -1; block_counts holds perm_count_rows(pairs) * (E + 1)
+// words.  No m-tile table.
+hipError_t launch_group(const int32_t* ids, int64_t pairs, int E, int32_t* counts,
+                        int32_t* offsets, int32_t* sorted_src, int32_t* src_pos,
+                        uint32_t* block_counts, hipStream_t stream);
 // Expert loads only (no permutation): counts[E] must be a device buffer.
 hipError_t launch_count(const int32_t* ids, int64_t pairs, int E, int32_t* counts,
                         hipStream_t stream);
@@ -157,6 +163,42 @@ hipError_t launch_router_shared_gateup(const uint16_t* x, int64_t N, int d,
 hipError_t launch_combine(const uint16_t* sh, const uint16_t* Y, const float* S,
                           const int32_t* src_pos, int64_t N, int K, int d,
                           uint16_t* y, hipStream_t stream);
+
+// ---------------------------------------------------------------- rows
+// Rows of bf16, or fp32 (f32), between tokens and their places src_pos [N,K] in
+// the grouped order (a place outside [0, N*K): none).  x_scales / row_scales:
+// x / rows are E4M3 codes with these scales (d % 128 == 0, 16-byte aligned, bf16
+// otherwise).  w, base, codes (with scales), drows and dw may be NULL.
+hipError_t launch_permute_rows(const void* x, const float* x_scales, const int32_t* src_pos,
+                               int64_t N, int d, int K, bool f32, void* rows, hipStream_t stream);
+hipError_t launch_unpermute_rows(const void* rows, const int32_t* src_pos, const float* w,
+                                 const void* base, int64_t N, int d, int K, bool f32, void* y,
+                                 uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_unpermute_grad(const void* dy, const void* rows, const float* row_scales,
+                                 const int32_t* src_pos, const float* w, int64_t N, int d, int K,
+                                 bool f32, void* drows, float* dw, hipStream_t stream);
+
+// ---------------------------------------------------------------- int8
+// n rows of cols bf16 (cols % 16 == 0, 16-byte aligned) -> integers and scales.
+hipError_t launch_quant_int8(const uint16_t* X, int64_t n, int cols, int8_t* Q, float* S,
+                             hipStream_t stream);
+// out[r] = the scaled product of A's row (r, or sorted_src[r] / K) and the
+// weights of the expert whose segment offsets[e] .. offsets[e + 1] - 1 holds r
+// (offsets NULL: one weight); w_up: silu of it times the product with w_up.
+struct Int8Args {
+  const int8_t* a;           // [a_rows][k]
+  const float* a_scales;     // [a_rows]
+  const int8_t* w;           // [E][cols][k]
+  const float* w_scales;     // [E][cols]
+  const int8_t* w_up;        // as w, or NULL
+  const float* w_up_scales;
+  const int32_t* offsets;    // [E + 1] or NULL
+  const int32_t* sorted_src; // [rows] or NULL
+  uint16_t* out;             // [rows][cols]
+  int64_t a_rows, rows;
+  int k, cols, E, K;         // k % 16 == 0, cols % 8 == 0
+};
+hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream);
 
 // ---------------------------------------------------------------- diagnostics
 // Same layout as moe_route_stats_t of the public header.

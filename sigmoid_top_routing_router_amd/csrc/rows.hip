@@ -1,0 +1,356 @@
+// Rows of tokens on their way to the experts and back, and the gradients.
+//
+// "Kolibri Pre-Training from Scratch" §6.1: y_t = f_shared(x_t) + sum_k s_tk
+// f_e(x_t), e = I_tk.  With pos(t, k) the place of pair (t, k) in the order
+// grouped by expert (permute.hip; none for a pair whose expert is elsewhere),
+// base the shared expert's output and R the experts' output rows:
+//   permute            rows[pos(t, k)] = x_t
+//   permute_backward   dx_t = sum_k drows[pos(t, k)]
+//   unpermute          y_t = base_t + sum_k s_tk R[pos(t, k)]
+//   unpermute_backward dR[pos(t, k)] = s_tk dy_t,  ds_tk = <dy_t, R[pos(t, k)]>
+// ("Kolibri 1 im Detail", routing section: tokens are brought to their experts
+// with no per-expert capacity.)  Every kernel walks the tokens, so a token's
+// row is read or written once and each grouped row once; a pair's place is
+// checked against the number of pairs, so that no access leaves the rows.
+// Sums over k run in fp32 in the order of k and are rounded once.
+//
+// Rows kept in 8 bits are E4M3 codes with one fp32 scale per 1 x 128 group (the
+// rule of fp8_quant.hip): unpermute can leave them for the rows that it reads,
+// permute and unpermute_backward read them in the place of bf16 rows.
+#include <algorithm>
+#include <initializer_list>
+#include <type_traits>
+
+#include "common.h"
+#include "fp8_codes.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2_t v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// What a thread moves of a row: 16 bytes, or one element where the rows are not
+// whole aligned 16-byte words.
+template <bool F32, bool VEC>
+struct Piece;
+template <>
+struct Piece<false, true> {
+  typedef u32x4_t raw;
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void open(raw v, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ raw close(const float (&f)[V]) {
+    return raw{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+               pack_bf16(f[6], f[7])};
+  }
+};
+template <>
+struct Piece<true, true> {
+  typedef u32x4_t raw;
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void open(raw v, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+  static __device__ __forceinline__ raw close(const float (&f)[V]) {
+    return raw{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+               __float_as_uint(f[3])};
+  }
+};
+template <>
+struct Piece<false, false> {
+  typedef uint16_t raw;
+  static constexpr int V = 1;
+  static __device__ __forceinline__ void open(raw v, float (&f)[V]) { f[0] = bf16_to_f32(v); }
+  static __device__ __forceinline__ raw close(const float (&f)[V]) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f[0]);
+  }
+};
+template <>
+struct Piece<true, false> {
+  typedef uint32_t raw;
+  static constexpr int V = 1;
+  static __device__ __forceinline__ void open(raw v, float (&f)[V]) { f[0] = __uint_as_float(v); }
+  static __device__ __forceinline__ raw close(const float (&f)[V]) { return __float_as_uint(f[0]); }
+};
+
+// Eight E4M3 codes times their group's scale, in fp32.
+__device__ __forceinline__ void open_codes(u32x2_t c, float s, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], false);
+    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], true);
+    f[4 * i] = lo[0] * s;
+    f[4 * i + 1] = lo[1] * s;
+    f[4 * i + 2] = hi[0] * s;
+    f[4 * i + 3] = hi[1] * s;
+  }
+}
+
+// Token and piece of a thread in a launch over all pieces of all rows.
+__device__ __forceinline__ bool piece_of(int64_t N, uint32_t ppr, int64_t& t, uint32_t& c) {
+  const int64_t first = (int64_t)blockIdx.x * 256, t0 = first / ppr;
+  const uint32_t r = (uint32_t)(first - t0 * ppr) + threadIdx.x;
+  t = t0 + r / ppr;
+  c = r % ppr;
+  return t < N;
+}
+
+template <bool F32, bool VEC, bool KEPT, int K>
+__global__ __launch_bounds__(256) void permute_kernel(
+    const void* __restrict__ x, const float* __restrict__ xs, const int32_t* __restrict__ src_pos,
+    int64_t N, uint32_t ppr, uint32_t n_rows, void* __restrict__ rows) {
+  typedef Piece<F32, VEC> P;
+  typedef typename P::raw raw;
+  int64_t t;
+  uint32_t c;
+  if (!piece_of(N, ppr, t, c)) return;
+  raw v;
+  if constexpr (KEPT) {
+    float f[8];
+    open_codes(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(x) + t * ppr + c),
+               xs[(t * ppr + c) >> 4], f);
+    v = P::close(f);
+  } else {
+    v = __builtin_nontemporal_load(reinterpret_cast<const raw*>(x) + t * ppr + c);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t p = (uint32_t)src_pos[t * K + k];
+    if (p < n_rows)
+      __builtin_nontemporal_store(v, reinterpret_cast<raw*>(rows) + (int64_t)p * ppr + c);
+  }
+}
+
+// y = base + sum_k w R (w NULL: 1, base NULL: 0).  KEEP: the rows' codes too;
+// 16 lanes hold a group of a row.
+template <bool F32, bool VEC, bool KEEP, int K>
+__global__ __launch_bounds__(256) void unpermute_kernel(
+    const void* __restrict__ rows, const int32_t* __restrict__ src_pos,
+    const float* __restrict__ w, const void* __restrict__ base, int64_t N, uint32_t ppr,
+    uint32_t n_rows, void* __restrict__ y, u32x2_t* __restrict__ codes,
+    float* __restrict__ scales) {
+  typedef Piece<F32, VEC> P;
+  typedef typename P::raw raw;
+  int64_t t;
+  uint32_t c;
+  if (!piece_of(N, ppr, t, c)) return;
+  uint32_t p[K];
+  float s[K];
+  raw v[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    p[k] = (uint32_t)src_pos[t * K + k];
+    s[k] = w ? w[t * K + k] : 1.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (p[k] < n_rows)
+      v[k] = __builtin_nontemporal_load(reinterpret_cast<const raw*>(rows) + (int64_t)p[k] * ppr + c);
+  float acc[P::V];
+  if (base) {
+    P::open(__builtin_nontemporal_load(reinterpret_cast<const raw*>(base) + t * ppr + c), acc);
+  } else {
+#pragma unroll
+    for (int j = 0; j < P::V; ++j) acc[j] = 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (p[k] >= n_rows) continue;
+    float f[P::V];
+    P::open(v[k], f);
+#pragma unroll
+    for (int j = 0; j < P::V; ++j) acc[j] = fmaf(s[k], f[j], acc[j]);
+    if constexpr (KEEP) {
+      const uint4 u = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+      const float top = __uint_as_float(row16_max_u32(abs_max8(u)));
+      const float scale = top / kE4M3Max;
+      const uint2 q = top != 0.0f ? quant8(u, scale) : make_uint2(0, 0);
+      const int64_t at = (int64_t)p[k] * ppr + c;
+      __builtin_nontemporal_store(u32x2_t{q.x, q.y}, codes + at);
+      if ((threadIdx.x & 15) == 0) scales[at >> 4] = top != 0.0f ? scale : 0.0f;
+    }
+  }
+  __builtin_nontemporal_store(P::close(acc), reinterpret_cast<raw*>(y) + t * ppr + c);
+}
+
+// A wave takes a token: its dy row once, the K rows beside it.
+template <bool F32, bool VEC, bool KEPT, int K>
+__global__ __launch_bounds__(256) void unpermute_grad_kernel(
+    const void* __restrict__ dy, const void* __restrict__ rows, const float* __restrict__ scales,
+    const int32_t* __restrict__ src_pos, const float* __restrict__ w, int64_t N, uint32_t ppr,
+    uint32_t n_rows, void* __restrict__ drows, float* __restrict__ dw) {
+  typedef Piece<F32, VEC> P;
+  typedef typename P::raw raw;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= N) return;
+  const int lane = lane_id();
+  uint32_t p[K];
+  float s[K], dot[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    p[k] = (uint32_t)src_pos[t * K + k];
+    s[k] = w ? w[t * K + k] : 1.0f;
+    dot[k] = 0.0f;
+  }
+  for (uint32_t c = lane; c < ppr; c += kWave) {
+    float g[P::V];
+    P::open(__builtin_nontemporal_load(reinterpret_cast<const raw*>(dy) + t * ppr + c), g);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (p[k] >= n_rows) continue;
+      const int64_t at = (int64_t)p[k] * ppr + c;
+      if (dw) {
+        float f[P::V];
+        if constexpr (KEPT)
+          open_codes(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(rows) + at),
+                     scales[at >> 4], f);
+        else
+          P::open(__builtin_nontemporal_load(reinterpret_cast<const raw*>(rows) + at), f);
+#pragma unroll
+        for (int j = 0; j < P::V; ++j) dot[k] = fmaf(g[j], f[j], dot[k]);
+      }
+      if (drows) {
+        float o[P::V];
+#pragma unroll
+        for (int j = 0; j < P::V; ++j) o[j] = s[k] * g[j];
+        __builtin_nontemporal_store(P::close(o), reinterpret_cast<raw*>(drows) + at);
+      }
+    }
+  }
+  if (!dw) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) dot[k] += __shfl_xor(dot[k], o);
+    if (lane == 0) dw[t * K + k] = dot[k];
+  }
+}
+
+// fn(K) with K as a constant.
+template <class F>
+hipError_t with_k(int K, F&& fn) {
+  switch (K) {
+#define MOE_K_CASE(n) case n: fn(std::integral_constant<int, n>{}); break;
+    MOE_K_CASE(1) MOE_K_CASE(2) MOE_K_CASE(3) MOE_K_CASE(4)
+    MOE_K_CASE(5) MOE_K_CASE(6) MOE_K_CASE(7) MOE_K_CASE(8)
+#undef MOE_K_CASE
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+// Rows in whole aligned 16-byte words.
+bool words(int d, bool f32, std::initializer_list<const void*> buffers) {
+  if ((int64_t)d * (f32 ? 4 : 2) % 16) return false;
+  for (const void* p : buffers)
+    if ((uintptr_t)p % 16) return false;
+  return true;
+}
+template <class T>
+T* at(T* p, int64_t bytes) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
+  return p ? reinterpret_cast<T*>(reinterpret_cast<byte*>(p) + bytes) : nullptr;
+}
+// Calls fn(t0, n) for runs of tokens whose launch stays below 2^31 threads.
+template <class F>
+hipError_t token_runs(int64_t N, int64_t threads_per_token, F&& fn) {
+  const int64_t most = std::max<int64_t>(1, ((int64_t(1) << 31) - 256) / threads_per_token);
+  for (int64_t t0 = 0; t0 < N; t0 += most) {
+    const hipError_t e = fn(t0, std::min(most, N - t0));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
+
+}  // namespace
+
+hipError_t launch_permute_rows(const void* x, const float* x_scales, const int32_t* src_pos,
+                               int64_t N, int d, int K, bool f32, void* rows, hipStream_t stream) {
+  const bool kept = x_scales != nullptr;
+  const bool vec = kept || words(d, f32, {x, rows});
+  const int es = f32 ? 4 : 2, ppr = vec ? d * es / 16 : d;
+  const uint32_t n_rows = (uint32_t)(N * K);
+  return token_runs(N, ppr, [&](int64_t t0, int64_t n) {
+    const void* xt = at(x, t0 * d * (kept ? 1 : es));
+    const float* st = x_scales ? x_scales + t0 * (d / 128) : nullptr;
+    const dim3 grid(blocks_of(n * ppr)), block(256);
+    return with_k(K, [&](auto k) {
+      constexpr int kk = decltype(k)::value;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, xt, st, src_pos + t0 * K, n,
+                           (uint32_t)ppr, n_rows, rows);
+      };
+      if (kept) go(permute_kernel<false, true, true, kk>);
+      else if (f32 && vec) go(permute_kernel<true, true, false, kk>);
+      else if (f32) go(permute_kernel<true, false, false, kk>);
+      else if (vec) go(permute_kernel<false, true, false, kk>);
+      else go(permute_kernel<false, false, false, kk>);
+    });
+  });
+}
+
+hipError_t launch_unpermute_rows(const void* rows, const int32_t* src_pos, const float* w,
+                                 const void* base, int64_t N, int d, int K, bool f32, void* y,
+                                 uint8_t* codes, float* scales, hipStream_t stream) {
+  const bool vec = codes || words(d, f32, {rows, base, y});
+  const int es = f32 ? 4 : 2, ppr = vec ? d * es / 16 : d;
+  const uint32_t n_rows = (uint32_t)(N * K);
+  return token_runs(N, ppr, [&](int64_t t0, int64_t n) {
+    const dim3 grid(blocks_of(n * ppr)), block(256);
+    return with_k(K, [&](auto k) {
+      constexpr int kk = decltype(k)::value;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, rows, src_pos + t0 * K,
+                           w ? w + t0 * K : nullptr, at(base, t0 * d * es), n, (uint32_t)ppr,
+                           n_rows, at(y, t0 * d * es), reinterpret_cast<u32x2_t*>(codes), scales);
+      };
+      if (codes) go(unpermute_kernel<false, true, true, kk>);
+      else if (f32 && vec) go(unpermute_kernel<true, true, false, kk>);
+      else if (f32) go(unpermute_kernel<true, false, false, kk>);
+      else if (vec) go(unpermute_kernel<false, true, false, kk>);
+      else go(unpermute_kernel<false, false, false, kk>);
+    });
+  });
+}
+
+hipError_t launch_unpermute_grad(const void* dy, const void* rows, const float* row_scales,
+                                 const int32_t* src_pos, const float* w, int64_t N, int d, int K,
+                                 bool f32, void* drows, float* dw, hipStream_t stream) {
+  const bool kept = row_scales != nullptr;
+  const bool vec = kept || words(d, f32, {dy, rows, drows});
+  const int es = f32 ? 4 : 2, ppr = vec ? d * es / 16 : d;
+  const uint32_t n_rows = (uint32_t)(N * K);
+  return token_runs(N, 64, [&](int64_t t0, int64_t n) {
+    const dim3 grid(blocks_of(n * 64)), block(256);
+    return with_k(K, [&](auto k) {
+      constexpr int kk = decltype(k)::value;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, at(dy, t0 * d * es), rows, row_scales,
+                           src_pos + t0 * K, w ? w + t0 * K : nullptr, n, (uint32_t)ppr, n_rows,
+                           drows, dw ? dw + t0 * K : nullptr);
+      };
+      if (kept) go(unpermute_grad_kernel<false, true, true, kk>);
+      else if (f32 && vec) go(unpermute_grad_kernel<true, true, false, kk>);
+      else if (f32) go(unpermute_grad_kernel<true, false, false, kk>);
+      else if (vec) go(unpermute_grad_kernel<false, true, false, kk>);
+      else go(unpermute_grad_kernel<false, false, false, kk>);
+    });
+  });
+}
+
+}  // namespace moe
