@@ -720,8 +720,8 @@ moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const 
  *               r, and a_rows = rows.
  *  out          [rows,cols] bf16 bits.
  * 0 <= rows <= 2^27, a_rows likewise; 1 <= E <= 384; k % 16 == 0 (16 <= k <=
- * 65536); cols % 8 == 0 (8 <= cols <= 65536); 1 <= K <= 8.  a, w, w_up and out
- * 16-byte aligned, the others 4-byte.  The output shares memory with no input.
+ * 65536); cols % 8 == 0 (8 <= cols <= 65536); 1 <= K <= 8; with sorted_src
+ * a_rows*k at most 4 GiB - 512 KiB.  a, w, w_up and out 16-byte aligned, the others 4-byte.  The output shares memory with no input.
  * The first call on a device sets the kernels' LDS attributes: make one
  * uncaptured call before capturing.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.

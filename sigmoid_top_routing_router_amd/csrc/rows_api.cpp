@@ -202,6 +202,9 @@ moe_status_t moe_int8_matmul(const moe_int8_matmul_t* p, uint16_t* out, void* st
     return fail(MOE_ERR_INVALID_ARGUMENT, "w_up and w_up_scales: both or neither");
   if (!p->sorted_src && p->a_rows != p->rows)
     return fail(MOE_ERR_INVALID_ARGUMENT, "without sorted_src a_rows must be rows");
+  if (p->sorted_src && (uint64_t)p->a_rows * p->k > moe::kInt8MaxGathered)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "a_rows=%lld k=%d: a gathered a must be at most 4 GiB - "
+                "512 KiB", (long long)p->a_rows, p->k);
   if (p->rows == 0) return moe::set_error(MOE_OK, "");
   if (p->a_rows == 0) return fail(MOE_ERR_INVALID_ARGUMENT, "rows of an empty a");
   if (!p->a || !p->a_scales || !p->w || !p->w_scales || !out)

@@ -203,6 +203,7 @@ def test_int8_matmul(lib, page):
                dict(k=40), dict(k=65552), dict(cols=0), dict(cols=20), dict(cols=65544),
                dict(E=0), dict(E=385), dict(K=0), dict(K=9)):
         assert says(lib, call(**kw), SHAPE, "k % 16 == 0"), kw
+    assert says(lib, call(ar=65536, k=65536), SHAPE, "a gathered a")
     assert says(lib, call(off=None), INVALID, "one weight and no sorted_src")
     assert says(lib, call(off=None, src=None), INVALID, "one weight and no sorted_src")
     assert says(lib, call(off=None, E=1), INVALID, "one weight and no sorted_src")
