@@ -11,12 +11,14 @@
 // section, SwiGLU paragraph).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
 #include "fp8_codes.h"
 #include "gemm_args.h"
 #include "kernels.h"
+#include "lane_swaps.h"
 
 namespace moe {
 namespace {
@@ -25,7 +27,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr float kInt8Max = 127.0f;
 
@@ -90,8 +92,8 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const u32x4_t* __restri
 constexpr int kCols = 256;
 constexpr int kStage = 128;                  // bytes of k in a stage: a whole line of a row
 constexpr int kQuarter = 64 * kStage;        // 64 weight rows of a stage
-constexpr int kLds = 160 * 1024;
-constexpr int kXcds = 8;
+constexpr int kXcds = 8, kCus = 256;
+constexpr int kListed = 64;                  // tiles that a block works on, at most
 constexpr uint32_t kNoRow = 0xFFFFFFFFu - 256u * 1024u;  // past any buffer: the load gives zeros
 
 template <int MB>
@@ -99,8 +101,9 @@ struct TileShape {
   static constexpr int rows = 64 * MB;
   static constexpr int a_bytes = rows * kStage;
   static constexpr int b_at = 2 * a_bytes;
-  static constexpr int quarters = (kLds - b_at) / kQuarter;  // of B's ring: 12 or 10
-  static_assert(quarters >= 8, "two stages of B at least");
+  static constexpr int quarters = 12;  // of B's ring: three stages
+  static constexpr int lds = b_at + quarters * kQuarter;
+  static_assert(lds <= 160 * 1024, "a CU's LDS");
 };
 
 // Rows of one tile.
@@ -121,7 +124,7 @@ __device__ __forceinline__ uint32_t seg_rows(uint32_t c, uint32_t n) {
 struct Segments {
   static constexpr int kGroups = 6;  // E <= 384
   uint32_t lo[kGroups], n[kGroups], incl[kGroups], total;
-  __device__ __forceinline__ void read(const Int8Args& a, uint32_t bm, bool) {
+  __device__ __forceinline__ void read(const Int8Args& a, uint32_t bm) {
     const int lane = lane_id();
     total = 0;
 #pragma unroll
@@ -161,13 +164,6 @@ struct Segments {
   }
 };
 
-// Blocks are dealt to the XCDs in turn; each takes a contiguous run of the work.
-__device__ __forceinline__ bool xcd_item(int64_t block, int64_t work, int64_t& item) {
-  const int64_t share = (work + kXcds - 1) / kXcds, local = block / kXcds;
-  item = block % kXcds * share + local;
-  return local < share && item < work;
-}
-
 // The row of A behind output row r.
 __device__ __forceinline__ int64_t a_row_of(const Int8Args& a, int64_t r) {
   if (!a.sorted_src) return r;
@@ -178,24 +174,78 @@ __device__ __forceinline__ int64_t a_row_of(const Int8Args& a, int64_t r) {
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const bf16x2_t v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
-}
 __device__ __forceinline__ void block_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
+// The tiles of a block, one a lane: blocks are dealt to the XCDs in turn, each XCD
+// takes a contiguous run of the work and its blocks take that run's tiles in turn,
+// so that the blocks at work together share operands in the XCD's L2.
+struct List {
+  uint32_t row0, rest;  // rest: expert, rows, column tile
+  int count;
+  // fn(item, column tile) -> Tile
+  template <class F>
+  __device__ __forceinline__ void fill(uint32_t work, F&& fn) {
+    const uint32_t share = (work + kXcds - 1) / kXcds, per = gridDim.x / kXcds;
+    const uint32_t begin = blockIdx.x % kXcds * share, end = min(begin + share, work);
+    const int lane = lane_id();
+    count = 0;
+    row0 = rest = 0;
+    for (uint32_t item = begin + blockIdx.x / kXcds; item < end && count < kListed; item += per) {
+      uint32_t nt = 0;
+      const Tile t = fn(item, nt);
+      if (t.rows > 0) {
+        row0 = lane == count ? (uint32_t)t.row0 : row0;
+        rest = lane == count ? (uint32_t)t.expert << 22 | (uint32_t)t.rows << 12 | nt : rest;
+        ++count;
+      }
+    }
+    count = __builtin_amdgcn_readfirstlane(count);
+  }
+  __device__ __forceinline__ Tile tile(int i, int& nt) const {
+    const uint32_t r = readlane_u32(rest, i);
+    nt = (int)(r & 0xFFFu);
+    return Tile{(int)(r >> 22), (int)(r >> 12 & 0x3FFu), (int64_t)readlane_u32(row0, i)};
+  }
+};
+
+// A buffer whose place is the same in all lanes, kept in scalar registers.
+struct Buffer {
+  uint32_t lo, hi, bytes;
+  __device__ __forceinline__ void set(const void* base, uint32_t n) {
+    lo = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)base);
+    hi = __builtin_amdgcn_readfirstlane((uint32_t)((uintptr_t)base >> 32));
+    bytes = __builtin_amdgcn_readfirstlane(n);
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const {
+    const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(hi) << 32 |
+                        (uint32_t)__builtin_amdgcn_readfirstlane(lo);
+    return make_rsrc((const void*)at, (uint32_t)__builtin_amdgcn_readfirstlane(bytes));
+  }
+};
+
+// A block's tiles one after the other.  While a tile's results are scaled, rounded
+// and stored (straight from registers), the next tile's first stages are on their
+// way into LDS: a block to each tile spent 1.9 us on finding it, 4.4 until its first
+// products and 5.1 behind its last ones, next to 25 us of products.  98304 rows of
+// 384 experts, 2560 deep, 2 x 512 columns: 355 us that way, 344 this way; 2048 rows
+// of 128 experts, 512 deep, 2560 columns: 41 and 32.
+//
+// What bounds it: dense, the power of the matrix instructions (8192 x 8192 x 8192:
+// 405 us, 2.7 POP/s, in use 71% of the time at 1.7 GHz); few rows an expert, the
+// weights' way from HBM (64 tokens of six among 384 experts: 0.64 GB in 112 us, 5.7
+// TB/s); many rows of many experts, both in part: without products the same loads
+// take 313 of the 344 us (1.44 GB past L2), from L2 alone with products 280.
 template <int MB, bool UP>
-__device__ __forceinline__ void int8_tile(const Int8Args& a, const Tile& tile, int nt,
-                                          char* lds) {
+__device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, char* lds) {
   typedef TileShape<MB> S;
   constexpr int OC = UP ? kCols / 2 : kCols;  // output columns of a tile
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wg = wave >> 2, wp = wave & 3;
-  const int rows = tile.rows, col0 = nt * OC, cols = min(OC, a.cols - col0);
+  const int nk = (a.k + kStage - 1) / kStage;
 
   // Loads: a wave brings MB times 8 rows of A and 4 times 8 rows of B a stage,
   // 128 bytes a row; load i covers rows 8 (8 i + wave) .. + 7 of the tile.
@@ -203,92 +253,53 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const Tile& tile, i
   // & 7).  Rows past the tile and chunks past k read zeros.
   const int sub = lane >> 3;
   const int chunk = (lane & 7) ^ ((4 * wave + (sub >> 1)) & 7);
-  uint32_t a_off[MB], b_off[4];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int r = 8 * (8 * i + wave) + sub;
-    a_off[i] = kNoRow;
-    if (r < rows)
-      a_off[i] = (uint32_t)(a.sorted_src ? a_row_of(a, tile.row0 + r) : r) * (uint32_t)a.k +
-                 (uint32_t)chunk * 16u;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (8 * (8 * i + wave) + sub) & (OC - 1);
-    b_off[i] = r < cols ? (uint32_t)r * (uint32_t)a.k + (uint32_t)chunk * 16u : kNoRow;
-  }
-  const int64_t w_row = (int64_t)tile.expert * a.cols + col0;
-  const __amdgpu_buffer_rsrc_t ra =
-      a.sorted_src ? make_rsrc(a.a, (uint32_t)(a.a_rows * a.k))
-                   : make_rsrc(a.a + tile.row0 * a.k, (uint32_t)rows * (uint32_t)a.k);
-  const uint32_t w_bytes = (uint32_t)cols * (uint32_t)a.k;
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + w_row * a.k, w_bytes);
-  const __amdgpu_buffer_rsrc_t ru = make_rsrc((UP ? a.w_up : a.w) + w_row * a.k, w_bytes);
-  const int nk = (a.k + kStage - 1) / kStage;
   const bool k_in = (nk - 1) * kStage + chunk * 16 < a.k;  // this lane's chunk of the last stage
-
+  uint32_t a_off[MB], a_next[MB], b_off;
+  Buffer ra, rw, ru;
+  Tile tile;
+  int col0, cols;
+  // the tile's rows of A
+  auto rows_of = [&](int i) {
+    int nt;
+    const Tile t = list.tile(i, nt);
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int r = 8 * (8 * j + wave) + sub;
+      a_next[j] = kNoRow;
+      if (r < t.rows) a_next[j] = a.sorted_src ? (uint32_t)a_row_of(a, t.row0 + r) : (uint32_t)r;
+    }
+  };
+  auto open = [&](int i) {
+    int nt;
+    tile = list.tile(i, nt);
+    col0 = nt * OC;
+    cols = min(OC, a.cols - col0);
+#pragma unroll
+    for (int j = 0; j < MB; ++j)
+      a_off[j] = a_next[j] == kNoRow ? kNoRow : a_next[j] * (uint32_t)a.k + (uint32_t)chunk * 16u;
+    b_off = (uint32_t)(8 * wave + sub) * (uint32_t)a.k + (uint32_t)chunk * 16u;
+    const int64_t w_row = (int64_t)tile.expert * a.cols + col0;
+    const uint32_t w_bytes = (uint32_t)cols * (uint32_t)a.k;
+    if (a.sorted_src) ra.set(a.a, (uint32_t)(a.a_rows * a.k));
+    else ra.set(a.a + tile.row0 * a.k, (uint32_t)tile.rows * (uint32_t)a.k);
+    rw.set(a.w + w_row * a.k, w_bytes);
+    ru.set((UP ? a.w_up : a.w) + w_row * a.k, w_bytes);
+  };
   auto load_a = [&](int kt, int slot, int i) {
-    dma16(ra, kt == nk - 1 && !k_in ? kNoRow : a_off[i], (uint32_t)kt * kStage,
+    dma16(ra.rsrc(), kt == nk - 1 && !k_in ? kNoRow : a_off[i], (uint32_t)kt * kStage,
           (lds_void_t*)(lds + slot * S::a_bytes + (8 * i + wave) * 1024));
   };
-  // quarter i of stage kt at place q of the ring
+  // quarter i of stage kt at place q of the ring: rows 64 i .. + 63 of the tile's
+  // weight, with UP 64 (i % 2) .. + 63 of w or w_up; rows past the tile's columns
+  // lie past the buffer
   auto load_b = [&](int kt, int q, int i) {
-    dma16(UP && i >= 2 ? ru : rw, b_off[i], (uint32_t)kt * kStage,
-          (lds_void_t*)(lds + S::b_at + q * kQuarter + wave * 1024));
+    const uint32_t off = b_off + (uint32_t)(UP ? i & 1 : i) * 64u * (uint32_t)a.k;
+    dma16(UP && i >= 2 ? ru.rsrc() : rw.rsrc(), kt == nk - 1 && !k_in ? kNoRow : off,
+          (uint32_t)kt * kStage, (lds_void_t*)(lds + S::b_at + q * kQuarter + wave * 1024));
   };
   auto place = [&](int q) { return q >= S::quarters ? q - S::quarters : q; };
-
-  // Wave (wg, wp): the first or second half of the tile's 32-row blocks, and
-  // weight rows 64 wp .. + 63, or with UP 32 wp of w and of w_up.
-  const int blocks = (rows + 31) / 32, half = (blocks + 1) / 2;
-  const int first = wg ? half : 0;
-  const int live = __builtin_amdgcn_readfirstlane(wg ? blocks - half : half);
-  int b_row[2];
-  b_row[0] = UP ? 32 * wp : 64 * wp;
-  b_row[1] = UP ? kCols / 2 + 32 * wp : 64 * wp + 32;
-  const bool any = __builtin_amdgcn_readfirstlane(
-      live > 0 && (UP ? 32 * wp : 64 * wp) < cols ? 1 : 0) != 0;
-  const int fr = lane & 31;
-  const int a_base = (32 * first + fr) * kStage;
-  const int b_quarter[2] = {b_row[0] >> 6, b_row[1] >> 6};
-  const int b_base[2] = {((b_row[0] & 63) + fr) * kStage, ((b_row[1] & 63) + fr) * kStage};
-  int slot_of[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) slot_of[s] = ((2 * s + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
-
-  i32x16_t acc[MB][2];
-#pragma unroll
-  for (int m = 0; m < MB; ++m)
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[m][f][r] = 0;
-
-  // Stage kt is four steps of 32 bytes of k; the fragments of the next step are
-  // read while a step's products run.  The barrier in front of the last step
-  // frees A's slot and B's quarters of the stage: A two stages on goes there at
-  // once (two loads, the rest in the next stage's first step).  B's ring holds
-  // three stages (MB 4), so that all of B three stages on follows in the second
-  // and third step; with MB 5 two and a half: there the second half of B two
-  // stages on, then the first half three stages on.
-  constexpr bool kDeep = S::quarters >= 12;
-  constexpr int kAhead = kDeep ? 4 : 2;  // quarters three stages on, in flight at the barrier
-  typedef std::true_type T;
-  typedef std::false_type F;
-  auto run = [&](auto live_tag) {
-    constexpr int LIVE = decltype(live_tag)::value;
-    constexpr int NF = LIVE > 0 ? LIVE : 1;
-    i32x4_t fa[2][NF], fb[2][2];
-    auto read = [&](int set, int slot, int q0, int step) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-        fb[set][f] = *reinterpret_cast<const i32x4_t*>(
-            lds + S::b_at + place(q0 + b_quarter[f]) * kQuarter + b_base[f] + slot_of[step]);
-#pragma unroll
-      for (int m = 0; m < NF; ++m)
-        fa[set][m] = *reinterpret_cast<const i32x4_t*>(lds + slot * S::a_bytes + a_base +
-                                                       32 * m * kStage + slot_of[step]);
-    };
+  // a tile's first stages: A's two slots, B's three stages
+  auto load_first = [&] {
 #pragma unroll
     for (int i = 0; i < MB; ++i) load_a(0, 0, i);
 #pragma unroll
@@ -301,211 +312,376 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const Tile& tile, i
     }
     if (nk > 2) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) load_b(2, 8 + i, i);
+      for (int i = 0; i < 4; ++i) load_b(2, 8 + i, i);
     }
-    if (nk > 2) wait_vmcnt<MB + 4 + kAhead>();
-    else if (nk > 1) wait_vmcnt<MB + 4>();
-    else wait_vmcnt<0>();
-    block_barrier();
-    int slot = 0, q0 = 0;  // of stage kt
-    if (LIVE > 0) read(0, 0, 0, 0);
-    // ld_a1: the rest of A(kt + 1) and, with MB 5, of B(kt + 1); ld_b: B(kt + 2);
-    // ld_a2: A(kt + 2); next: there is a stage kt + 1; ahead: loads of B(kt + 2)
-    // may be in flight at the barrier.
-    auto stage = [&](int kt, auto ld_a1, auto ld_b, auto ld_a2, auto next, auto ahead) {
-      const int q1 = place(q0 + 4);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int cur = s & 1;
-        if (s == 3 && next) {
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          if (ahead) wait_vmcnt<kAhead>();
-          else wait_vmcnt<0>();
-          block_barrier();
-        }
-        if (s == 0 && ld_a1) {
-#pragma unroll
-          for (int i = 2; i < MB; ++i) load_a(kt + 1, slot ^ 1, i);
-        }
-        if (s == 1) {
-          if (kDeep) {
-            if (ld_b) {
-              load_b(kt + 2, place(q1 + 4), 0);
-              load_b(kt + 2, place(q1 + 5), 1);
-            }
-          } else if (ld_a1) {
-            load_b(kt + 1, place(q1 + 2), 2);
-            load_b(kt + 1, place(q1 + 3), 3);
-          }
-        }
-        if (s == 2 && ld_b) {
-          if (kDeep) {
-            load_b(kt + 2, place(q1 + 6), 2);
-            load_b(kt + 2, place(q1 + 7), 3);
-          } else {
-            load_b(kt + 2, place(q1 + 4), 0);
-            load_b(kt + 2, place(q1 + 5), 1);
-          }
-        }
-        if (s == 3 && ld_a2) {
-          load_a(kt + 2, slot, 0);
-          load_a(kt + 2, slot, 1);
-        }
-        if (LIVE > 0) {
-          if (s < 3) read(cur ^ 1, slot, q0, s + 1);
-          else if (next) read(cur ^ 1, slot ^ 1, q1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (LIVE > 0) {
-#pragma unroll
-          for (int m = 0; m < NF; ++m)
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-              acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][f], fa[cur][m], acc[m][f],
-                                                                0, 0, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      slot ^= 1;
-      q0 = q1;
-    };
-    // stage 0: A(1), B(1) and the first of B(2) came with the prologue, with MB 5
-    // but for nothing; its barrier leaves those of B(2) in flight
-    stage(0, F{}, F{}, nk > 2, nk > 1, nk > 2);
-    for (int kt = 1; kt + 2 < nk; ++kt) stage(kt, T{}, T{}, T{}, T{}, T{});
-    if (nk >= 3) stage(nk - 2, T{}, F{}, F{}, T{}, F{});
-    if (nk >= 2) stage(nk - 1, F{}, F{}, F{}, F{}, F{});
   };
-  switch (any ? live : 0) {
-    case 0: run(std::integral_constant<int, 0>{}); break;
-    case 1: run(std::integral_constant<int, 1>{}); break;
-    case 2: run(std::integral_constant<int, 2>{}); break;
-    case 3: run(std::integral_constant<int, 3>{}); break;
-    case 4: run(std::integral_constant<int, 4>{}); break;
-    default: run(std::integral_constant<int, MB>{}); break;
-  }
 
-  // ---- epilogue.  The products have the weights first, so a lane holds output
-  // row (l & 31) of a block and columns 8 (r / 4) + 4 (l / 32) + r % 4.
-  const int ocol = 4 * (lane >> 5);
-  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(a.w_scales + w_row, (uint32_t)cols * 4u);
-  const __amdgpu_buffer_rsrc_t rsu =
-      make_rsrc((UP ? a.w_up_scales : a.w_scales) + w_row, (uint32_t)cols * 4u);
-  typedef float f32x4_t __attribute__((ext_vector_type(4)));
-  f32x4_t sc[2][4];
-  float sr[MB];
-  if (any) {
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        sc[f][q] = __builtin_bit_cast(
-            f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                         UP && f ? rsu : rsw,
-                         (int)((uint32_t)((UP ? 32 * wp : b_row[f]) + 8 * q + ocol) * 4u), 0, 0));
+  // Wave (wg, wp): the first or second half of the tile's 32-row blocks, and
+  // weight rows 64 wp .. + 63, or with UP 32 wp of w and of w_up.
+  const int b_row[2] = {UP ? 32 * wp : 64 * wp, UP ? kCols / 2 + 32 * wp : 64 * wp + 32};
+  const int fr = lane & 31;
+  const int b_quarter[2] = {b_row[0] >> 6, b_row[1] >> 6};
+  const int b_base[2] = {((b_row[0] & 63) + fr) * kStage, ((b_row[1] & 63) + fr) * kStage};
+  const int slot0 = ((lane >> 5) ^ ((lane >> 1) & 7)) * 16;  // of step s: ^ 32 s
+
+  rows_of(0);
+  open(0);
+  load_first();
+  for (int it = 0; it < list.count; ++it) {
+    const Tile now = tile;
+    const int now_col0 = col0, now_cols = cols;
+    const int blocks = (now.rows + 31) / 32, half = (blocks + 1) / 2;
+    const int first = wg ? half : 0;
+    const int live = __builtin_amdgcn_readfirstlane(
+        (UP ? 32 * wp : 64 * wp) < now_cols ? (wg ? blocks - half : half) : 0);
+    const int a_base = (32 * first + fr) * kStage;
+    // the rows' scales, and the next tile's rows
+    float sr[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       const int r = 32 * (first + m) + fr;
-      sr[m] = m < live && r < rows ? a.a_scales[a_row_of(a, tile.row0 + r)] : 0.0f;
+      sr[m] = m < live && r < now.rows ? a.a_scales[a_row_of(a, now.row0 + r)] : 0.0f;
     }
-  }
-  __syncthreads();  // the last fragments have been read
-  if constexpr (UP) {
-    constexpr int kRow = OC * 2 + 8;
-    static_assert(S::rows * kRow <= kLds, "staged tile");
-    if (any) {
+    if (it + 1 < list.count) rows_of(it + 1);
+
+    i32x16_t acc[MB][2];
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        if (m >= live) break;
-        char* to = lds + (32 * (first + m) + fr) * kRow + (32 * wp + ocol) * 2;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            h[j] = silu_mul((float)acc[m][0][4 * q + j] * (sr[m] * sc[0][q][j]),
-                            (float)acc[m][1][4 * q + j] * (sr[m] * sc[1][q][j]));
-          *reinterpret_cast<u32x2_t*>(to + 16 * q) =
-              u32x2_t{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
-        }
-      }
-    }
-    __syncthreads();
-    // 16 lanes a row
-    const int ch = tid & 15;
-    if (8 * ch < cols) {
-      for (int r = tid >> 4; r < rows; r += 32) {
-        const char* from = lds + r * kRow + ch * 16;
-        const u32x2_t lo = *reinterpret_cast<const u32x2_t*>(from);
-        const u32x2_t hi = *reinterpret_cast<const u32x2_t*>(from + 8);
-        *reinterpret_cast<u32x4_t*>(a.out + (tile.row0 + r) * a.cols + col0 + 8 * ch) =
-            u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-      }
-    }
-  } else if (any) {
-    // the wave's 64 columns of a block, one whole line of every row: through LDS
-    // of its own
-    constexpr int kRow = 128 + 8;
-    char* mine = lds + wave * (32 * kRow + 128);
-    const int ch = lane & 7, col = col0 + 64 * wp + 8 * ch;
-    const bool col_ok = 64 * wp + 8 * ch < cols;
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      if (m >= live) break;
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float y[4];
+        for (int r = 0; r < 16; ++r) acc[m][f][r] = 0;
+
+    // Stage kt is four steps of 32 bytes of k; the fragments of the next step are
+    // read while a step's products run.  The barrier in front of the last step
+    // frees A's slot and B's quarters of the stage: A two stages on goes there at
+    // once (two loads, the rest in the next stage's first step), B three stages on
+    // in that stage's second and third step.  The waits count the loads that may
+    // be in flight, all of them younger than those waited for; others between
+    // them (scales, the last tile's stores) make a wait longer, never shorter.
+    typedef std::true_type T;
+    typedef std::false_type F;
+    auto run = [&](auto live_tag) {
+      constexpr int LIVE = decltype(live_tag)::value;
+      constexpr int NF = LIVE > 0 ? LIVE : 1;
+      i32x4_t fa[2][NF], fb[2][2];
+      auto read = [&](int set, int slot, int q0, int step) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = (float)acc[m][f][4 * q + j] * (sr[m] * sc[f][q][j]);
-          *reinterpret_cast<u32x2_t*>(mine + fr * kRow + (32 * f + 8 * q + ocol) * 2) =
-              u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        for (int f = 0; f < 2; ++f)
+          fb[set][f] = *reinterpret_cast<const i32x4_t*>(
+              lds + S::b_at + place(q0 + b_quarter[f]) * kQuarter + ((b_base[f] + slot0) ^ (32 * step)));
+#pragma unroll
+        for (int m = 0; m < NF; ++m)
+          fa[set][m] = *reinterpret_cast<const i32x4_t*>(
+              lds + slot * S::a_bytes + 32 * m * kStage + ((a_base + slot0) ^ (32 * step)));
+      };
+      if (nk > 2) wait_vmcnt<MB + 8>();
+      else if (nk > 1) wait_vmcnt<MB + 4>();
+      else wait_vmcnt<0>();
+      block_barrier();
+      int slot = 0, q0 = 0;  // of stage kt
+      if (LIVE > 0) read(0, 0, 0, 0);
+      // ld_a1: the rest of A(kt + 1); ld_b: B(kt + 2); ld_a2: A(kt + 2);
+      // next: there is a stage kt + 1; ahead: loads of B(kt + 2) may be in flight at the barrier.
+      auto stage = [&](int kt, auto ld_a1, auto ld_b, auto ld_a2, auto next, auto ahead) {
+        const int q1 = place(q0 + 4);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int cur = s & 1;
+          if (s == 3 && next) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (ahead) wait_vmcnt<4>();
+            else wait_vmcnt<0>();
+            block_barrier();
+          }
+          if (s == 0 && ld_a1) {
+#pragma unroll
+            for (int i = 2; i < MB; ++i) load_a(kt + 1, slot ^ 1, i);
+          }
+          if ((s == 1 || s == 2) && ld_b) {
+            load_b(kt + 2, place(q1 + 2 * s + 2), 2 * s - 2);
+            load_b(kt + 2, place(q1 + 2 * s + 3), 2 * s - 1);
+          }
+          if (s == 3 && ld_a2) {
+#pragma unroll
+            for (int i = 0; i < (MB < 2 ? MB : 2); ++i) load_a(kt + 2, slot, i);
+          }
+          if (LIVE > 0) {
+            if (s < 3) read(cur ^ 1, slot, q0, s + 1);
+            else if (next) read(cur ^ 1, slot ^ 1, q1, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (LIVE > 0) {
+#pragma unroll
+            for (int m = 0; m < NF; ++m)
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+                acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][f], fa[cur][m],
+                                                                  acc[m][f], 0, 0, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        slot ^= 1;
+        q0 = q1;
+      };
+      stage(0, F{}, F{}, nk > 2, nk > 1, nk > 2);
+      for (int kt = 1; kt + 2 < nk; ++kt) stage(kt, T{}, T{}, T{}, T{}, T{});
+      if (nk >= 3) stage(nk - 2, T{}, F{}, F{}, T{}, F{});
+      if (nk >= 2) stage(nk - 1, F{}, F{}, F{}, F{}, F{});
+    };
+    switch (live) {
+      case 0: run(std::integral_constant<int, 0>{}); break;
+      case 1: run(std::integral_constant<int, 1>{}); break;
+      case 2: run(std::integral_constant<int, MB < 2 ? MB : 2>{}); break;
+      case 3: run(std::integral_constant<int, MB < 3 ? MB : 3>{}); break;
+      default: run(std::integral_constant<int, MB>{}); break;
+    }
+    // what follows is formed from the lane's number anew: kept from tile to tile it
+    // would not fit the registers next to the products
+    int me = lane;
+    asm volatile("" : "+v"(me));
+    // the channels' scales, ahead of the next tile's loads: they come back first
+    f32x4_t sc[2][4];
+    if (live > 0) {
+      const int64_t w_row = (int64_t)now.expert * a.cols + now_col0;
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.w_scales + w_row, (uint32_t)now_cols * 4u);
+      const __amdgpu_buffer_rsrc_t rt =
+          make_rsrc((UP ? a.w_up_scales : a.w_scales) + w_row, (uint32_t)now_cols * 4u);
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          sc[f][q] = __builtin_bit_cast(
+              f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                           UP && f ? rt : rs,
+                           (int)((uint32_t)((UP ? 32 * wp : b_row[f]) + 8 * q + 4 * (me >> 5)) * 4u), 0, 0));
+    }
+    if (it + 1 < list.count) {
+      // all waves have read their last fragments before LDS is filled again
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      block_barrier();
+      open(it + 1);
+      load_first();
+    }
+
+    // The products have the weights first, so a lane holds output row (l & 31) of a
+    // block and columns 8 (r / 4) + 4 (l / 32) + r % 4.  Columns of two register
+    // groups are joined with the other half's to eight (16 bytes), then rows trade
+    // places between lanes: eight lanes hold 64 columns of a row, a whole line
+    // (with UP four lanes 32 columns).
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      if (m >= live) break;
+      uint32_t v[2][2][4];  // [f][column groups 2 u and 2 u + 1]
+#pragma unroll
+      for (int f = 0; f < (UP ? 1 : 2); ++f)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int q = 2 * u + g, r = 4 * q + 2 * j + e;
+                y[e] = (float)acc[m][f][r] * (sr[m] * sc[f][q][2 * j + e]);
+                if (UP) y[e] = silu_mul(y[e], (float)acc[m][1][r] * (sr[m] * sc[1][q][2 * j + e]));
+              }
+              v[f][u][2 * g + j] = pack_bf16(y[0], y[1]);
+            }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) swap_halves(v[f][u][j], v[f][u][2 + j]);
         }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + sub, at = 32 * (first + m) + r;
-        const char* from = mine + r * kRow + ch * 16;
-        const u32x2_t lo = *reinterpret_cast<const u32x2_t*>(from);
-        const u32x2_t hi = *reinterpret_cast<const u32x2_t*>(from + 8);
-        if (col_ok && at < rows)
-          *reinterpret_cast<u32x4_t*>(a.out + (tile.row0 + at) * a.cols + col) =
-              u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+      for (int f = 0; f < (UP ? 1 : 2); ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) swap_rows16(v[f][0][j], v[f][1][j]);
+      auto store = [&](const uint32_t (&w)[4], int r, int c) {
+        const int at = 32 * (first + m) + r;
+        if (at < now.rows && c < now_cols)
+          *reinterpret_cast<u32x4_t*>(a.out + (now.row0 + at) * a.cols + now_col0 + c) =
+              u32x4_t{w[0], w[1], w[2], w[3]};
+      };
+      if constexpr (UP) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          store(v[0][u], 16 * u + (me & 15),
+                32 * wp + 16 * ((me >> 4) & 1) + 8 * (me >> 5));
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) swap_rows8(v[0][u][j], v[1][u][j]);
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            store(v[f][u], 16 * u + 8 * f + line_row(me), 64 * wp + line_col(me));
+        }
       }
     }
   }
 }
 
-// Dense: the tiles of four row tiles follow each other on a column tile, so that
-// the blocks of an XCD at work together share both operands.
-constexpr int kRowGroup = 4;
+// Dense: the tiles of four row tiles follow each other on a column tile.
+constexpr uint32_t kRowGroup = 4;
 
-template <bool UP>
-__global__ __launch_bounds__(512, 2) void int8_dense_kernel(Int8Args a, int64_t m_tiles,
-                                                            int col_tiles) {
+template <int MB, bool UP>
+__global__ __launch_bounds__(512, 2) void int8_dense_kernel(Int8Args a, uint32_t m_tiles,
+                                                            uint32_t col_tiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  int64_t item;
-  if (!xcd_item(blockIdx.x, m_tiles * col_tiles, item)) return;
-  const int64_t group = item / (kRowGroup * col_tiles), in = item % (kRowGroup * col_tiles);
-  const int deep = (int)min((int64_t)kRowGroup, m_tiles - group * kRowGroup);
-  Tile t;
-  t.expert = 0;
-  t.row0 = (group * kRowGroup + in % deep) * TileShape<4>::rows;
-  t.rows = (int)min((int64_t)TileShape<4>::rows, a.rows - t.row0);
-  int8_tile<4, UP>(a, t, (int)(in / deep), lds);
+  List list;
+  list.fill(m_tiles * col_tiles, [&](uint32_t item, uint32_t& nt) {
+    const uint32_t group = item / (kRowGroup * col_tiles), in = item % (kRowGroup * col_tiles);
+    const uint32_t deep = min(kRowGroup, m_tiles - group * kRowGroup);
+    nt = in / deep;
+    Tile t;
+    t.expert = 0;
+    t.row0 = (int64_t)(group * kRowGroup + in % deep) * TileShape<MB>::rows;
+    t.rows = (int)min((int64_t)TileShape<MB>::rows, a.rows - t.row0);
+    return t;
+  });
+  if (list.count > 0) int8_tiles<MB, UP>(a, list, lds);
 }
 
-template <bool UP>
-__global__ __launch_bounds__(512, 2) void int8_grouped_kernel(Int8Args a, int col_tiles) {
+template <int MB, bool UP>
+__global__ __launch_bounds__(512, 2) void int8_grouped_kernel(Int8Args a, uint32_t col_tiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  constexpr uint32_t bm = TileShape<5>::rows;
-  Segments s;
-  s.read(a, bm, true);
-  int64_t item;
-  if (!xcd_item(blockIdx.x, (int64_t)s.total * col_tiles, item)) return;
-  const Tile t = s.tile((uint32_t)(item / col_tiles), bm, true);
-  if (t.rows <= 0) return;
-  int8_tile<5, UP>(a, t, (int)(item % col_tiles), lds);
+  constexpr uint32_t bm = TileShape<MB>::rows;
+  List list;
+  {
+    Segments s;
+    s.read(a, bm);
+    list.fill(s.total * col_tiles, [&](uint32_t item, uint32_t& nt) {
+      nt = item % col_tiles;
+      return s.tile(item / col_tiles, bm, true);
+    });
+  }
+  if (list.count > 0) int8_tiles<MB, UP>(a, list, lds);
+}
+
+// Few rows: a block takes 16 RG rows and 16 CB columns (of each weight), its four
+// waves share out k, 128 bytes (a line of every row) in turn, straight from memory
+// into the matrix instructions' registers (v_mfma_i32_16x16x64_i8), kDepth lines of
+// each row in flight a wave; the waves' sums meet in LDS (integers: in any order
+// the same).
+template <int RG, int CB, bool UP, bool GROUPED>
+__global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_tiles) {
+  constexpr int NB = UP ? 2 * CB : CB, kOut = RG * NB;
+  constexpr int kDepth = RG + NB >= 8 ? 2 : RG + NB >= 5 ? 3 : 16 / (RG + NB);
+  constexpr int kBm = 16 * RG, kOc = 16 * CB;
+  __shared__ __attribute__((aligned(16))) i32x4_t sums[4][kOut][64];
+  Tile tile;
+  const int nt = (int)(blockIdx.x % (unsigned)col_tiles);
+  const uint32_t mt = blockIdx.x / (unsigned)col_tiles;
+  if constexpr (GROUPED) {
+    Segments s;
+    s.read(a, kBm);
+    if (mt >= s.total) return;
+    tile = s.tile(mt, kBm, false);
+    if (tile.rows <= 0) return;
+  } else {
+    tile.expert = 0;
+    tile.row0 = (int64_t)mt * kBm;
+    tile.rows = (int)min((int64_t)kBm, a.rows - tile.row0);
+  }
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, piece = 16 * (lane >> 4);
+  const int col0 = nt * kOc, cols = min(kOc, a.cols - col0);
+  const int64_t w_row = (int64_t)tile.expert * a.cols + col0;
+  const uint32_t w_bytes = (uint32_t)cols * (uint32_t)a.k;
+  const __amdgpu_buffer_rsrc_t ra =
+      a.sorted_src ? make_rsrc(a.a, (uint32_t)(a.a_rows * a.k))
+                   : make_rsrc(a.a + tile.row0 * a.k, (uint32_t)tile.rows * (uint32_t)a.k);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + w_row * a.k, w_bytes);
+  const __amdgpu_buffer_rsrc_t ru = make_rsrc((UP ? a.w_up : a.w) + w_row * a.k, w_bytes);
+  uint32_t a_off[RG], b_off[CB];
+#pragma unroll
+  for (int r = 0; r < RG; ++r) {
+    const int i = 16 * r + row;
+    a_off[r] = kNoRow;
+    if (i < tile.rows)
+      a_off[r] = (uint32_t)(a.sorted_src ? a_row_of(a, tile.row0 + i) : i) * (uint32_t)a.k;
+  }
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+    b_off[c] = 16 * c + row < cols ? (uint32_t)(16 * c + row) * (uint32_t)a.k : kNoRow;
+
+  i32x4_t fa[kDepth][2][RG], fb[kDepth][2][NB], acc[RG][NB];
+  // line i of this wave
+  auto load = [&](int buf, int i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = (4 * i + wave) * 128 + 64 * h + piece;
+      const bool in = at < a.k;
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        const uint32_t off = b_off[c % CB];
+        fb[buf][h][c] = __builtin_bit_cast(
+            i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         c < CB ? rw : ru, (int)(in && off != kNoRow ? off + (uint32_t)at : kNoRow),
+                         0, 0));
+      }
+#pragma unroll
+      for (int r = 0; r < RG; ++r)
+        fa[buf][h][r] = __builtin_bit_cast(
+            i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         ra, (int)(in && a_off[r] != kNoRow ? a_off[r] + (uint32_t)at : kNoRow), 0,
+                         0));
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < RG; ++r)
+#pragma unroll
+    for (int c = 0; c < NB; ++c) acc[r][c] = i32x4_t{0, 0, 0, 0};
+  const int lines = (a.k + 127) / 128, mine = (lines - wave + 3) / 4;  // of this wave
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load(d, d);
+  for (int i = 0; i < mine; i += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+          for (int r = 0; r < RG; ++r)
+            acc[r][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[d][h][c], fa[d][h][r], acc[r][c],
+                                                              0, 0, 0);
+      load(d, i + kDepth + d);  // past the wave's last line: zeros, without a memory access
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RG; ++r)
+#pragma unroll
+    for (int c = 0; c < NB; ++c) sums[wave][r * NB + c][lane] = acc[r][c];
+  __syncthreads();
+  // output block (r, c) of the columns: wave (r CB + c) % 4; lane l has row l & 15
+  // and columns 4 (l / 16) ..
+  for (int o = wave; o < RG * CB; o += 4) {
+    const int r = o / CB, c = o % CB;
+    const int i = 16 * r + row, col = 16 * c + 4 * (lane >> 4);
+    if (i >= tile.rows || col >= cols) continue;
+    auto total = [&](int b) {
+      i32x4_t t = sums[0][b][lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) t += sums[w][b][lane];
+      return t;
+    };
+    const float sr = a.a_scales[a_row_of(a, tile.row0 + i)];
+    const f32x4_t sc = *reinterpret_cast<const f32x4_t*>(a.w_scales + w_row + col);
+    const i32x4_t g = total(r * NB + c);
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = (float)g[j] * (sr * sc[j]);
+    if constexpr (UP) {
+      const f32x4_t su = *reinterpret_cast<const f32x4_t*>(a.w_up_scales + w_row + col);
+      const i32x4_t u = total(r * NB + CB + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = silu_mul(y[j], (float)u[j] * (sr * su[j]));
+    }
+    *reinterpret_cast<u32x2_t*>(a.out + (tile.row0 + i) * a.cols + col0 + col) =
+        u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+  }
 }
 
 }  // namespace
@@ -527,36 +703,127 @@ hipError_t launch_quant_int8(const uint16_t* X, int64_t n, int cols, int8_t* Q, 
 namespace {
 // Both launches' kernels use all of a CU's LDS.
 template <class Kernel, class... Args>
-hipError_t launch_tiles(Kernel kernel, std::atomic<uint32_t>& configured, int64_t blocks,
+hipError_t launch_tiles(Kernel kernel, int lds, std::atomic<uint32_t>& configured, int64_t blocks,
                         hipStream_t stream, Args... args) {
-  const hipError_t e = set_lds_limit_once((const void*)kernel, kLds, configured);
+  const hipError_t e = set_lds_limit_once((const void*)kernel, lds, configured);
   if (e != hipSuccess) return e;
   if (blocks >= (int64_t(1) << 23)) return hipErrorInvalidConfiguration;  // 2^32 threads
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(512), kLds, stream, args...);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(512), lds, stream, args...);
   return hipGetLastError();
 }
-int64_t xcd_blocks(int64_t work) { return (work + kXcds - 1) / kXcds * kXcds; }
+// Blocks for that many tiles: one a CU, unless their lists overflow.
+int64_t tile_blocks(int64_t tiles) {
+  const int64_t need = std::max(std::min<int64_t>(tiles, kCus), (tiles + kListed - 1) / kListed);
+  return (need + kXcds - 1) / kXcds * kXcds;
+}
+
+// Tiles of bm rows, at most: experts without rows have none.
+int64_t most_tiles(const Int8Args& a, int64_t bm) {
+  return a.offsets ? a.rows / bm + std::min<int64_t>(a.E, a.rows) : (a.rows + bm - 1) / bm;
+}
+
+template <int RG, int CB>
+hipError_t launch_few(const Int8Args& a, hipStream_t stream) {
+  const int col_tiles = (a.cols + 16 * CB - 1) / (16 * CB);
+  const int64_t blocks = most_tiles(a, 16 * RG) * col_tiles;
+  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;  // 2^32 threads
+  const dim3 grid((unsigned)blocks), block(256);
+  if (a.offsets && a.w_up)
+    hipLaunchKernelGGL((int8_few_kernel<RG, CB, true, true>), grid, block, 0, stream, a, col_tiles);
+  else if (a.offsets)
+    hipLaunchKernelGGL((int8_few_kernel<RG, CB, false, true>), grid, block, 0, stream, a, col_tiles);
+  else if (a.w_up)
+    hipLaunchKernelGGL((int8_few_kernel<RG, CB, true, false>), grid, block, 0, stream, a, col_tiles);
+  else
+    hipLaunchKernelGGL((int8_few_kernel<RG, CB, false, false>), grid, block, 0, stream, a, col_tiles);
+  return hipGetLastError();
+}
 }  // namespace
 
-hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream) {
-  static std::atomic<uint32_t> configured[4];
+namespace {
+int column_tiles(const Int8Args& a) {
   const int oc = a.w_up ? kCols / 2 : kCols;
-  const int col_tiles = (a.cols + oc - 1) / oc;
-  if (a.offsets) {
-    const int64_t bm = TileShape<5>::rows;
-    const int64_t m_tiles = a.rows / bm + std::min<int64_t>(a.E, a.rows);
-    const int64_t blocks = xcd_blocks(m_tiles * col_tiles);
-    if (a.w_up)
-      return launch_tiles(int8_grouped_kernel<true>, configured[0], blocks, stream, a, col_tiles);
-    return launch_tiles(int8_grouped_kernel<false>, configured[1], blocks, stream, a, col_tiles);
-  }
-  const int64_t bm = TileShape<4>::rows, m_tiles = (a.rows + bm - 1) / bm;
-  const int64_t blocks = xcd_blocks(m_tiles * col_tiles);
+  return (a.cols + oc - 1) / oc;
+}
+template <int MB>
+hipError_t launch_grouped(const Int8Args& a, hipStream_t stream) {
+  static std::atomic<uint32_t> configured[2];
+  const int col_tiles = column_tiles(a);
+  const int64_t blocks = tile_blocks(most_tiles(a, TileShape<MB>::rows) * col_tiles);
   if (a.w_up)
-    return launch_tiles(int8_dense_kernel<true>, configured[2], blocks, stream, a, m_tiles,
-                        col_tiles);
-  return launch_tiles(int8_dense_kernel<false>, configured[3], blocks, stream, a, m_tiles,
-                      col_tiles);
+    return launch_tiles(int8_grouped_kernel<MB, true>, TileShape<MB>::lds, configured[0], blocks,
+                        stream, a, (uint32_t)col_tiles);
+  return launch_tiles(int8_grouped_kernel<MB, false>, TileShape<MB>::lds, configured[1], blocks,
+                      stream, a, (uint32_t)col_tiles);
+}
+template <int MB>
+hipError_t launch_dense(const Int8Args& a, hipStream_t stream) {
+  static std::atomic<uint32_t> configured[2];
+  const int col_tiles = column_tiles(a);
+  const int64_t m_tiles = most_tiles(a, TileShape<MB>::rows);
+  const int64_t blocks = tile_blocks(m_tiles * col_tiles);
+  if (a.w_up)
+    return launch_tiles(int8_dense_kernel<MB, true>, TileShape<MB>::lds, configured[0], blocks,
+                        stream, a, (uint32_t)m_tiles, (uint32_t)col_tiles);
+  return launch_tiles(int8_dense_kernel<MB, false>, TileShape<MB>::lds, configured[1], blocks,
+                      stream, a, (uint32_t)m_tiles, (uint32_t)col_tiles);
+}
+}  // namespace
+
+namespace {
+// Tiles of bm rows that are expected: every expert with rows has its share of
+// them, and half a tile more where that share is over half a tile.
+double expected_tiles(const Int8Args& a, int bm) {
+  if (!a.offsets) return (double)((a.rows + bm - 1) / bm);
+  const double experts = (double)std::min<int64_t>(a.E, a.rows), share = (double)a.rows / experts;
+  return experts * std::max(1.0, share / bm + 0.5);
+}
+// Microseconds of a launch, by a fit to what shapes from 1 to 16384 rows, 512 to
+// 8192 deep, took dense and with 16 to 384 experts (within a fifth of most).
+// Tiles: 0.22 (MB + 1) a stage and 1 a tile, 256 at a time.
+double tile_cost(const Int8Args& a, int mb) {
+  const double rounds = std::ceil(expected_tiles(a, 64 * mb) * column_tiles(a) / kCus);
+  return 3.5 + rounds * (1.0 + (a.k + kStage - 1) / kStage * 0.22 * (mb + 1));
+}
+// Few rows: what the blocks read at 8 TB/s, 1.2 for every further 256 blocks (twice
+// that where each looks for its expert), but no block faster than its own operands
+// at 40 KB a microsecond.
+double few_cost(const Int8Args& a, int rg, int cb) {
+  const int nb = a.w_up ? 2 * cb : cb;
+  const double tiles = expected_tiles(a, 16 * rg);
+  const double rows = std::min((double)a.rows / tiles, 16.0 * rg);
+  const double blocks = tiles * ((a.cols + 16 * cb - 1) / (16 * cb));
+  const double bytes = (rows + 16.0 * nb) * a.k;  // of a block
+  const double more = (a.offsets ? 2.4 : 1.2) * std::max(0.0, blocks / kCus - 1.0);
+  return (a.offsets ? 5.0 : 4.2) + std::max(blocks * bytes / 8e6 + more, bytes / 40e3);
+}
+}  // namespace
+
+// The cheapest form by the fits above.  2560 x 2560 weights, us: 1 row 5.3 (few,
+// 1 x 1; tiles of MB 1 11.7), 64 rows 8.6 (few, 2 x 2; 11.7), 512 rows 12.7 (MB 1;
+// MB 4 27, few 4 x 4 25), 4096 rows 29 (MB 3; MB 1 42); 8192 x 8192 x 8192 405 (MB
+// 4; MB 2 449).
+hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream) {
+  typedef hipError_t (*Launch)(const Int8Args&, hipStream_t);
+  struct Form {
+    double cost;
+    Launch launch;
+  };
+  const Form forms[] = {
+      {tile_cost(a, 1), a.offsets ? launch_grouped<1> : launch_dense<1>},
+      {tile_cost(a, 2), a.offsets ? launch_grouped<2> : launch_dense<2>},
+      {tile_cost(a, 3), a.offsets ? launch_grouped<3> : launch_dense<3>},
+      {tile_cost(a, 4), a.offsets ? launch_grouped<4> : launch_dense<4>},
+      {few_cost(a, 1, 1), launch_few<1, 1>},
+      {few_cost(a, 1, 2), launch_few<1, 2>},
+      {few_cost(a, 2, 1), launch_few<2, 1>},
+      {few_cost(a, 2, 2), launch_few<2, 2>},
+      {few_cost(a, 4, 2), launch_few<4, 2>},
+  };
+  const Form* best = forms;
+  for (const Form& f : forms)
+    if (f.cost < best->cost) best = &f;
+  return best->launch(a, stream);
 }
 
 }  // namespace moe

@@ -61,6 +61,7 @@
 #include "common.h"
 #include "gemm_args.h"
 #include "kernels.h"
+#include "lane_swaps.h"
 
 namespace moe {
 
@@ -90,7 +91,6 @@ constexpr int64_t kMaxGradBlocks = (1 << 24) - 8;  // a grid's threads stay belo
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 // The wave's LDS reads have come back before it lets the others on: what they
 // read may be overwritten then.
@@ -98,10 +98,6 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const bf16x2_t v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
 }
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
@@ -211,26 +207,6 @@ __device__ __forceinline__ void multiply(const Fragments<LIVE>& f, floatx16_t (&
 // The accumulators hold the wave's 128 x 64 outputs transposed (the B fragment
 // is the first operand): lane l has row (l & 31) of a block and columns
 // 8 (r / 4) + 4 (l / 32) + r % 4 of its register r.
-//
-// The upper 32 lanes' a change places with the lower lanes' b; the odd rows'
-// (of 16 lanes) a with the even rows' b; within every 16 lanes, the upper
-// eight's a with the lower eight's b.
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b) {
-  constexpr int kRor8 = 0x128;  // row_ror:8; the bank masks write one half of the 16
-  const uint32_t a0 = a;
-  a = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, kRor8, 0xF, 0xC, false);
-  b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a0, kRor8, 0xF, 0x3, false);
-}
 
 // bf16 results, sixteen stores of 8 rows x 128 bytes: a lane's four columns of
 // two register groups are joined with the other half's to eight (16 bytes),
@@ -239,10 +215,6 @@ __device__ __forceinline__ void swap_rows8(uint32_t& a, uint32_t& b) {
 // time).  Always sixteen: rows and columns past the result fall outside the
 // buffer.  Lane l stores row line_row(l), columns line_col(l) .. + 7 of every
 // group of eight rows; `at` is that place's byte offset, pitch a row's bytes.
-__device__ __forceinline__ int line_row(int lane) { return lane & 7; }
-__device__ __forceinline__ int line_col(int lane) {
-  return 32 * ((lane >> 3) & 1) + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
-}
 constexpr uint32_t kNoStore = 0x80000000u;  // past any result (below 2 GiB)
 template <int CPOL>
 __device__ __forceinline__ void store_lines(const floatx16_t (&acc)[4][2],

@@ -24,6 +24,7 @@
 #include "common.h"
 #include "fp8_codes.h"
 #include "kernels.h"
+#include "lane_swaps.h"
 
 namespace moe {
 namespace {
@@ -31,12 +32,6 @@ namespace {
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const bf16x2_t v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
-}
 
 // What a thread moves of a row: 16 bytes, or one element where the rows are not
 // whole aligned 16-byte words.
