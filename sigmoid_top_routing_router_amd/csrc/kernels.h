@@ -97,9 +97,10 @@ int64_t perm_max_tiles(int64_t pairs, int E, int bm);
 // (the shared expert folded into the weight-streaming products).
 hipError_t launch_permute(const int32_t* ids, int64_t N, int E, int K, int bm, int xr,
                           const PermWork& w, hipStream_t stream, int shared_rows = 0);
-// The public grouping: pairs whose id lies outside [0, E) come last, with
-// sorted_src and src_pos -1; block_counts holds perm_count_rows(pairs) * (E + 1)
-// words.  No m-tile table.
+// The grouping for callers outside the layer: pairs whose id lies outside [0, E)
+// have no place (-1 in sorted_src, behind the others, and in src_pos).
+// block_counts holds group_work_words(pairs, E) words.  No m-tile table.
+size_t group_work_words(int64_t pairs, int E);
 hipError_t launch_group(const int32_t* ids, int64_t pairs, int E, int32_t* counts,
                         int32_t* offsets, int32_t* sorted_src, int32_t* src_pos,
                         uint32_t* block_counts, hipStream_t stream);

@@ -42,22 +42,6 @@ constexpr int kPermWaves = 4;       // waves (chunks) per block
 constexpr int kPermMaxBlocks = 64;  // blocks of the two chunk kernels, at most
 constexpr int kMaxE = 384;
 
-// DROP (the public grouping): the last of the E buckets holds the pairs whose
-// id is no expert of the caller's, [0, E - 1); it has no count and no offset of
-// its own, and its pairs have no place in the grouped order.  There are no
-// m-tiles then.
-template <bool DROP>
-__device__ __forceinline__ uint32_t bucket_of(int32_t id, int E) {
-  return DROP ? min((uint32_t)id, (uint32_t)(E - 1)) : (uint32_t)id;
-}
-template <bool DROP>
-__device__ __forceinline__ void place_pair(uint32_t e, int E, int32_t pair, uint32_t dst,
-                                           int32_t* sorted_src, int32_t* src_pos) {
-  const bool here = !DROP || e != (uint32_t)(E - 1);
-  sorted_src[dst] = here ? pair : -1;
-  src_pos[pair] = here ? (int32_t)dst : -1;
-}
-
 // Pairs per chunk: 512, or more so that the batch needs at most
 // kPermMaxBlocks blocks; a multiple of 64.
 static int64_t perm_chunk(int64_t pairs) {
@@ -93,29 +77,27 @@ __device__ __forceinline__ void emit_tiles(int32_t* tiles, uint32_t t0, int e, u
   }
 }
 
-template <bool DROP>
 __global__ __launch_bounds__(256) void perm_count_kernel(
     const int32_t* __restrict__ ids, int64_t pairs, int E, int64_t cw,
     uint32_t* __restrict__ block_counts) {
-  __shared__ uint32_t cnt[kMaxE + DROP];
+  __shared__ uint32_t cnt[kMaxE];
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0u;
   __syncthreads();
   const int64_t i0 = (int64_t)blockIdx.x * kPermWaves * cw;
   const int64_t i1 = min(pairs, i0 + kPermWaves * cw);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) atomicAdd(&cnt[bucket_of<DROP>(ids[i], E)], 1u);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) atomicAdd(&cnt[ids[i]], 1u);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x)
     block_counts[(size_t)blockIdx.x * E + e] = cnt[e];
 }
 
-template <bool DROP>
 __global__ __launch_bounds__(256) void perm_scatter_kernel(
     const int32_t* __restrict__ ids, int64_t pairs, int E, int64_t cw, int64_t n_blocks,
     const uint32_t* __restrict__ block_counts, int bm, int xr, int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ tiles, int32_t* __restrict__ n_tiles,
     int32_t* __restrict__ sorted_src, int32_t* __restrict__ src_pos) {
-  __shared__ uint32_t pos[kPermWaves][kMaxE + DROP];  // chunk counts, then chunk bases
-  __shared__ uint32_t base_s[kMaxE + DROP];    // segment start + pairs of earlier blocks
+  __shared__ uint32_t pos[kPermWaves][kMaxE];  // chunk counts, then chunk bases
+  __shared__ uint32_t base_s[kMaxE];           // segment start + pairs of earlier blocks
   __shared__ uint32_t wsum_c[4], wsum_t[4];
   const int tid = threadIdx.x, w = tid >> 6, lane = lane_id();
   const int64_t b = blockIdx.x;
@@ -123,7 +105,7 @@ __global__ __launch_bounds__(256) void perm_scatter_kernel(
   const int64_t i1 = min(pairs, i0 + cw);
   for (int e = lane; e < E; e += kWave) pos[w][e] = 0u;
   __builtin_amdgcn_wave_barrier();
-  for (int64_t i = i0 + lane; i < i1; i += kWave) atomicAdd(&pos[w][bucket_of<DROP>(ids[i], E)], 1u);
+  for (int64_t i = i0 + lane; i < i1; i += kWave) atomicAdd(&pos[w][ids[i]], 1u);
 
   // Totals and earlier-block sums of experts 2 tid and 2 tid + 1 (E <= 512),
   // so that the block-wide scan below runs in expert order.
@@ -164,19 +146,19 @@ __global__ __launch_bounds__(256) void perm_scatter_kernel(
   for (int i = 0; i < w; ++i) { bc += wsum_c[i]; bt += wsum_t[i]; }
   const uint32_t off0 = bc + ic - (tot0 + tot1), toff0 = bt + it - (t0 + t1);
   if (b == 0) {
-    if (!DROP && tid == 255) {
+    if (tid == 255) {
       offsets[E] = (int32_t)(bc + ic);
       *n_tiles = (int32_t)(bt + it);
     }
     if (e0 < E) {
-      if (e0 < E - DROP) counts[e0] = (int32_t)tot0;
+      counts[e0] = (int32_t)tot0;
       offsets[e0] = (int32_t)off0;
-      if (!DROP) emit_tiles(tiles, toff0, e0, off0, tot0, t0, bm);
+      emit_tiles(tiles, toff0, e0, off0, tot0, t0, bm);
     }
     if (e1 < E) {
-      if (e1 < E - DROP) counts[e1] = (int32_t)tot1;
+      counts[e1] = (int32_t)tot1;
       offsets[e1] = (int32_t)(off0 + tot0);
-      if (!DROP) emit_tiles(tiles, toff0 + t0, e1, off0 + tot0, tot1, t1, bm);
+      emit_tiles(tiles, toff0 + t0, e1, off0 + tot0, tot1, t1, bm);
     }
   }
   if (e0 < E) base_s[e0] = off0 + pre0;
@@ -196,7 +178,7 @@ __global__ __launch_bounds__(256) void perm_scatter_kernel(
   for (int64_t j = i0; j < i1; j += kWave) {
     const int64_t i = j + lane;
     const bool ok = i < i1;
-    const uint32_t e = ok ? bucket_of<DROP>(ids[i], E) : 0u;
+    const uint32_t e = ok ? (uint32_t)ids[i] : 0u;
     uint64_t mask = ballot(ok);
 #pragma unroll
     for (int bit_i = 0; bit_i < 9; ++bit_i) {
@@ -206,8 +188,9 @@ __global__ __launch_bounds__(256) void perm_scatter_kernel(
     }
     const uint64_t lower = mask & lanemask_lt();
     if (ok) {
-      place_pair<DROP>(e, E, (int32_t)i, pos[w][e] + (uint32_t)__popcll(lower), sorted_src,
-                       src_pos);
+      const uint32_t dst = pos[w][e] + (uint32_t)__popcll(lower);
+      sorted_src[dst] = (int32_t)i;
+      src_pos[i] = (int32_t)dst;
     }
     __builtin_amdgcn_wave_barrier();
     if (ok && lower == 0ull) pos[w][e] += (uint32_t)__popcll(mask);
@@ -242,23 +225,21 @@ __global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ 
 constexpr int kSmallWaves = 16;
 constexpr int64_t kSmallPairs = 16384;
 
-template <bool DROP>
 __global__ __launch_bounds__(1024) void perm_small_kernel(
     const int32_t* __restrict__ ids, int64_t pairs, int E, int bm, int xr,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ sorted_src, int32_t* __restrict__ src_pos,
     int32_t* __restrict__ tiles, int32_t* __restrict__ n_tiles, int shared_rows) {
-  constexpr int kBuckets = kMaxE + DROP;
-  __shared__ uint32_t wcnt[kSmallWaves][kBuckets];  // counts, then bases per wave
-  __shared__ uint32_t tot[kBuckets];
+  __shared__ uint32_t wcnt[kSmallWaves][kMaxE];  // counts, then bases per wave
+  __shared__ uint32_t tot[kMaxE];
   __shared__ uint32_t wsum_c[kSmallWaves], wsum_t[kSmallWaves];
   const int tid = threadIdx.x, w = tid >> 6, lane = lane_id();
   const int64_t len = (pairs + kSmallWaves - 1) / kSmallWaves;
   const int64_t i0 = (int64_t)w * len;
   const int64_t i1 = min(pairs, i0 + len);
-  for (int i = tid; i < kSmallWaves * kBuckets; i += blockDim.x) (&wcnt[0][0])[i] = 0u;
+  for (int i = tid; i < kSmallWaves * kMaxE; i += blockDim.x) (&wcnt[0][0])[i] = 0u;
   __syncthreads();
-  for (int64_t i = i0 + lane; i < i1; i += kWave) atomicAdd(&wcnt[w][bucket_of<DROP>(ids[i], E)], 1u);
+  for (int64_t i = i0 + lane; i < i1; i += kWave) atomicAdd(&wcnt[w][ids[i]], 1u);
   __syncthreads();
   // (2) bases of the waves inside each expert's segment (exclusive), totals
   for (int e = tid; e < E; e += blockDim.x) {
@@ -283,7 +264,7 @@ __global__ __launch_bounds__(1024) void perm_small_kernel(
   for (int q = 0; q < w; ++q) { bc += wsum_c[q]; bt += wsum_t[q]; }
   const uint32_t off = bc + ic - c;
   uint32_t toff = bt + it - t;
-  if (!DROP && tid == blockDim.x - 1) {
+  if (tid == blockDim.x - 1) {
     offsets[E] = (int32_t)(bc + ic);
     // the shared expert's tiles after the routed ones, 16 rows each: the
     // weight-streaming kernel streams a tile's weights once per 16 rows, so
@@ -295,9 +276,9 @@ __global__ __launch_bounds__(1024) void perm_small_kernel(
     *n_tiles = (int32_t)nt;
   }
   if (tid < E) {
-    if (tid < E - DROP) counts[tid] = (int32_t)c;
+    counts[tid] = (int32_t)c;
     offsets[tid] = (int32_t)off;
-    if (!DROP) emit_tiles(tiles, toff, tid, off, c, t, bm);
+    emit_tiles(tiles, toff, tid, off, c, t, bm);
     tot[tid] = off;  // segment starts, for the scatter
   }
   __syncthreads();
@@ -307,7 +288,7 @@ __global__ __launch_bounds__(1024) void perm_small_kernel(
   for (int64_t j = i0; j < i1; j += kWave) {
     const int64_t i = j + lane;
     const bool ok = i < i1;
-    const uint32_t e = ok ? bucket_of<DROP>(ids[i], E) : 0u;
+    const uint32_t e = ok ? (uint32_t)ids[i] : 0u;
     uint64_t mask = ballot(ok);
 #pragma unroll
     for (int b = 0; b < 9; ++b) {
@@ -317,8 +298,9 @@ __global__ __launch_bounds__(1024) void perm_small_kernel(
     }
     const uint64_t lower = mask & lanemask_lt();
     if (ok) {
-      place_pair<DROP>(e, E, (int32_t)i, wcnt[w][e] + (uint32_t)__popcll(lower), sorted_src,
-                       src_pos);
+      const uint32_t dst = wcnt[w][e] + (uint32_t)__popcll(lower);
+      sorted_src[dst] = (int32_t)i;
+      src_pos[i] = (int32_t)dst;
     }
     __builtin_amdgcn_wave_barrier();
     if (ok && lower == 0ull) wcnt[w][e] += (uint32_t)__popcll(mask);
@@ -330,7 +312,7 @@ hipError_t launch_permute(const int32_t* ids, int64_t N, int E, int K, int bm, i
                           const PermWork& w, hipStream_t stream, int shared_rows) {
   const int64_t pairs = N * (int64_t)K;
   if (pairs <= kSmallPairs) {
-    hipLaunchKernelGGL(perm_small_kernel<false>, dim3(1), dim3(1024), 0, stream, ids, pairs, E, bm, xr,
+    hipLaunchKernelGGL(perm_small_kernel, dim3(1), dim3(1024), 0, stream, ids, pairs, E, bm, xr,
                        w.counts, w.offsets, w.sorted_src, w.src_pos, w.tiles, w.n_tiles,
                        shared_rows);
     return hipGetLastError();
@@ -339,31 +321,11 @@ hipError_t launch_permute(const int32_t* ids, int64_t N, int E, int K, int bm, i
   const int64_t cw = perm_chunk(pairs);
   const int64_t n_blocks = perm_count_rows(pairs);
   const dim3 grid((unsigned)n_blocks), block(256);
-  hipLaunchKernelGGL(perm_count_kernel<false>, grid, block, 0, stream, ids, pairs, E, cw,
+  hipLaunchKernelGGL(perm_count_kernel, grid, block, 0, stream, ids, pairs, E, cw,
                      w.block_counts);
-  hipLaunchKernelGGL(perm_scatter_kernel<false>, grid, block, 0, stream, ids, pairs, E, cw, n_blocks,
+  hipLaunchKernelGGL(perm_scatter_kernel, grid, block, 0, stream, ids, pairs, E, cw, n_blocks,
                      w.block_counts, bm, xr, w.counts, w.offsets, w.tiles, w.n_tiles,
                      w.sorted_src, w.src_pos);
-  return hipGetLastError();
-}
-
-hipError_t launch_group(const int32_t* ids, int64_t pairs, int E, int32_t* counts,
-                        int32_t* offsets, int32_t* sorted_src, int32_t* src_pos,
-                        uint32_t* block_counts, hipStream_t stream) {
-  const int B = E + 1;  // the last bucket: pairs without an expert
-  if (pairs <= kSmallPairs) {
-    hipLaunchKernelGGL(perm_small_kernel<true>, dim3(1), dim3(1024), 0, stream, ids, pairs, B, 1,
-                       0, counts, offsets, sorted_src, src_pos, nullptr, nullptr, 0);
-    return hipGetLastError();
-  }
-  const int64_t cw = perm_chunk(pairs);
-  const int64_t n_blocks = perm_count_rows(pairs);
-  const dim3 grid((unsigned)n_blocks), block(256);
-  hipLaunchKernelGGL(perm_count_kernel<true>, grid, block, 0, stream, ids, pairs, B, cw,
-                     block_counts);
-  hipLaunchKernelGGL(perm_scatter_kernel<true>, grid, block, 0, stream, ids, pairs, B, cw,
-                     n_blocks, block_counts, 1, 0, counts, offsets, nullptr, nullptr, sorted_src,
-                     src_pos);
   return hipGetLastError();
 }
 

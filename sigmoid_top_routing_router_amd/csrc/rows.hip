@@ -18,7 +18,6 @@
 // rule of fp8_quant.hip): unpermute can leave them for the rows that it reads,
 // permute and unpermute_backward read them in the place of bf16 rows.
 #include <algorithm>
-#include <initializer_list>
 #include <type_traits>
 
 #include "common.h"
@@ -33,13 +32,21 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
-// What a thread moves of a row: 16 bytes, or one element where the rows are not
-// whole aligned 16-byte words.
+// What a thread moves of a row: 16 bytes, at any element (gfx950 takes them from any
+// address), or one element of rows shorter than that.  The last piece of a row that
+// is not whole pieces ends with the row and repeats elements of the one before it:
+// copies and sums write the same values there twice, dot products leave them out.
+// (Element by element, 1237 tokens of 777 fp32, five each: the gradients 18.8 us;
+// this way GRAD_ODD_US.)
 template <bool F32, bool VEC>
 struct Piece;
+typedef u32x4_t u32x4b_t __attribute__((aligned(2)));  // of bf16 elements
+typedef u32x4_t u32x4f_t __attribute__((aligned(4)));  // of fp32 elements
 template <>
 struct Piece<false, true> {
   typedef u32x4_t raw;
+  typedef u32x4b_t mem;
+  static constexpr bool F32 = false;
   static constexpr int V = 8;
   static __device__ __forceinline__ void open(raw v, float (&f)[V]) {
 #pragma unroll
@@ -56,6 +63,8 @@ struct Piece<false, true> {
 template <>
 struct Piece<true, true> {
   typedef u32x4_t raw;
+  typedef u32x4f_t mem;
+  static constexpr bool F32 = true;
   static constexpr int V = 4;
   static __device__ __forceinline__ void open(raw v, float (&f)[V]) {
 #pragma unroll
@@ -69,6 +78,8 @@ struct Piece<true, true> {
 template <>
 struct Piece<false, false> {
   typedef uint16_t raw;
+  typedef uint16_t mem;
+  static constexpr bool F32 = false;
   static constexpr int V = 1;
   static __device__ __forceinline__ void open(raw v, float (&f)[V]) { f[0] = bf16_to_f32(v); }
   static __device__ __forceinline__ raw close(const float (&f)[V]) {
@@ -78,6 +89,8 @@ struct Piece<false, false> {
 template <>
 struct Piece<true, false> {
   typedef uint32_t raw;
+  typedef uint32_t mem;
+  static constexpr bool F32 = true;
   static constexpr int V = 1;
   static __device__ __forceinline__ void open(raw v, float (&f)[V]) { f[0] = __uint_as_float(v); }
   static __device__ __forceinline__ raw close(const float (&f)[V]) { return __float_as_uint(f[0]); }
@@ -96,6 +109,33 @@ __device__ __forceinline__ void open_codes(u32x2_t c, float s, float (&f)[8]) {
   }
 }
 
+// Rows of d elements in ppr pieces.
+struct Shape {
+  uint32_t d, ppr, n_rows;
+  // first element of piece c of a row
+  template <int V>
+  __device__ __forceinline__ int64_t at(int64_t row, uint32_t c) const {
+    return row * d + min(c * V, d - V);
+  }
+  // elements that the piece repeats
+  template <int V>
+  __device__ __forceinline__ uint32_t repeated(uint32_t c) const {
+    return c * V - min(c * V, d - V);
+  }
+};
+template <class P>
+__device__ __forceinline__ typename P::raw load_piece(const void* p, int64_t at) {
+  typedef typename std::conditional<P::F32, uint32_t, uint16_t>::type elem;
+  return __builtin_nontemporal_load(
+      reinterpret_cast<const typename P::mem*>(reinterpret_cast<const elem*>(p) + at));
+}
+template <class P>
+__device__ __forceinline__ void store_piece(typename P::raw v, void* p, int64_t at) {
+  typedef typename std::conditional<P::F32, uint32_t, uint16_t>::type elem;
+  __builtin_nontemporal_store(
+      v, reinterpret_cast<typename P::mem*>(reinterpret_cast<elem*>(p) + at));
+}
+
 // Token and piece of a thread in a launch over all pieces of all rows.
 __device__ __forceinline__ bool piece_of(int64_t N, uint32_t ppr, int64_t& t, uint32_t& c) {
   const int64_t first = (int64_t)blockIdx.x * 256, t0 = first / ppr;
@@ -105,30 +145,30 @@ __device__ __forceinline__ bool piece_of(int64_t N, uint32_t ppr, int64_t& t, ui
   return t < N;
 }
 
+// KEPT: x are codes, with scales xs.
 template <bool F32, bool VEC, bool KEPT, int K>
 __global__ __launch_bounds__(256) void permute_kernel(
     const void* __restrict__ x, const float* __restrict__ xs, const int32_t* __restrict__ src_pos,
-    int64_t N, uint32_t ppr, uint32_t n_rows, void* __restrict__ rows) {
+    int64_t N, Shape shape, void* __restrict__ rows) {
   typedef Piece<F32, VEC> P;
-  typedef typename P::raw raw;
   int64_t t;
   uint32_t c;
-  if (!piece_of(N, ppr, t, c)) return;
-  raw v;
+  if (!piece_of(N, shape.ppr, t, c)) return;
+  uint32_t p[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) p[k] = (uint32_t)src_pos[t * K + k];
+  typename P::raw v;
   if constexpr (KEPT) {
+    const int64_t at = t * shape.ppr + c;
     float f[8];
-    open_codes(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(x) + t * ppr + c),
-               xs[(t * ppr + c) >> 4], f);
+    open_codes(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(x) + at), xs[at >> 4], f);
     v = P::close(f);
   } else {
-    v = __builtin_nontemporal_load(reinterpret_cast<const raw*>(x) + t * ppr + c);
+    v = load_piece<P>(x, shape.at<P::V>(t, c));
   }
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const uint32_t p = (uint32_t)src_pos[t * K + k];
-    if (p < n_rows)
-      __builtin_nontemporal_store(v, reinterpret_cast<raw*>(rows) + (int64_t)p * ppr + c);
-  }
+  for (int k = 0; k < K; ++k)
+    if (p[k] < shape.n_rows) store_piece<P>(v, rows, shape.at<P::V>(p[k], c));
 }
 
 // y = base + sum_k w R (w NULL: 1, base NULL: 0).  KEEP: the rows' codes too;
@@ -136,17 +176,15 @@ __global__ __launch_bounds__(256) void permute_kernel(
 template <bool F32, bool VEC, bool KEEP, int K>
 __global__ __launch_bounds__(256) void unpermute_kernel(
     const void* __restrict__ rows, const int32_t* __restrict__ src_pos,
-    const float* __restrict__ w, const void* __restrict__ base, int64_t N, uint32_t ppr,
-    uint32_t n_rows, void* __restrict__ y, u32x2_t* __restrict__ codes,
-    float* __restrict__ scales) {
+    const float* __restrict__ w, const void* __restrict__ base, int64_t N, Shape shape,
+    void* __restrict__ y, u32x2_t* __restrict__ codes, float* __restrict__ scales) {
   typedef Piece<F32, VEC> P;
-  typedef typename P::raw raw;
   int64_t t;
   uint32_t c;
-  if (!piece_of(N, ppr, t, c)) return;
+  if (!piece_of(N, shape.ppr, t, c)) return;
   uint32_t p[K];
   float s[K];
-  raw v[K];
+  typename P::raw v[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     p[k] = (uint32_t)src_pos[t * K + k];
@@ -154,18 +192,17 @@ __global__ __launch_bounds__(256) void unpermute_kernel(
   }
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (p[k] < n_rows)
-      v[k] = __builtin_nontemporal_load(reinterpret_cast<const raw*>(rows) + (int64_t)p[k] * ppr + c);
+    if (p[k] < shape.n_rows) v[k] = load_piece<P>(rows, shape.at<P::V>(p[k], c));
   float acc[P::V];
   if (base) {
-    P::open(__builtin_nontemporal_load(reinterpret_cast<const raw*>(base) + t * ppr + c), acc);
+    P::open(load_piece<P>(base, shape.at<P::V>(t, c)), acc);
   } else {
 #pragma unroll
     for (int j = 0; j < P::V; ++j) acc[j] = 0.0f;
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (p[k] >= n_rows) continue;
+    if (p[k] >= shape.n_rows) continue;
     float f[P::V];
     P::open(v[k], f);
 #pragma unroll
@@ -175,25 +212,25 @@ __global__ __launch_bounds__(256) void unpermute_kernel(
       const float top = __uint_as_float(row16_max_u32(abs_max8(u)));
       const float scale = top / kE4M3Max;
       const uint2 q = top != 0.0f ? quant8(u, scale) : make_uint2(0, 0);
-      const int64_t at = (int64_t)p[k] * ppr + c;
+      const int64_t at = (int64_t)p[k] * shape.ppr + c;
       __builtin_nontemporal_store(u32x2_t{q.x, q.y}, codes + at);
       if ((threadIdx.x & 15) == 0) scales[at >> 4] = top != 0.0f ? scale : 0.0f;
     }
   }
-  __builtin_nontemporal_store(P::close(acc), reinterpret_cast<raw*>(y) + t * ppr + c);
+  store_piece<P>(P::close(acc), y, shape.at<P::V>(t, c));
 }
 
-// A wave takes a token: its dy row once, the K rows beside it.
-template <bool F32, bool VEC, bool KEPT, int K>
+// LANES lanes take a token: its dy row once, the K rows beside it.  KEPT: the rows
+// are codes.
+template <bool F32, bool VEC, bool KEPT, int K, int LANES>
 __global__ __launch_bounds__(256) void unpermute_grad_kernel(
     const void* __restrict__ dy, const void* __restrict__ rows, const float* __restrict__ scales,
-    const int32_t* __restrict__ src_pos, const float* __restrict__ w, int64_t N, uint32_t ppr,
-    uint32_t n_rows, void* __restrict__ drows, float* __restrict__ dw) {
+    const int32_t* __restrict__ src_pos, const float* __restrict__ w, int64_t N, Shape shape,
+    void* __restrict__ drows, float* __restrict__ dw) {
   typedef Piece<F32, VEC> P;
-  typedef typename P::raw raw;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const uint32_t lane = threadIdx.x % LANES;
+  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   if (t >= N) return;
-  const int lane = lane_id();
   uint32_t p[K];
   float s[K], dot[K];
 #pragma unroll
@@ -202,37 +239,65 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(
     s[k] = w ? w[t * K + k] : 1.0f;
     dot[k] = 0.0f;
   }
-  for (uint32_t c = lane; c < ppr; c += kWave) {
+  for (uint32_t c = lane; c < shape.ppr; c += LANES) {
+    const typename P::raw gv = load_piece<P>(dy, shape.at<P::V>(t, c));
+    typename P::raw v[K];
+    u32x2_t q[K];
+    float qs[K];
+    if (dw) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (p[k] >= shape.n_rows) continue;
+        if constexpr (KEPT) {
+          const int64_t at = (int64_t)p[k] * shape.ppr + c;
+          q[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(rows) + at);
+          qs[k] = scales[at >> 4];
+        } else {
+          v[k] = load_piece<P>(rows, shape.at<P::V>(p[k], c));
+        }
+      }
+    }
     float g[P::V];
-    P::open(__builtin_nontemporal_load(reinterpret_cast<const raw*>(dy) + t * ppr + c), g);
+    P::open(gv, g);
+    const uint32_t skip = shape.repeated<P::V>(c);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (p[k] >= n_rows) continue;
-      const int64_t at = (int64_t)p[k] * ppr + c;
-      if (dw) {
-        float f[P::V];
-        if constexpr (KEPT)
-          open_codes(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(rows) + at),
-                     scales[at >> 4], f);
-        else
-          P::open(__builtin_nontemporal_load(reinterpret_cast<const raw*>(rows) + at), f);
-#pragma unroll
-        for (int j = 0; j < P::V; ++j) dot[k] = fmaf(g[j], f[j], dot[k]);
-      }
+      if (p[k] >= shape.n_rows) continue;
       if (drows) {
         float o[P::V];
 #pragma unroll
         for (int j = 0; j < P::V; ++j) o[j] = s[k] * g[j];
-        __builtin_nontemporal_store(P::close(o), reinterpret_cast<raw*>(drows) + at);
+        store_piece<P>(P::close(o), drows, shape.at<P::V>(p[k], c));
+      }
+      if (dw) {
+        float f[P::V];
+        if constexpr (KEPT) open_codes(q[k], qs[k], f);
+        else P::open(v[k], f);
+#pragma unroll
+        for (int j = 0; j < P::V; ++j)
+          if (KEPT || (uint32_t)j >= skip) dot[k] = fmaf(g[j], f[j], dot[k]);
       }
     }
   }
   if (!dw) return;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) dot[k] += __shfl_xor(dot[k], o);
-    if (lane == 0) dw[t * K + k] = dot[k];
+    for (int o = (LANES < kWave ? LANES : kWave) / 2; o > 0; o >>= 1)
+      dot[k] += __shfl_xor(dot[k], o);
+  if constexpr (LANES > kWave) {
+    static_assert(LANES == 256, "the block's four waves");
+    __shared__ float part[4][K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (lane % kWave == 0) part[lane / kWave][k] = dot[k];
+    __syncthreads();
+    if (lane < K)
+      dw[t * K + lane] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (lane == 0) dw[t * K + k] = dot[k];
   }
 }
 
@@ -248,12 +313,11 @@ hipError_t with_k(int K, F&& fn) {
   }
   return hipGetLastError();
 }
-// Rows in whole aligned 16-byte words.
-bool words(int d, bool f32, std::initializer_list<const void*> buffers) {
-  if ((int64_t)d * (f32 ? 4 : 2) % 16) return false;
-  for (const void* p : buffers)
-    if ((uintptr_t)p % 16) return false;
-  return true;
+// Pieces of a row; vec: of 16 bytes.
+Shape shape_of(int64_t N, int d, int K, bool f32, bool& vec) {
+  const int V = f32 ? 4 : 8;
+  vec = d >= V;
+  return Shape{(uint32_t)d, (uint32_t)(vec ? (d + V - 1) / V : d), (uint32_t)(N * K)};
 }
 template <class T>
 T* at(T* p, int64_t bytes) {
@@ -277,18 +341,18 @@ unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); 
 hipError_t launch_permute_rows(const void* x, const float* x_scales, const int32_t* src_pos,
                                int64_t N, int d, int K, bool f32, void* rows, hipStream_t stream) {
   const bool kept = x_scales != nullptr;
-  const bool vec = kept || words(d, f32, {x, rows});
-  const int es = f32 ? 4 : 2, ppr = vec ? d * es / 16 : d;
-  const uint32_t n_rows = (uint32_t)(N * K);
-  return token_runs(N, ppr, [&](int64_t t0, int64_t n) {
+  bool vec;
+  const Shape shape = shape_of(N, d, K, f32, vec);
+  const int es = f32 ? 4 : 2;
+  return token_runs(N, shape.ppr, [&](int64_t t0, int64_t n) {
     const void* xt = at(x, t0 * d * (kept ? 1 : es));
     const float* st = x_scales ? x_scales + t0 * (d / 128) : nullptr;
-    const dim3 grid(blocks_of(n * ppr)), block(256);
+    const dim3 grid(blocks_of(n * shape.ppr)), block(256);
     return with_k(K, [&](auto k) {
       constexpr int kk = decltype(k)::value;
       auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, stream, xt, st, src_pos + t0 * K, n,
-                           (uint32_t)ppr, n_rows, rows);
+                           shape, rows);
       };
       if (kept) go(permute_kernel<false, true, true, kk>);
       else if (f32 && vec) go(permute_kernel<true, true, false, kk>);
@@ -302,17 +366,17 @@ hipError_t launch_permute_rows(const void* x, const float* x_scales, const int32
 hipError_t launch_unpermute_rows(const void* rows, const int32_t* src_pos, const float* w,
                                  const void* base, int64_t N, int d, int K, bool f32, void* y,
                                  uint8_t* codes, float* scales, hipStream_t stream) {
-  const bool vec = codes || words(d, f32, {rows, base, y});
-  const int es = f32 ? 4 : 2, ppr = vec ? d * es / 16 : d;
-  const uint32_t n_rows = (uint32_t)(N * K);
-  return token_runs(N, ppr, [&](int64_t t0, int64_t n) {
-    const dim3 grid(blocks_of(n * ppr)), block(256);
+  bool vec;
+  const Shape shape = shape_of(N, d, K, f32, vec);
+  const int es = f32 ? 4 : 2;
+  return token_runs(N, shape.ppr, [&](int64_t t0, int64_t n) {
+    const dim3 grid(blocks_of(n * shape.ppr)), block(256);
     return with_k(K, [&](auto k) {
       constexpr int kk = decltype(k)::value;
       auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, stream, rows, src_pos + t0 * K,
-                           w ? w + t0 * K : nullptr, at(base, t0 * d * es), n, (uint32_t)ppr,
-                           n_rows, at(y, t0 * d * es), reinterpret_cast<u32x2_t*>(codes), scales);
+                           w ? w + t0 * K : nullptr, at(base, t0 * d * es), n, shape,
+                           at(y, t0 * d * es), reinterpret_cast<u32x2_t*>(codes), scales);
       };
       if (codes) go(unpermute_kernel<false, true, true, kk>);
       else if (f32 && vec) go(unpermute_kernel<true, true, false, kk>);
@@ -327,23 +391,30 @@ hipError_t launch_unpermute_grad(const void* dy, const void* rows, const float* 
                                  const int32_t* src_pos, const float* w, int64_t N, int d, int K,
                                  bool f32, void* drows, float* dw, hipStream_t stream) {
   const bool kept = row_scales != nullptr;
-  const bool vec = kept || words(d, f32, {dy, rows, drows});
-  const int es = f32 ? 4 : 2, ppr = vec ? d * es / 16 : d;
-  const uint32_t n_rows = (uint32_t)(N * K);
-  return token_runs(N, 64, [&](int64_t t0, int64_t n) {
-    const dim3 grid(blocks_of(n * 64)), block(256);
+  bool vec;
+  const Shape shape = shape_of(N, d, K, f32, vec);
+  const int es = f32 ? 4 : 2;
+  const int lanes = shape.ppr > 128 ? 256 : shape.ppr > 24 ? 64 : 16;
+  return token_runs(N, lanes, [&](int64_t t0, int64_t n) {
+    const dim3 grid(blocks_of(n * lanes)), block(256);
     return with_k(K, [&](auto k) {
       constexpr int kk = decltype(k)::value;
       auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, stream, at(dy, t0 * d * es), rows, row_scales,
-                           src_pos + t0 * K, w ? w + t0 * K : nullptr, n, (uint32_t)ppr, n_rows,
+                           src_pos + t0 * K, w ? w + t0 * K : nullptr, n, shape,
                            drows, dw ? dw + t0 * K : nullptr);
       };
-      if (kept) go(unpermute_grad_kernel<false, true, true, kk>);
-      else if (f32 && vec) go(unpermute_grad_kernel<true, true, false, kk>);
-      else if (f32) go(unpermute_grad_kernel<true, false, false, kk>);
-      else if (vec) go(unpermute_grad_kernel<false, true, false, kk>);
-      else go(unpermute_grad_kernel<false, false, false, kk>);
+      auto pick = [&](auto l) {
+        constexpr int W = decltype(l)::value;
+        if (kept) go(unpermute_grad_kernel<false, true, true, kk, W>);
+        else if (f32 && vec) go(unpermute_grad_kernel<true, true, false, kk, W>);
+        else if (f32) go(unpermute_grad_kernel<true, false, false, kk, W>);
+        else if (vec) go(unpermute_grad_kernel<false, true, false, kk, W>);
+        else go(unpermute_grad_kernel<false, false, false, kk, W>);
+      };
+      if (lanes == 256) pick(std::integral_constant<int, 256>{});
+      else if (lanes == 64) pick(std::integral_constant<int, 64>{});
+      else pick(std::integral_constant<int, 16>{});
     });
   });
 }

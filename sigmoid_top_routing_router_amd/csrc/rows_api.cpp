@@ -47,7 +47,7 @@ extern "C" {
 
 size_t moe_group_workspace_bytes(int64_t N, int32_t E, int32_t K) {
   if (!group_sizes_ok(N, E, K)) return 0;
-  return up((size_t)moe::perm_count_rows(N * K) * (size_t)(E + 1) * 4 + 4);
+  return up(moe::group_work_words(N * K, E) * 4 + 4);
 }
 
 moe_status_t moe_group(const int32_t* topk_ids, int64_t N, int32_t E, int32_t K, int32_t* counts,

@@ -64,9 +64,9 @@ def choice(rng, N, E, K, away):
 GROUPS = [  # N, E, K, away
     (0, 3, 2, "none"), (1, 1, 1, "none"), (1, 384, 6, "none"), (1, 2, 8, "some"),
     (64, 384, 6, "none"), (37, 5, 3, "some"), (50, 7, 2, "all"), (300, 384, 8, "one"),
-    (2730, 384, 6, "some"),      # 16380 pairs: the last size of the one-block form
-    (2731, 384, 6, "none"),      # 16386 pairs
-    (4097, 128, 8, "some"), (70001, 384, 1, "some"), (33000, 2, 4, "all"),
+    (1365, 384, 6, "some"),      # 8190 pairs: the last size of the one-block form
+    (1366, 384, 6, "none"),      # 8196 pairs
+    (2731, 384, 6, "some"), (4097, 128, 8, "some"), (65537, 384, 8, "some"), (70001, 384, 1, "some"), (33000, 2, 4, "all"),
 ]
 
 
@@ -112,6 +112,13 @@ ROWS = [  # N, d, E, K, type, away, offset
     (17, 128, 9, 4, "f32", "all", 0),
     (260, 516, 11, 8, "f32", "some", 1),
     (4100, 72, 20, 3, "bf16", "some", 0),
+    # about one piece of eight (four) elements, and a piece more than a block's
+    (19, 7, 4, 2, "bf16", "some", 0), (19, 8, 4, 2, "bf16", "some", 1),
+    (19, 9, 4, 2, "bf16", "none", 0), (19, 15, 4, 3, "bf16", "some", 0),
+    (19, 3, 4, 2, "f32", "some", 0), (19, 4, 4, 2, "f32", "none", 1),
+    (19, 5, 4, 6, "f32", "some", 0), (19, 7, 4, 8, "f32", "some", 0),
+    (11, 1025, 4, 2, "bf16", "some", 0), (11, 1023, 4, 2, "f32", "some", 1),
+    (11, 2049, 4, 2, "bf16", "some", 0), (11, 8191, 4, 3, "f32", "some", 0),
 ]
 
 
@@ -277,11 +284,12 @@ def test_gradients_against_differences(M):
             assert abs(num - f64(dw)[t, k]) <= tol, (t, k)
 
 
-def test_infinities_and_nan_stay_where_they_are(M):
+@pytest.mark.parametrize("width", [256, 11, 261, 5])
+def test_infinities_and_nan_stay_where_they_are(M, width):
     """A NaN or infinity in a row reaches its own token only, also with a weight
     of zero next to it; rows without a pair reach none."""
     import torch
-    N, d, E, K = 6, 256, 3, 2
+    N, d, E, K = 6, width, 3, 2
     ids = torch.tensor([[0, 1], [1, 2], [-1, 0], [2, 2], [-1, -1], [1, 0]], dtype=torch.int32).cuda()
     g = M.group_tokens(ids, E)
     pos = host(g.src_pos)
@@ -301,6 +309,8 @@ def test_infinities_and_nan_stay_where_they_are(M):
         assert np.isnan(dw[1, 0]) and np.isinf(dw[3, 1])
         dw[1, 0] = dw[3, 1] = 0
         assert np.all(np.isfinite(dw)) and np.all(dw[4] == 0)
+    if d != 256:
+        return
     rows = torch.ones(N * K, d, dtype=torch.bfloat16, device="cuda")
     rows[int(pos[1, 0]), 3] = float("nan")
     rows[int(pos[3, 1]), 200] = float("-inf")
