@@ -68,7 +68,7 @@ __device__ __forceinline__ void place_wave(uint32_t e, bool ok, int E, int64_t p
 __device__ __forceinline__ uint32_t bucket_start(const uint32_t* tot, int B, uint32_t* wave_sum) {
   const int tid = threadIdx.x, w = tid >> 6;
   const uint32_t c = tid < B ? tot[tid] : 0u;
-  const uint32_t incl = wave_inclusive_sum_u32(c);
+  const uint32_t incl = wave_inclusive_sum_dpp_u32(c);
   if (lane_id() == kWave - 1) wave_sum[w] = incl;
   __syncthreads();
   uint32_t before = 0;

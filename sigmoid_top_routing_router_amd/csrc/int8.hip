@@ -48,39 +48,63 @@ __device__ __forceinline__ uint32_t int8x4(const float (&v)[4], float s, float y
   return c;
 }
 
-// A wave takes a row.  A row with an infinity or NaN has the scale NaN and
-// integers 0.
+// LANES lanes take a row of up to WORDS 16-byte words each, which stay in registers
+// between the maximum and the integers; WORDS 0: rows longer than that, read twice.
+// A row with an infinity or NaN has the scale NaN and integers 0.
+template <int LANES, int WORDS>
 __global__ __launch_bounds__(256) void quant_int8_kernel(const u32x4_t* __restrict__ X, int64_t n,
                                                          int words, u32x2_t* __restrict__ Q,
                                                          float* __restrict__ S) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x % LANES;
+  const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   if (row >= n) return;
-  const int lane = lane_id();
   const u32x4_t* x = X + row * words;
+  constexpr int kHeld = WORDS > 0 ? WORDS : 1;
+  u32x4_t v[kHeld];
   uint32_t m = 0;
-  for (int c = lane; c < words; c += kWave) {
-    const u32x4_t v = x[c];
-    m = max(m, abs_max8(make_uint4(v[0], v[1], v[2], v[3])));
+  auto top = [&](u32x4_t w) { m = max(m, abs_max8(make_uint4(w[0], w[1], w[2], w[3]))); };
+  if constexpr (WORDS > 0) {
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j)
+      v[j] = j * LANES + lane < words ? __builtin_nontemporal_load(x + j * LANES + lane)
+                                      : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) top(v[j]);
+  } else {
+    for (int c = lane; c < words; c += LANES) top(x[c]);
   }
   m = wave_max_u32(m);
+  if constexpr (LANES > kWave) {
+    static_assert(LANES == 256, "the block's four waves");
+    __shared__ uint32_t part[4];
+    if (lane % kWave == 0) part[lane / kWave] = m;
+    __syncthreads();
+    m = max(max(part[0], part[1]), max(part[2], part[3]));
+  }
   const float amax = __uint_as_float(m);
   const bool finite = m < 0x7F800000u, zero = m == 0u;
   const float s = amax / kInt8Max, inv = 1.0f / s;
   const bool divide = amax < 0x1p-60f;
-  for (int c = lane; c < words; c += kWave) {
-    const u32x4_t v = x[c];
+  auto store = [&](u32x4_t w, int c) {
     u32x2_t q = {0u, 0u};
     if (finite && !zero) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float f[4] = {__uint_as_float(v[2 * i] << 16),
-                            __uint_as_float(v[2 * i] & 0xFFFF0000u),
-                            __uint_as_float(v[2 * i + 1] << 16),
-                            __uint_as_float(v[2 * i + 1] & 0xFFFF0000u)};
+        const float f[4] = {__uint_as_float(w[2 * i] << 16),
+                            __uint_as_float(w[2 * i] & 0xFFFF0000u),
+                            __uint_as_float(w[2 * i + 1] << 16),
+                            __uint_as_float(w[2 * i + 1] & 0xFFFF0000u)};
         q[i] = int8x4(f, s, inv, divide);
       }
     }
     Q[row * words + c] = q;
+  };
+  if constexpr (WORDS > 0) {
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j)
+      if (j * LANES + lane < words) store(v[j], j * LANES + lane);
+  } else {
+    for (int c = lane; c < words; c += LANES) store(x[c], c);
   }
   if (lane == 0) S[row] = finite ? s : __uint_as_float(0x7FC00000u);
 }
@@ -688,12 +712,22 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
 
 hipError_t launch_quant_int8(const uint16_t* X, int64_t n, int cols, int8_t* Q, float* S,
                              hipStream_t stream) {
-  const int64_t most = int64_t(1) << 24;  // rows a launch: fewer than 2^32 threads
+  const int words = cols / 8;
+  const int lanes = words <= 6 * 64 ? 64 : 256;
+  const int64_t most = int64_t(1) << 23;  // rows a launch: fewer than 2^32 threads
   for (int64_t r0 = 0; r0 < n; r0 += most) {
     const int64_t m = std::min(most, n - r0);
-    hipLaunchKernelGGL(quant_int8_kernel, dim3((unsigned)((m + 3) / 4)), dim3(256), 0, stream,
-                       reinterpret_cast<const u32x4_t*>(X + r0 * cols), m, cols / 8,
-                       reinterpret_cast<u32x2_t*>(Q + r0 * cols), S + r0);
+    const dim3 grid((unsigned)((m * lanes + 255) / 256)), block(256);
+    const u32x4_t* x = reinterpret_cast<const u32x4_t*>(X + r0 * cols);
+    u32x2_t* q = reinterpret_cast<u32x2_t*>(Q + r0 * cols);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, stream, x, m, words, q, S + r0);
+    };
+    if (words <= 2 * 64) go(quant_int8_kernel<64, 2>);
+    else if (words <= 6 * 64) go(quant_int8_kernel<64, 6>);
+    else if (words <= 4 * 256) go(quant_int8_kernel<256, 4>);
+    else if (words <= 8 * 256) go(quant_int8_kernel<256, 8>);
+    else go(quant_int8_kernel<256, 0>);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -39,7 +39,8 @@ def bf16(a):
 
 
 @pytest.mark.parametrize("n,cols", [(1, 16), (3, 48), (64, 2560), (1, 65536), (130, 8192),
-                                    (257, 8208), (5, 512), (1000, 1040)])
+                                    (257, 8208), (5, 512), (1000, 1040), (7, 1024), (9, 3056),
+                                    (6, 3088), (3, 16384), (3, 16400)])
 def test_quantize_rows(M, n, cols):
     say("quantize", n, cols)
     rng = np.random.default_rng(n + cols)
