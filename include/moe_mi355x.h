@@ -700,9 +700,10 @@ moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const 
  * that are exact), dense or over the sorted rows of the experts.
  *
  * moe_int8_quantize_rows - bf16 rows x [n,cols] -> integers codes [n,cols] and
- * scales [n]: s = fp32(amax) / 127, code = x / s rounded to nearest even, in
- * [-127, 127]; a row of zeros has s = 0 and zeros.  A row with an infinity or
- * a NaN has the scale NaN and zeros.  Weights [E,cols,k] are quantised as
+ * scales [n]: s = amax * (1 / 127), the reciprocal and the product rounded to
+ * fp32, code = x / s rounded to nearest even, in [-127, 127]; a row of zeros
+ * has s = 0 and zeros.  A row with an infinity or a NaN has the scale NaN and
+ * zeros.  Weights [E,cols,k] are quantised as
  * E*cols rows of k: a scale for each output channel.  n >= 0, cols % 16 == 0
  * (16 <= cols <= 65536); x and codes 16-byte aligned.
  *
@@ -721,7 +722,8 @@ moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const 
  *  out          [rows,cols] bf16 bits.
  * 0 <= rows <= 2^27, a_rows likewise; 1 <= E <= 384; k % 16 == 0 (16 <= k <=
  * 65536); cols % 8 == 0 (8 <= cols <= 65536); 1 <= K <= 8; with sorted_src
- * a_rows*k at most 4 GiB - 512 KiB.  a, w, w_up and out 16-byte aligned, the others 4-byte.  The output shares memory with no input.
+ * a_rows*k at most 4 GiB - 512 KiB.  a, w, w_up and out 16-byte aligned, the
+ * others 4-byte.  The output shares memory with no input.
  * The first call on a device sets the kernels' LDS attributes: make one
  * uncaptured call before capturing.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED_SHAPE, HIP.

@@ -62,11 +62,11 @@ def unpermute_backward(dy, pos, weights, rows, out):
 
 
 def int8_quantize(x):
-    """Integers and scales of the rows of x (bf16 values in fp64): s = fp32(amax) /
-    127 and x / s, each rounded to fp32, the latter then to the nearest integer,
+    """Integers and scales of the rows of x (bf16 values in fp64): s = amax times
+    1 / 127 and x / s, each rounded to fp32, the latter then to the nearest integer,
     halves to even."""
     x = np.asarray(x, np.float64).astype(np.float32)
-    s = np.abs(x).max(axis=-1) / np.float32(127.0)
+    s = np.abs(x).max(axis=-1) * (np.float32(1.0) / np.float32(127.0))
     live = (s > 0)[..., None]
     q = np.where(live, np.rint(x / np.where(live, s[..., None], np.float32(1.0))), 0.0)
     return np.clip(q, -127, 127).astype(np.int8), s

@@ -1,8 +1,9 @@
 // Products in 8-bit integers with a scale for each row (token) and each output
 // channel, dense or grouped by expert, and the row quantiser.
 //
-// A row x becomes s = amax|x| / 127 and the integers q = rne(x / s) in [-127,
-// 127]; weights the same way, a row of W being an output channel.  Then
+// A row x becomes s = amax|x| (1 / 127), the reciprocal and the product rounded to
+// fp32, and the integers q = rne(x / s) in [-127, 127]; weights the same way, a row
+// of W being an output channel.  Then
 //   y_tc = s_t s_c sum_k q_tk q_ck,
 // the sum exact in 32-bit integers (|sum| <= 2^14 k < 2^31 for k <= 65536; the
 // code -128 of a caller's own included), converted to fp32 (one rounding of
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const u32x4_t* __restri
   }
   const float amax = __uint_as_float(m);
   const bool finite = m < 0x7F800000u, zero = m == 0u;
-  const float s = amax / kInt8Max, inv = 1.0f / s;
+  const float s = amax * (1.0f / kInt8Max), inv = 1.0f / s;
   const bool divide = amax < 0x1p-60f;
   auto store = [&](u32x4_t w, int c) {
     u32x2_t q = {0u, 0u};

@@ -76,7 +76,7 @@ def test_corrected_product_gives_the_quotients_integer():
         top = float(sig) / 128.0
         x = bf16_values(top)
         x = x[x > top / 1024.0].astype(np.float32)
-        s = np.float32(top) / np.float32(127.0)
+        s = np.float32(top) * (np.float32(1.0) / np.float32(127.0))
         y = np.float32(1.0) / s
         q = x * y
         r = (x.astype(np.float64) - s.astype(np.float64) * q.astype(np.float64)).astype(np.float32)
