@@ -152,16 +152,19 @@ struct Segments {
   __device__ __forceinline__ void read(const Int8Args& a, uint32_t bm) {
     const int lane = lane_id();
     total = 0;
+    int32_t first[kGroups], end[kGroups];  // all loads in flight at once
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const int e = 64 * g + lane;
-      lo[g] = n[g] = 0;
-      if (e < a.E) {
-        const int64_t l = min(max((int64_t)a.offsets[e], (int64_t)0), a.rows);
-        const int64_t h = min(max((int64_t)a.offsets[e + 1], l), a.rows);
-        lo[g] = (uint32_t)l;
-        n[g] = (uint32_t)(h - l);
-      }
+      const int e = min(64 * g + lane, a.E - 1);
+      first[g] = a.offsets[e];
+      end[g] = a.offsets[e + 1];
+    }
+    const int rows = (int)a.rows;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int l = min(max(first[g], 0), rows), h = min(max(end[g], l), rows);
+      lo[g] = (uint32_t)l;
+      n[g] = 64 * g + lane < a.E ? (uint32_t)(h - l) : 0u;
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -272,6 +275,20 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
   const int wg = wave >> 2, wp = wave & 3;
   const int nk = (a.k + kStage - 1) / kStage;
 
+  // Wave (wg, wp): the first or second half of the tile's 32-row blocks, and
+  // weight rows 64 wp .. + 63, or with UP 32 wp of w and of w_up.
+  const int b_row[2] = {UP ? 32 * wp : 64 * wp, UP ? kCols / 2 + 32 * wp : 64 * wp + 32};
+  const int fr = lane & 31;
+  const int b_quarter[2] = {b_row[0] >> 6, b_row[1] >> 6};
+  const int b_base[2] = {((b_row[0] & 63) + fr) * kStage, ((b_row[1] & 63) + fr) * kStage};
+  // the first 32-row block of the wave's half, and how many it has
+  auto first_of = [&](const Tile& t) { return wg ? ((t.rows + 31) / 32 + 1) / 2 : 0; };
+  auto live_of = [&](const Tile& t, int n) {
+    const int blocks = (t.rows + 31) / 32, half = (blocks + 1) / 2;
+    return __builtin_amdgcn_readfirstlane((UP ? 32 * wp : 64 * wp) < n ? (wg ? blocks - half : half)
+                                                                       : 0);
+  };
+
   // Loads: a wave brings MB times 8 rows of A and 4 times 8 rows of B a stage,
   // 128 bytes a row; load i covers rows 8 (8 i + wave) .. + 7 of the tile.
   // Lane l fills slot l & 7 of row l >> 3 with the row's chunk (l & 7) ^ ((row >> 1)
@@ -279,20 +296,32 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
   const int sub = lane >> 3;
   const int chunk = (lane & 7) ^ ((4 * wave + (sub >> 1)) & 7);
   const bool k_in = (nk - 1) * kStage + chunk * 16 < a.k;  // this lane's chunk of the last stage
-  uint32_t a_off[MB], a_next[MB], b_off;
+  uint32_t a_off[MB], a_pair[MB], r_pair[MB], b_off;
   Buffer ra, rw, ru;
   Tile tile;
   int col0, cols;
-  // the tile's rows of A
-  auto rows_of = [&](int i) {
-    int nt;
-    const Tile t = list.tile(i, nt);
+  // The pairs of the rows of A that the wave loads (a_pair) and of those whose
+  // results it holds (r_pair), all loads at once and none waited for here; a row
+  // past the tile gives its last one's.
+  auto pairs_of = [&](const Tile& t, auto row, uint32_t(&pair)[MB]) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
-      const int r = 8 * (8 * j + wave) + sub;
-      a_next[j] = kNoRow;
-      if (r < t.rows) a_next[j] = a.sorted_src ? (uint32_t)a_row_of(a, t.row0 + r) : (uint32_t)r;
+      const int r = min(row(j), t.rows - 1);
+      pair[j] = a.sorted_src ? (uint32_t)a.sorted_src[t.row0 + r] : (uint32_t)r;
     }
+  };
+  auto a_pairs = [&](int i) {
+    int nt;
+    pairs_of(list.tile(i, nt), [&](int j) { return 8 * (8 * j + wave) + sub; }, a_pair);
+  };
+  auto r_pairs = [&](int i) {
+    int nt;
+    const Tile t = list.tile(i, nt);
+    pairs_of(t, [&](int m) { return 32 * (first_of(t) + m) + fr; }, r_pair);
+  };
+  // the row of A of a pair, or of the tile's row
+  auto a_row = [&](uint32_t pair) {
+    return a.sorted_src ? min(max((int)pair, 0) / (uint32_t)a.K, (uint32_t)a.a_rows - 1u) : pair;
   };
   auto open = [&](int i) {
     int nt;
@@ -301,7 +330,9 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
     cols = min(OC, a.cols - col0);
 #pragma unroll
     for (int j = 0; j < MB; ++j)
-      a_off[j] = a_next[j] == kNoRow ? kNoRow : a_next[j] * (uint32_t)a.k + (uint32_t)chunk * 16u;
+      a_off[j] = 8 * (8 * j + wave) + sub < tile.rows
+                     ? a_row(a_pair[j]) * (uint32_t)a.k + (uint32_t)chunk * 16u
+                     : kNoRow;
     b_off = (uint32_t)(8 * wave + sub) * (uint32_t)a.k + (uint32_t)chunk * 16u;
     const int64_t w_row = (int64_t)tile.expert * a.cols + col0;
     const uint32_t w_bytes = (uint32_t)cols * (uint32_t)a.k;
@@ -325,49 +356,47 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
   auto place = [&](int q) { return q >= S::quarters ? q - S::quarters : q; };
   // a tile's first stages: A's two slots, B's three stages
   auto load_first = [&] {
+    // stage by stage, as the waits count them
+    auto in_order = [] {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+    };
 #pragma unroll
     for (int i = 0; i < MB; ++i) load_a(0, 0, i);
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_b(0, i, i);
+    in_order();
     if (nk > 1) {
 #pragma unroll
       for (int i = 0; i < MB; ++i) load_a(1, 1, i);
 #pragma unroll
       for (int i = 0; i < 4; ++i) load_b(1, 4 + i, i);
     }
+    in_order();
     if (nk > 2) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) load_b(2, 8 + i, i);
     }
+    in_order();
   };
 
-  // Wave (wg, wp): the first or second half of the tile's 32-row blocks, and
-  // weight rows 64 wp .. + 63, or with UP 32 wp of w and of w_up.
-  const int b_row[2] = {UP ? 32 * wp : 64 * wp, UP ? kCols / 2 + 32 * wp : 64 * wp + 32};
-  const int fr = lane & 31;
-  const int b_quarter[2] = {b_row[0] >> 6, b_row[1] >> 6};
-  const int b_base[2] = {((b_row[0] & 63) + fr) * kStage, ((b_row[1] & 63) + fr) * kStage};
   const int slot0 = ((lane >> 5) ^ ((lane >> 1) & 7)) * 16;  // of step s: ^ 32 s
 
-  rows_of(0);
+  a_pairs(0);
+  r_pairs(0);
   open(0);
   load_first();
   for (int it = 0; it < list.count; ++it) {
     const Tile now = tile;
     const int now_col0 = col0, now_cols = cols;
-    const int blocks = (now.rows + 31) / 32, half = (blocks + 1) / 2;
-    const int first = wg ? half : 0;
-    const int live = __builtin_amdgcn_readfirstlane(
-        (UP ? 32 * wp : 64 * wp) < now_cols ? (wg ? blocks - half : half) : 0);
+    const int first = first_of(now), live = live_of(now, now_cols);
     const int a_base = (32 * first + fr) * kStage;
-    // the rows' scales, and the next tile's rows
+    // the rows' scales, and the next tile's pairs
     float sr[MB];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int r = 32 * (first + m) + fr;
-      sr[m] = m < live && r < now.rows ? a.a_scales[a_row_of(a, now.row0 + r)] : 0.0f;
-    }
-    if (it + 1 < list.count) rows_of(it + 1);
+    for (int m = 0; m < MB; ++m)
+      sr[m] = a.a_scales[a.sorted_src ? (int64_t)a_row(r_pair[m]) : now.row0 + r_pair[m]];
+    if (it + 1 < list.count) a_pairs(it + 1);
 
     i32x16_t acc[MB][2];
 #pragma unroll
@@ -482,6 +511,7 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
                            (int)((uint32_t)((UP ? 32 * wp : b_row[f]) + 8 * q + 4 * (me >> 5)) * 4u), 0, 0));
     }
     if (it + 1 < list.count) {
+      r_pairs(it + 1);
       // all waves have read their last fragments before LDS is filled again
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       block_barrier();
@@ -736,12 +766,35 @@ hipError_t launch_quant_int8(const uint16_t* X, int64_t n, int cols, int8_t* Q, 
 }
 
 namespace {
-// Both launches' kernels use all of a CU's LDS.
-template <class Kernel, class... Args>
-hipError_t launch_tiles(Kernel kernel, int lds, std::atomic<uint32_t>& configured, int64_t blocks,
-                        hipStream_t stream, Args... args) {
-  const hipError_t e = set_lds_limit_once((const void*)kernel, lds, configured);
+template <int MB>
+hipError_t allow_lds() {
+  const void* kernels[] = {
+      (const void*)int8_grouped_kernel<MB, true>, (const void*)int8_grouped_kernel<MB, false>,
+      (const void*)int8_dense_kernel<MB, true>, (const void*)int8_dense_kernel<MB, false>};
+  static std::atomic<uint32_t> done[4];
+  for (int i = 0; i < 4; ++i) {
+    const hipError_t e = set_lds_limit_once(kernels[i], TileShape<MB>::lds, done[i]);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+// The LDS of every tile kernel, on a device's first call: another size's call, which
+// may be a captured one, finds its kernel ready.
+hipError_t allow_lds_once() {
+  static std::atomic<uint32_t> all{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
+  const uint32_t bit = dev >= 0 && dev < 32 ? 1u << dev : 0u;
+  if (bit && (all.load(std::memory_order_acquire) & bit)) return hipSuccess;
+  if ((e = allow_lds<1>()) != hipSuccess || (e = allow_lds<2>()) != hipSuccess ||
+      (e = allow_lds<3>()) != hipSuccess || (e = allow_lds<4>()) != hipSuccess)
+    return e;
+  all.fetch_or(bit, std::memory_order_release);
+  return hipSuccess;
+}
+template <class Kernel, class... Args>
+hipError_t launch_tiles(Kernel kernel, int lds, int64_t blocks, hipStream_t stream, Args... args) {
   if (blocks >= (int64_t(1) << 23)) return hipErrorInvalidConfiguration;  // 2^32 threads
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(512), lds, stream, args...);
   return hipGetLastError();
@@ -782,30 +835,25 @@ int column_tiles(const Int8Args& a) {
 }
 template <int MB>
 hipError_t launch_grouped(const Int8Args& a, hipStream_t stream) {
-  static std::atomic<uint32_t> configured[2];
   const int col_tiles = column_tiles(a);
   const int64_t blocks = tile_blocks(most_tiles(a, TileShape<MB>::rows) * col_tiles);
-  if (a.w_up)
-    return launch_tiles(int8_grouped_kernel<MB, true>, TileShape<MB>::lds, configured[0], blocks,
-                        stream, a, (uint32_t)col_tiles);
-  return launch_tiles(int8_grouped_kernel<MB, false>, TileShape<MB>::lds, configured[1], blocks,
-                      stream, a, (uint32_t)col_tiles);
+  auto go = [&](auto kernel) {
+    return launch_tiles(kernel, TileShape<MB>::lds, blocks, stream, a, (uint32_t)col_tiles);
+  };
+  return a.w_up ? go(int8_grouped_kernel<MB, true>) : go(int8_grouped_kernel<MB, false>);
 }
 template <int MB>
 hipError_t launch_dense(const Int8Args& a, hipStream_t stream) {
-  static std::atomic<uint32_t> configured[2];
   const int col_tiles = column_tiles(a);
   const int64_t m_tiles = most_tiles(a, TileShape<MB>::rows);
   const int64_t blocks = tile_blocks(m_tiles * col_tiles);
-  if (a.w_up)
-    return launch_tiles(int8_dense_kernel<MB, true>, TileShape<MB>::lds, configured[0], blocks,
-                        stream, a, (uint32_t)m_tiles, (uint32_t)col_tiles);
-  return launch_tiles(int8_dense_kernel<MB, false>, TileShape<MB>::lds, configured[1], blocks,
-                      stream, a, (uint32_t)m_tiles, (uint32_t)col_tiles);
+  auto go = [&](auto kernel) {
+    return launch_tiles(kernel, TileShape<MB>::lds, blocks, stream, a, (uint32_t)m_tiles,
+                        (uint32_t)col_tiles);
+  };
+  return a.w_up ? go(int8_dense_kernel<MB, true>) : go(int8_dense_kernel<MB, false>);
 }
-}  // namespace
 
-namespace {
 // Tiles of bm rows that are expected: every expert with rows has its share of
 // them, and half a tile more where that share is over half a tile.
 double expected_tiles(const Int8Args& a, int bm) {
@@ -855,6 +903,8 @@ hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream) {
       {few_cost(a, 2, 2), launch_few<2, 2>},
       {few_cost(a, 4, 2), launch_few<4, 2>},
   };
+  const hipError_t e = allow_lds_once();
+  if (e != hipSuccess) return e;
   const Form* best = forms;
   for (const Form& f : forms)
     if (f.cost < best->cost) best = &f;
