@@ -67,8 +67,7 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const u32x4_t* __restri
   if constexpr (WORDS > 0) {
 #pragma unroll
     for (int j = 0; j < WORDS; ++j)
-      v[j] = j * LANES + lane < words ? __builtin_nontemporal_load(x + j * LANES + lane)
-                                      : u32x4_t{0u, 0u, 0u, 0u};
+      v[j] = j * LANES + lane < words ? x[j * LANES + lane] : u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < WORDS; ++j) top(v[j]);
   } else {

@@ -123,17 +123,24 @@ struct Shape {
     return c * V - min(c * V, d - V);
   }
 };
-template <class P>
+// Of the tokens' rows, which the call before often left in the memory-side cache
+// and the K pairs' blocks share; NT: of the grouped rows, read once (16384 tokens of
+// 2560 bf16, six each: permute 98 us with the former so, 115 with non-temporal loads;
+// the sum of grouped rows 99 with the latter so, 106 without).
+template <class P, bool NT>
 __device__ __forceinline__ typename P::raw load_piece(const void* p, int64_t at) {
   typedef typename std::conditional<P::F32, uint32_t, uint16_t>::type elem;
-  return __builtin_nontemporal_load(
-      reinterpret_cast<const typename P::mem*>(reinterpret_cast<const elem*>(p) + at));
+  const typename P::mem* from =
+      reinterpret_cast<const typename P::mem*>(reinterpret_cast<const elem*>(p) + at);
+  if constexpr (NT) return __builtin_nontemporal_load(from);
+  else return *from;
 }
-template <class P>
+template <class P, bool NT>
 __device__ __forceinline__ void store_piece(typename P::raw v, void* p, int64_t at) {
   typedef typename std::conditional<P::F32, uint32_t, uint16_t>::type elem;
-  __builtin_nontemporal_store(
-      v, reinterpret_cast<typename P::mem*>(reinterpret_cast<elem*>(p) + at));
+  typename P::mem* to = reinterpret_cast<typename P::mem*>(reinterpret_cast<elem*>(p) + at);
+  if constexpr (NT) __builtin_nontemporal_store(v, to);
+  else *to = v;
 }
 
 // Token and piece of a thread in a launch over all pieces of all rows.
@@ -161,14 +168,14 @@ __global__ __launch_bounds__(256) void permute_kernel(
   if constexpr (KEPT) {
     const int64_t at = t * shape.ppr + c;
     float f[8];
-    open_codes(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(x) + at), xs[at >> 4], f);
+    open_codes(reinterpret_cast<const u32x2_t*>(x)[at], xs[at >> 4], f);
     v = P::close(f);
   } else {
-    v = load_piece<P>(x, shape.at<P::V>(t, c));
+    v = load_piece<P, false>(x, shape.at<P::V>(t, c));
   }
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (p[k] < shape.n_rows) store_piece<P>(v, rows, shape.at<P::V>(p[k], c));
+    if (p[k] < shape.n_rows) store_piece<P, true>(v, rows, shape.at<P::V>(p[k], c));
 }
 
 // y = base + sum_k w R (w NULL: 1, base NULL: 0).  KEEP: the rows' codes too;
@@ -192,10 +199,10 @@ __global__ __launch_bounds__(256) void unpermute_kernel(
   }
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (p[k] < shape.n_rows) v[k] = load_piece<P>(rows, shape.at<P::V>(p[k], c));
+    if (p[k] < shape.n_rows) v[k] = load_piece<P, true>(rows, shape.at<P::V>(p[k], c));
   float acc[P::V];
   if (base) {
-    P::open(load_piece<P>(base, shape.at<P::V>(t, c)), acc);
+    P::open(load_piece<P, false>(base, shape.at<P::V>(t, c)), acc);
   } else {
 #pragma unroll
     for (int j = 0; j < P::V; ++j) acc[j] = 0.0f;
@@ -217,7 +224,7 @@ __global__ __launch_bounds__(256) void unpermute_kernel(
       if ((threadIdx.x & 15) == 0) scales[at >> 4] = top != 0.0f ? scale : 0.0f;
     }
   }
-  store_piece<P>(P::close(acc), y, shape.at<P::V>(t, c));
+  store_piece<P, false>(P::close(acc), y, shape.at<P::V>(t, c));
 }
 
 // LANES lanes take a token: its dy row once, the K rows beside it.  KEPT: the rows
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(
     dot[k] = 0.0f;
   }
   for (uint32_t c = lane; c < shape.ppr; c += LANES) {
-    const typename P::raw gv = load_piece<P>(dy, shape.at<P::V>(t, c));
+    const typename P::raw gv = load_piece<P, false>(dy, shape.at<P::V>(t, c));
     typename P::raw v[K];
     u32x2_t q[K];
     float qs[K];
@@ -253,7 +260,7 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(
           q[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(rows) + at);
           qs[k] = scales[at >> 4];
         } else {
-          v[k] = load_piece<P>(rows, shape.at<P::V>(p[k], c));
+          v[k] = load_piece<P, true>(rows, shape.at<P::V>(p[k], c));
         }
       }
     }
@@ -267,7 +274,7 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(
         float o[P::V];
 #pragma unroll
         for (int j = 0; j < P::V; ++j) o[j] = s[k] * g[j];
-        store_piece<P>(P::close(o), drows, shape.at<P::V>(p[k], c));
+        store_piece<P, true>(P::close(o), drows, shape.at<P::V>(p[k], c));
       }
       if (dw) {
         float f[P::V];
@@ -394,7 +401,7 @@ hipError_t launch_unpermute_grad(const void* dy, const void* rows, const float* 
   bool vec;
   const Shape shape = shape_of(N, d, K, f32, vec);
   const int es = f32 ? 4 : 2;
-  const int lanes = shape.ppr > 128 ? 256 : shape.ppr > 24 ? 64 : 16;
+  const int lanes = shape.ppr > 128 ? 256 : shape.ppr > 32 ? 64 : shape.ppr > 16 ? 32 : 16;
   return token_runs(N, lanes, [&](int64_t t0, int64_t n) {
     const dim3 grid(blocks_of(n * lanes)), block(256);
     return with_k(K, [&](auto k) {
@@ -414,6 +421,7 @@ hipError_t launch_unpermute_grad(const void* dy, const void* rows, const float* 
       };
       if (lanes == 256) pick(std::integral_constant<int, 256>{});
       else if (lanes == 64) pick(std::integral_constant<int, 64>{});
+      else if (lanes == 32) pick(std::integral_constant<int, 32>{});
       else pick(std::integral_constant<int, 16>{});
     });
   });
