@@ -109,6 +109,23 @@ __device__ __forceinline__ void open_codes(u32x2_t c, float s, float (&f)[8]) {
   }
 }
 
+// quant8 of fp8_codes.h, with the quotients v / s as q = v y, q + (v - s q) y, y =
+// 1 / s: three operations for the division's ten, and the same bits (the residual is
+// exact and y is rounded once, so the sum is the rounded quotient; divide: s so small
+// that the residual would not be exact).
+__device__ __forceinline__ uint2 quant8_by(uint4 v, float s, float y, bool divide) {
+  if (divide) return quant8(v, s);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  auto quotient = [&](uint32_t bits) {
+    const float x = __uint_as_float(bits), q = x * y;
+    return fminf(fmaxf(fmaf(fmaf(-s, q, x), y, q), -kE4M3Max), kE4M3Max);
+  };
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = fp8x2(quotient(w[i] << 16), quotient(w[i] & 0xFFFF0000u));
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 // Rows of d elements in ppr pieces.
 struct Shape {
   uint32_t d, ppr, n_rows;
@@ -218,7 +235,8 @@ __global__ __launch_bounds__(256) void unpermute_kernel(
       const uint4 u = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
       const float top = __uint_as_float(row16_max_u32(abs_max8(u)));
       const float scale = top / kE4M3Max;
-      const uint2 q = top != 0.0f ? quant8(u, scale) : make_uint2(0, 0);
+      const uint2 q =
+          top != 0.0f ? quant8_by(u, scale, 1.0f / scale, top < 0x1p-60f) : make_uint2(0, 0);
       const int64_t at = (int64_t)p[k] * shape.ppr + c;
       __builtin_nontemporal_store(u32x2_t{q.x, q.y}, codes + at);
       if ((threadIdx.x & 15) == 0) scales[at >> 4] = top != 0.0f ? scale : 0.0f;

@@ -258,6 +258,28 @@ def test_rows_kept_in_8_bits(M, N, d, E, K, away):
     assert torch.equal(drows[:n], plain[:n])
 
 
+def test_kept_codes_of_every_significand(M):
+    """The codes that unpermute leaves are the row quantiser's, bit for bit: every
+    significand of a group's largest value against every significand of its others,
+    over the E4M3 range and below, at exponents down to where the scale is
+    subnormal."""
+    import torch
+    sig = torch.arange(128, 256, device="cuda").double() / 128
+    for e in (-126, -100, -61, -59, 0, 40, 119):
+        groups = []
+        for shift in range(0, 20):
+            other = torch.ldexp(sig, torch.tensor(-shift, device="cuda"))
+            m = torch.where(torch.arange(128, device="cuda") % 2 == 1, -other, other).repeat(128, 1)
+            m[:, 0] = sig * 2      # the group's largest value
+            groups.append(m)
+        rows = torch.ldexp(torch.cat(groups, 1), torch.tensor(e, device="cuda")).bfloat16()
+        N = rows.shape[0]
+        g = M.group_tokens(torch.zeros(N, 1, dtype=torch.int32, device="cuda"), 2)
+        _, kept = M.unpermute(rows, g, checkpoint=True)
+        codes, scales = M.fp8_quantize_rows(rows)
+        assert torch.equal(kept[1], scales) and torch.equal(kept[0], codes), e
+
+
 def test_gradients_against_differences(M):
     """fp32 rows: (L(w + h) - L(w - h)) / 2h of L = <dy, y>, which is linear in
     every argument, so only roundings separate the two: 2 (K + 2) U of the terms
