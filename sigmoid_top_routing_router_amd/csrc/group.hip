@@ -17,9 +17,11 @@
 //     bucket are found with nine ballots over the bits of its number, the rank
 //     among them is a popcount, and the lowest such lane advances the bucket's
 //     running place.
-// The launches' latencies bound it (98304 pairs: 1.2 MB in GROUP_US us).  Sixteen
-// waves a block keep the table short and the walks shorter: with four waves (the
-// layer's form, which also makes the GEMMs' tile table) 14.4 us.
+// Latencies bound it: 98304 pairs (1.2 MB) take 11 us one call after the other, 6185
+// pairs in one block 9, six pairs 3.6.  Sixteen waves a block keep the table short and
+// the walks shorter: with four waves (the layer's form, which also makes the GEMMs'
+// tile table) 98304 pairs take 14.4 us.  In the one block the sorted pairs go straight
+// to their places; gathered in LDS first they took as long.
 #include <algorithm>
 
 #include "common.h"
@@ -30,7 +32,7 @@ namespace {
 
 constexpr int kBlockWaves = 16;
 constexpr int kThreads = kBlockWaves * kWave;
-constexpr int64_t kSmall = 8192;   // pairs of the one-block form (they fit 16 bits)
+constexpr int64_t kSmall = 8192;   // pairs of the one-block form
 constexpr int64_t kMaxBlocks = 64;
 constexpr int kAtOnce = 4;         // loads of ids in flight
 constexpr int64_t kChunk = kAtOnce * kWave;  // pairs a wave, at least
@@ -40,11 +42,11 @@ __device__ __forceinline__ uint32_t bucket_of(int32_t id, int E) {
   return min((uint32_t)id, (uint32_t)E);
 }
 
-// Places of up to 64 consecutive pairs, put(place, pair): pos holds the wave's
-// running place in every bucket.
-template <class Put>
+// Places of up to 64 consecutive pairs: pos holds the wave's running place in
+// every bucket.
 __device__ __forceinline__ void place_wave(uint32_t e, bool ok, int E, int64_t pair, uint32_t* pos,
-                                           int32_t* __restrict__ src_pos, Put&& put) {
+                                           int32_t* __restrict__ sorted_src,
+                                           int32_t* __restrict__ src_pos) {
   uint64_t same = ballot(ok);
 #pragma unroll
   for (int b = 0; b < 9; ++b) {
@@ -55,7 +57,7 @@ __device__ __forceinline__ void place_wave(uint32_t e, bool ok, int E, int64_t p
   const uint64_t lower = same & lanemask_lt();
   if (ok) {
     const uint32_t at = pos[e] + (uint32_t)__popcll(lower);
-    put(at, e < (uint32_t)E ? (int32_t)pair : -1);
+    sorted_src[at] = e < (uint32_t)E ? (int32_t)pair : -1;
     src_pos[pair] = e < (uint32_t)E ? (int32_t)at : -1;
   }
   __builtin_amdgcn_wave_barrier();
@@ -95,9 +97,6 @@ __global__ __launch_bounds__(kThreads) void group_small_kernel(
   constexpr int kSteps = (int)(kSmall / kThreads);
   __shared__ uint32_t pos[kBlockWaves][kBuckets];
   __shared__ uint32_t tot[kBuckets], wave_sum[kBlockWaves];
-  // the sorted pairs; stored straight to their places, one CU takes a cycle for
-  // every pair (6185 pairs: SMALL_BEFORE us, so SMALL_AFTER)
-  __shared__ int16_t sorted[kSmall];
   const int tid = threadIdx.x, w = tid >> 6, lane = lane_id(), B = E + 1;
   const int64_t len = (pairs + kBlockWaves - 1) / kBlockWaves;
   const int64_t i0 = w * len, i1 = min(pairs, i0 + len);
@@ -130,12 +129,8 @@ __global__ __launch_bounds__(kThreads) void group_small_kernel(
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int64_t i = i0 + s * kWave;
-    if (i < i1)
-      place_wave(e[s], i + lane < i1, E, i + lane, pos[w], src_pos,
-                 [&](uint32_t at, int32_t pair) { sorted[at] = (int16_t)pair; });
+    if (i < i1) place_wave(e[s], i + lane < i1, E, i + lane, pos[w], sorted_src, src_pos);
   }
-  __syncthreads();
-  for (int i = tid; i < (int)pairs; i += kThreads) sorted_src[i] = sorted[i];
 }
 
 __global__ __launch_bounds__(kThreads) void group_count_kernel(
@@ -228,9 +223,7 @@ __global__ __launch_bounds__(kThreads) void group_place_kernel(
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       const int64_t at = i + j * kWave;
-      if (at < i1)
-        place_wave(x[j], at + lane < i1, E, at + lane, pos[w], src_pos,
-                   [&](uint32_t to, int32_t pair) { sorted_src[to] = pair; });
+      if (at < i1) place_wave(x[j], at + lane < i1, E, at + lane, pos[w], sorted_src, src_pos);
     }
   }
 }

@@ -34,9 +34,10 @@ constexpr float kInt8Max = 127.0f;
 
 // Four integers.  The quotient v / s rounded to fp32 as q = v y, q + (v - s q) y
 // with y = 1 / s (three operations in the place of a division's; the residual is
-// exact): half of the largest value is a tie but for the rounding of s, and the
-// product alone then misses the quotient's integer.  divide: s is so small that
-// the residual would not be exact.
+// exact, and the sum is the rounded quotient for each of the 2^14 pairs of
+// significands of v and of the largest value): half of the largest value is a tie
+// but for the rounding of s, and the product alone then misses the quotient's
+// integer.  divide: s is so small that the residual would not be exact.
 __device__ __forceinline__ uint32_t int8x4(const float (&v)[4], float s, float y, bool divide) {
   uint32_t c = 0;
 #pragma unroll

@@ -280,6 +280,22 @@ def test_kept_codes_of_every_significand(M):
         assert torch.equal(kept[1], scales) and torch.equal(kept[0], codes), e
 
 
+def test_kept_codes_of_infinities(M):
+    """Groups with an infinity or a NaN: the row quantiser's codes and scales there too."""
+    import torch
+    rng = np.random.default_rng(5)
+    rows = torch.from_numpy(rng.standard_normal((6, 384)).astype(np.float32)).cuda().bfloat16()
+    rows[0, 3], rows[1, 200], rows[2, 383] = float("inf"), float("-inf"), float("nan")
+    rows[3, 0], rows[3, 1] = float("inf"), float("nan")
+    g = M.group_tokens(torch.zeros(6, 1, dtype=torch.int32, device="cuda"), 2)
+    _, kept = M.unpermute(rows, g, checkpoint=True)
+    codes, scales = M.fp8_quantize_rows(rows)
+    assert torch.equal(kept[0], codes)
+    assert torch.equal(kept[1].view(torch.int32) & 0x7FC00000, scales.view(torch.int32) & 0x7FC00000)
+    finite = torch.isfinite(scales)
+    assert int(finite.sum()) == 14 and torch.equal(kept[1][finite], scales[finite])
+
+
 def test_gradients_against_differences(M):
     """fp32 rows: (L(w + h) - L(w - h)) / 2h of L = <dy, y>, which is linear in
     every argument, so only roundings separate the two: 2 (K + 2) U of the terms
