@@ -318,3 +318,72 @@ def test_refusals(M):
         with pytest.raises(kind):
             call()
     assert M.int8_matmul((q[0][:0], q[1][:0]), w).shape == (0, 24)
+
+
+# Shapes large enough for the tiles of 64, 128, 192 and 256 rows, one to six stages
+# deep, and for the few-row forms that the lists above do not reach.
+DENSE_LARGE = [  # n, k, cols
+    (34, 48, 4112), (38, 384, 2272), (288, 32, 264), (35, 272, 4072),
+    (130, 48, 4024), (147, 160, 4160), (133, 320, 4136),
+    (5661, 16, 528), (5969, 144, 520), (5751, 272, 520), (5910, 16, 296), (5616, 400, 280),
+    (4695, 16, 1568), (4127, 144, 1800), (5457, 272, 1296), (5420, 16, 664), (4652, 656, 776),
+    (5489, 16, 2064), (4419, 144, 2600), (4821, 656, 2312), (1354, 16, 4128), (1731, 144, 3224),
+]
+GROUPED_LARGE = [  # N, E, K, k, cols
+    (5, 8, 1, 176, 3160), (101, 8, 3, 336, 3176), (8, 8, 1, 144, 640), (57, 3, 1, 288, 2032),
+    (5303, 5, 1, 16, 528), (5381, 5, 1, 272, 536), (2783, 5, 2, 144, 528), (330, 8, 1, 16, 3792),
+    (101, 8, 3, 656, 3848), (1541, 8, 1, 16, 4128), (786, 8, 2, 272, 3904), (577, 8, 1, 16, 3952),
+    (188, 8, 3, 400, 3928), (2365, 8, 1, 16, 3856), (1263, 8, 2, 656, 3728), (266, 8, 3, 144, 4088),
+]
+
+
+def check_large(y, q, s, w, w_up):
+    """check with the product by torch in 64 bits (sums below 2^53: exact)."""
+    def product(v):
+        return (q.double() @ v[0].double().T) * s.double()[:, None] * v[1].double()[None, :]
+    g, y = product(w), y.double()
+    if w_up is None:
+        assert bool(((y - g).abs() <= (3.1 * U + HALF) * g.abs() + TINY).all())
+        return
+    u = product(w_up)
+    h = g / (1 + (-g).exp()) * u
+    tol = (HALF + 2.0 ** -19 + g.abs() * 2.0 ** -22) * h.abs() + TINY * (1 + u.abs())
+    assert bool(((y - h).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("n,k,cols", DENSE_LARGE)
+def test_dense_large(M, n, k, cols, up):
+    say("dense", n, k, cols, up)
+    rng = np.random.default_rng(n * 7 + k + cols)
+    q, s = integers(rng, (n, k)), scales(rng, n, 1 / np.sqrt(k) / 5000)
+    w = integers(rng, (cols, k)), scales(rng, cols)
+    w_up = (integers(rng, (cols, k)), scales(rng, cols)) if up else None
+    check_large(M.int8_matmul((q, s), w, w_up=w_up), q, s, w, w_up)
+
+
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("N,E,K,k,cols", GROUPED_LARGE)
+def test_grouped_large(M, N, E, K, k, cols, up):
+    """Loads from none to half of the pairs, some pairs elsewhere; rows gathered where
+    a token has more than one expert."""
+    import torch
+    gather = K > 1
+    say("grouped", N, E, K, k, cols, gather, up)
+    rng = np.random.default_rng(N + E + k)
+    chance = np.array([0.0] + [2.0 ** -e for e in range(E - 1)] + [0.1])
+    ids = rng.choice(E + 1, (N, K), p=chance / chance.sum())
+    g = M.group_tokens(torch.from_numpy(ids.astype(np.int32)).cuda(), E)
+    n = N if gather else N * K
+    q, s = integers(rng, (n, k)), scales(rng, n, 1 / np.sqrt(k) / 5000)
+    w = integers(rng, (E, cols, k)), scales(rng, (E, cols))
+    w_up = (integers(rng, (E, cols, k)), scales(rng, (E, cols))) if up else None
+    out = torch.full((N * K, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    M.int8_matmul((q, s), w, w_up=w_up, grouping=g, gather=gather, out=out)
+    offsets, src = host(g.offsets), host(g.sorted_src)
+    for e in range(E):
+        lo, hi = offsets[e], offsets[e + 1]
+        rows = torch.from_numpy(src[lo:hi] // K if gather else np.arange(lo, hi)).long().cuda()
+        check_large(out[lo:hi], q[rows], s[rows], (w[0][e], w[1][e]),
+                    None if w_up is None else (w_up[0][e], w_up[1][e]))
+    assert bool((out[offsets[-1]:] == 7.0).all())
