@@ -266,7 +266,10 @@ struct Buffer {
 // weights' way from HBM (64 tokens of six among 384 experts: 0.64 GB in 112 us, 5.7
 // TB/s); many rows of many experts, both in part: without products the same loads
 // take 313 of the 344 us (1.44 GB past L2), from L2 alone with products 280.
-template <int MB, bool UP>
+//
+// The results go past the caches (98304 rows, 512 deep, 2560 columns: 281 us without,
+// 270 so).  ONCE: so do the weights.
+template <int MB, bool UP, bool ONCE>
 __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, char* lds) {
   typedef TileShape<MB> S;
   constexpr int OC = UP ? kCols / 2 : kCols;  // output columns of a tile
@@ -350,8 +353,9 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
   // lie past the buffer
   auto load_b = [&](int kt, int q, int i) {
     const uint32_t off = b_off + (uint32_t)(UP ? i & 1 : i) * 64u * (uint32_t)a.k;
-    dma16(UP && i >= 2 ? ru.rsrc() : rw.rsrc(), kt == nk - 1 && !k_in ? kNoRow : off,
-          (uint32_t)kt * kStage, (lds_void_t*)(lds + S::b_at + q * kQuarter + wave * 1024));
+    dma16<ONCE ? kCpolNT : 0>(
+        UP && i >= 2 ? ru.rsrc() : rw.rsrc(), kt == nk - 1 && !k_in ? kNoRow : off,
+        (uint32_t)kt * kStage, (lds_void_t*)(lds + S::b_at + q * kQuarter + wave * 1024));
   };
   auto place = [&](int q) { return q >= S::quarters ? q - S::quarters : q; };
   // a tile's first stages: A's two slots, B's three stages
@@ -555,8 +559,9 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
       auto store = [&](const uint32_t (&w)[4], int r, int c) {
         const int at = 32 * (first + m) + r;
         if (at < now.rows && c < now_cols)
-          *reinterpret_cast<u32x4_t*>(a.out + (now.row0 + at) * a.cols + now_col0 + c) =
-              u32x4_t{w[0], w[1], w[2], w[3]};
+          __builtin_nontemporal_store(
+              u32x4_t{w[0], w[1], w[2], w[3]},
+              reinterpret_cast<u32x4_t*>(a.out + (now.row0 + at) * a.cols + now_col0 + c));
       };
       if constexpr (UP) {
 #pragma unroll
@@ -595,10 +600,10 @@ __global__ __launch_bounds__(512, 2) void int8_dense_kernel(Int8Args a, uint32_t
     t.rows = (int)min((int64_t)TileShape<MB>::rows, a.rows - t.row0);
     return t;
   });
-  if (list.count > 0) int8_tiles<MB, UP>(a, list, lds);
+  if (list.count > 0) int8_tiles<MB, UP, false>(a, list, lds);
 }
 
-template <int MB, bool UP>
+template <int MB, bool UP, bool ONCE>
 __global__ __launch_bounds__(512, 2) void int8_grouped_kernel(Int8Args a, uint32_t col_tiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr uint32_t bm = TileShape<MB>::rows;
@@ -611,7 +616,7 @@ __global__ __launch_bounds__(512, 2) void int8_grouped_kernel(Int8Args a, uint32
       return s.tile(item / col_tiles, bm, true);
     });
   }
-  if (list.count > 0) int8_tiles<MB, UP>(a, list, lds);
+  if (list.count > 0) int8_tiles<MB, UP, ONCE>(a, list, lds);
 }
 
 // Few rows: a block takes 16 RG rows and 16 CB columns (of each weight), its four
@@ -769,10 +774,13 @@ namespace {
 template <int MB>
 hipError_t allow_lds() {
   const void* kernels[] = {
-      (const void*)int8_grouped_kernel<MB, true>, (const void*)int8_grouped_kernel<MB, false>,
+      (const void*)int8_grouped_kernel<MB, true, false>,
+      (const void*)int8_grouped_kernel<MB, false, false>,
+      (const void*)int8_grouped_kernel<MB, true, true>,
+      (const void*)int8_grouped_kernel<MB, false, true>,
       (const void*)int8_dense_kernel<MB, true>, (const void*)int8_dense_kernel<MB, false>};
-  static std::atomic<uint32_t> done[4];
-  for (int i = 0; i < 4; ++i) {
+  static std::atomic<uint32_t> done[6];
+  for (int i = 0; i < 6; ++i) {
     const hipError_t e = set_lds_limit_once(kernels[i], TileShape<MB>::lds, done[i]);
     if (e != hipSuccess) return e;
   }
@@ -840,7 +848,16 @@ hipError_t launch_grouped(const Int8Args& a, hipStream_t stream) {
   auto go = [&](auto kernel) {
     return launch_tiles(kernel, TileShape<MB>::lds, blocks, stream, a, (uint32_t)col_tiles);
   };
-  return a.w_up ? go(int8_grouped_kernel<MB, true>) : go(int8_grouped_kernel<MB, false>);
+  // Most experts have one tile, and their weights do not fit the memory-side cache:
+  // each is read once (2560 x 2 x 512, 384 experts, a row each 112 us, 101 so; 64 rows
+  // each 224, 211; 128 rows in tiles of 192 would take 260 for 257).
+  const int64_t experts = std::min<int64_t>(a.E, a.rows);
+  const int64_t weights = experts * a.cols * (int64_t)a.k * (a.w_up ? 2 : 1);
+  const bool once = a.rows <= experts * (TileShape<MB>::rows / 2) && weights > (int64_t(256) << 20);
+  if (once) return a.w_up ? go(int8_grouped_kernel<MB, true, true>)
+                          : go(int8_grouped_kernel<MB, false, true>);
+  return a.w_up ? go(int8_grouped_kernel<MB, true, false>)
+                : go(int8_grouped_kernel<MB, false, false>);
 }
 template <int MB>
 hipError_t launch_dense(const Int8Args& a, hipStream_t stream) {
@@ -863,10 +880,13 @@ double expected_tiles(const Int8Args& a, int bm) {
 }
 // Microseconds of a launch, by a fit to what shapes from 1 to 16384 rows, 512 to
 // 8192 deep, took dense and with 16 to 384 experts (within a fifth of most).
-// Tiles: 0.22 (MB + 1) a stage and 1 a tile, 256 at a time.
+// Tiles: 0.22 (MB + 1) a stage and 1 a tile, 256 at a time; experts' weights that no
+// more than a tile or two share slow a stage by 0.18 where memory is busy for more
+// than one round.
 double tile_cost(const Int8Args& a, int mb) {
   const double rounds = std::ceil(expected_tiles(a, 64 * mb) * column_tiles(a) / kCus);
-  return 3.5 + rounds * (1.0 + (a.k + kStage - 1) / kStage * 0.22 * (mb + 1));
+  const double stage = 0.22 * (mb + 1) + (a.offsets && rounds > 1 ? 0.18 : 0.0);
+  return 3.5 + rounds * (1.0 + (a.k + kStage - 1) / kStage * stage);
 }
 // Few rows: what the blocks read at 8 TB/s, 1.2 for every further 256 blocks (twice
 // that where each looks for its expert), but no block faster than its own operands

@@ -387,3 +387,31 @@ def test_grouped_large(M, N, E, K, k, cols, up):
         check_large(out[lo:hi], q[rows], s[rows], (w[0][e], w[1][e]),
                     None if w_up is None else (w_up[0][e], w_up[1][e]))
     assert bool((out[offsets[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("rows,E,k,cols,up", [
+    (16, 16, 4096, 4104, False), (16, 16, 4096, 2056, True), (4031, 64, 8192, 520, False),
+    (9999, 200, 2560, 264, True), (30720, 384, 4096, 264, False), (6079, 64, 528, 4104, True),
+    (42240, 384, 4096, 264, False), (24000, 200, 256, 4104, True)])
+def test_many_experts_of_few_rows(M, rows, E, k, cols, up):
+    """More weights than the memory-side cache holds, most experts in one tile."""
+    import torch
+    say("grouped", rows, E, k, cols, up)
+    gen = torch.Generator(device="cuda").manual_seed(rows + k)
+
+    def weight():
+        return (torch.randint(-127, 128, (E, cols, k), generator=gen, device="cuda",
+                              dtype=torch.int8),
+                torch.rand(E, cols, generator=gen, device="cuda") + 0.5)
+    w, w_up = weight(), weight() if up else None
+    ids = torch.randint(0, E, (rows, 1), generator=gen, device="cuda", dtype=torch.int32)
+    ids[rows // 2:rows // 2 + rows // 8] = E // 2    # one expert of several tiles
+    g = M.group_tokens(ids, E)
+    q = torch.randint(-127, 128, (rows, k), generator=gen, device="cuda", dtype=torch.int8)
+    s = (torch.rand(rows, generator=gen, device="cuda") + 0.5) / (5000 * k ** 0.5)
+    y = M.int8_matmul((q, s), w, w_up=w_up, grouping=g)
+    offsets = host(g.offsets)
+    for e in {0, 1, E // 2, E // 3, E - 1}:
+        lo, hi = offsets[e], offsets[e + 1]
+        check_large(y[lo:hi], q[lo:hi], s[lo:hi], (w[0][e], w[1][e]),
+                    None if w_up is None else (w_up[0][e], w_up[1][e]))
