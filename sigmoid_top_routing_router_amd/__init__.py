@@ -62,7 +62,7 @@ def _dev(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -851,6 +851,11 @@ class Grouping:
     src_pos: object     # [N, K] sorted row of every pair, -1 without one
 
 
+@functools.lru_cache(maxsize=1024)
+def _group_workspace(N, E, K):
+    return max(int(_lib.load().moe_group_workspace_bytes(N, E, K)), 256)
+
+
 def group_tokens(topk_ids, E: int, workspace=None, stream=None) -> Grouping:
     """Stable grouping of the pairs of topk_ids (int32 [N, K]) by expert
     (moe_group).  Ids outside [0, E) (experts on other GPUs, dropped pairs) have
@@ -862,7 +867,7 @@ def group_tokens(topk_ids, E: int, workspace=None, stream=None) -> Grouping:
         raise ValueError("topk_ids must be [N, K]")
     N, K = topk_ids.shape
     _one_device(topk_ids, workspace=workspace)
-    need = max(int(lib.moe_group_workspace_bytes(N, E, K)), 256) if workspace is None else 0
+    need = _group_workspace(N, E, K) if workspace is None else 0
     with _on_device(topk_ids, stream):
         # one allocation for the four outputs and the workspace: 3 us less a call on
         # the host than one each (of 14)
