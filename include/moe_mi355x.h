@@ -703,9 +703,9 @@ moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const 
  * scales [n]: s = amax * (1 / 127), the reciprocal and the product rounded to
  * fp32, code = x / s rounded to nearest even, in [-127, 127]; a row of zeros
  * has s = 0 and zeros.  A row with an infinity or a NaN has the scale NaN and
- * zeros.  Weights [E,cols,k] are quantised as
- * E*cols rows of k: a scale for each output channel.  n >= 0, cols % 16 == 0
- * (16 <= cols <= 65536); x and codes 16-byte aligned.
+ * zeros.  Weights [E,cols,k] are quantised as E*cols rows of k: a scale for
+ * each output channel.  n >= 0, cols % 16 == 0 (16 <= cols <= 65536); x and
+ * codes 16-byte aligned.
  *
  * moe_int8_matmul - out[r,c] = a_scales[s] w_scales[e,c] sum_k a[s,k] w[e,c,k],
  * rounded to bf16; with w_up silu(out) times the same of w_up, formed in fp32.

@@ -258,17 +258,20 @@ struct Buffer {
 // and stored (straight from registers), the next tile's first stages are on their
 // way into LDS: a block to each tile spent 1.9 us on finding it, 4.4 until its first
 // products and 5.1 behind its last ones, next to 25 us of products.  98304 rows of
-// 384 experts, 2560 deep, 2 x 512 columns: 355 us that way, 344 this way; 2048 rows
-// of 128 experts, 512 deep, 2560 columns: 41 and 32.
+// 384 experts, 2560 deep, 2 x 512 columns, tiles of 192 rows: 355 us that way, 344
+// this way; 2048 rows of 128 experts, 512 deep, 2560 columns: 41 and 32.
 //
 // What bounds it: dense, the power of the matrix instructions (8192 x 8192 x 8192:
 // 405 us, 2.7 POP/s, in use 71% of the time at 1.7 GHz); few rows an expert, the
-// weights' way from HBM (64 tokens of six among 384 experts: 0.64 GB in 112 us, 5.7
-// TB/s); many rows of many experts, both in part: without products the same loads
-// take 313 of the 344 us (1.44 GB past L2), from L2 alone with products 280.
+// weights' way from HBM (64 tokens of six among 384 experts: 0.64 GB in 97 us, 6.6
+// TB/s); many rows of many experts, both in part.  The 98304 rows above, 22 to 1243 an
+// expert: 339 us in tiles of 256, the same loads without products 304, from L2 with
+// products 265, products alone 210; 256 rows an expert: 298, 266, 233 and 186.  Tiles
+// in descending size, dealt so that all blocks end together, were no faster: a block
+// that ends early leaves its share of both to the others.
 //
-// The results go past the caches (98304 rows, 512 deep, 2560 columns: 281 us without,
-// 270 so).  ONCE: so do the weights.
+// The results go past the caches (98304 rows, 512 deep, 2560 columns: 287 us without,
+// 281 so).  ONCE: so do the weights.
 template <int MB, bool UP, bool ONCE>
 __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, char* lds) {
   typedef TileShape<MB> S;
@@ -904,8 +907,8 @@ double few_cost(const Int8Args& a, int rg, int cb) {
 
 // The cheapest form by the fits above.  2560 x 2560 weights, us: 1 row 5.3 (few,
 // 1 x 1; tiles of MB 1 11.7), 64 rows 8.6 (few, 2 x 2; 11.7), 512 rows 12.7 (MB 1;
-// MB 4 27, few 4 x 4 25), 4096 rows 29 (MB 3; MB 1 42); 8192 x 8192 x 8192 405 (MB
-// 4; MB 2 449).
+// MB 4 27, few-row blocks of 64 x 64 25), 4096 rows 29 (MB 3; MB 1 42); 8192 x 8192 x
+// 8192 405 (MB 4; MB 2 449).
 hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream) {
   typedef hipError_t (*Launch)(const Int8Args&, hipStream_t);
   struct Form {
