@@ -708,7 +708,9 @@ moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const 
  * codes 16-byte aligned.
  *
  * moe_int8_matmul - out[r,c] = a_scales[s] w_scales[e,c] sum_k a[s,k] w[e,c,k],
- * rounded to bf16; with w_up silu(out) times the same of w_up, formed in fp32.
+ * the two scales' product formed first, in fp32 (so it must not underflow), and
+ * the result rounded to bf16; with w_up silu(out) times the same of w_up, formed
+ * in fp32.
  *  a            [a_rows,k] integers (-128 too), a_scales [a_rows] fp32.
  *  w            [E,cols,k] integers, w_scales [E,cols] fp32; w_up, w_up_scales
  *               the same or both NULL.
