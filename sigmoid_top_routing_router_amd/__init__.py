@@ -67,23 +67,27 @@ def _dev(t, name, dtype=None, shape=None):
     return t
 
 
-def _current_device():
-    """torch.cuda.current_device(), by torch's own short cut where it has one (0.14
-    us a call instead of 0.26)."""
+_short_cuts = (None, None, None)
+
+
+def _torch_calls():
+    """torch, and its short cuts to the current device (0.14 us a call instead of
+    0.26) and to the handle of the current stream without its object (0.5 us
+    instead of 2.9, of the 13 that a small call takes on the host): not public
+    names of torch's, so either may be missing (None)."""
+    global _short_cuts
     torch = _torch()
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return torch.cuda.current_device() if get is None else get()
+    if _short_cuts[0] is not torch:
+        _short_cuts = (torch, getattr(torch._C, "_cuda_getDevice", None),
+                       getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return _short_cuts
 
 
 def _stream(stream):
-    torch = _torch()
     if stream is None:
-        # the handle of torch.cuda.current_stream() without its object (0.5 us a
-        # call instead of 2.9, of the 13 that a small call takes on the host);
-        # not a public name of torch's, so it may be missing
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch, get, raw = _torch_calls()
         if raw is not None:
-            return C.c_void_p(raw(_current_device()))
+            return C.c_void_p(raw(torch.cuda.current_device() if get is None else get()))
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
 
@@ -103,9 +107,9 @@ def _on(stream):
 def _on_device(t, stream):
     """_on(stream) with the device of t as the current one, for the calls that
     take tensors of another device than the current."""
-    torch = _torch()
-    if t.get_device() == _current_device():
-        return _on(stream)
+    torch, get, _ = _torch_calls()
+    if t.get_device() == (torch.cuda.current_device() if get is None else get()):
+        return _nothing if stream is None else _on(stream)
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(t.device))
     ctx.enter_context(_on(stream))
@@ -113,8 +117,9 @@ def _on_device(t, stream):
 
 
 def _one_device(first, **others):
+    device = first.get_device()
     for name, t in others.items():
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
