@@ -867,6 +867,8 @@ def group_tokens(topk_ids, E: int, workspace=None, stream=None) -> Grouping:
     no place."""
     torch = _torch()
     lib = _lib.load()
+    if stream is None and workspace is None and (r := _lib.calls.group(topk_ids, E)):
+        return Grouping(*r)
     topk_ids = _dev(topk_ids, "topk_ids", torch.int32)
     if topk_ids is None or topk_ids.dim() != 2:
         raise ValueError("topk_ids must be [N, K]")
@@ -923,6 +925,11 @@ def permute(x, grouping: Grouping, out=None, stream=None):
     held (without it they are unspecified)."""
     torch = _torch()
     lib = _lib.load()
+    if stream is None:
+        pair = x if isinstance(x, (tuple, list)) and len(x) == 2 else (x, None)
+        rows = _lib.calls.permute(*pair, grouping.src_pos, out)
+        if rows is not None:
+            return rows
     pos = _places(grouping)
     N, K = pos.shape
     scales, flags = None, 0
@@ -952,6 +959,10 @@ def permute_backward(grad_rows, grouping: Grouping, stream=None):
     grad_rows[src_pos[t, k]], [N, d] in the type of grad_rows [N*K, d]."""
     torch = _torch()
     lib = _lib.load()
+    if stream is None:
+        grad_x = _lib.calls.permute_backward(grad_rows, grouping.src_pos)
+        if grad_x is not None:
+            return grad_x
     pos = _places(grouping)
     N, K = pos.shape
     grad_rows = _dev(grad_rows, "grad_rows", _row_types())
@@ -978,6 +989,10 @@ def unpermute(rows, grouping: Grouping, weights=None, base=None, checkpoint: boo
     for unpermute_backward, else None."""
     torch = _torch()
     lib = _lib.load()
+    if stream is None:
+        r = _lib.calls.unpermute(rows, grouping.src_pos, weights, base, bool(checkpoint))
+        if r is not None:
+            return r[0], r[1:] if checkpoint else None
     pos = _places(grouping)
     N, K = pos.shape
     rows = _dev(rows, "rows", _row_types())
@@ -1010,6 +1025,11 @@ def unpermute_backward(grad_y, grouping: Grouping, weights=None, rows=None, out=
     they are unspecified)."""
     torch = _torch()
     lib = _lib.load()
+    if stream is None:
+        pair = rows if isinstance(rows, (tuple, list)) and len(rows) == 2 else (rows, None)
+        r = _lib.calls.unpermute_backward(grad_y, grouping.src_pos, weights, *pair, out)
+        if r is not None:
+            return r
     pos = _places(grouping)
     N, K = pos.shape
     grad_y = _dev(grad_y, "grad_y", _row_types())
@@ -1039,6 +1059,9 @@ def int8_quantize_rows(x, stream=None):
     [...]), one scale per row (moe_int8_quantize_rows): tokens [n, C], or
     weights [E, cols, k] with a scale for each output channel."""
     torch = _torch()
+    lib = _lib.load()
+    if stream is None and (r := _lib.calls.int8_quantize_rows(x)):
+        return r
     x = _dev(x, "x", _bf16())
     if x is None or x.dim() < 2:
         raise ValueError("x must be [..., C]")
@@ -1046,8 +1069,8 @@ def int8_quantize_rows(x, stream=None):
     with _on_device(x, stream):
         codes = x.new_empty(x.shape, dtype=torch.int8)
         scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
-        _lib.check(_lib.load().moe_int8_quantize_rows(_ptr(x), n, Cc, _ptr(codes), _ptr(scales),
-                                                      _stream(stream)))
+        _lib.check(lib.moe_int8_quantize_rows(_ptr(x), n, Cc, _ptr(codes), _ptr(scales),
+                                              _stream(stream)))
     return codes, scales
 
 
@@ -1076,6 +1099,13 @@ def int8_matmul(x, w, w_up=None, grouping: Grouping = None, gather: bool = False
     are unspecified)."""
     torch = _torch()
     lib = _lib.load()
+    if stream is None and (grouping is not None or not gather):
+        up, by = (None, None) if w_up is None else w_up, grouping
+        r = _lib.calls.int8_matmul(
+            *x[:2], *w[:2], *up[:2], by and by.offsets, by.sorted_src if gather else None,
+            by and by.src_pos, out)
+        if r is not None:
+            return r
     a = _dev(x[0], "x codes", torch.int8)
     if a is None or a.dim() != 2:
         raise ValueError("x codes must be [n, k]")

@@ -102,11 +102,12 @@ class MoeError(RuntimeError):
 
 
 _lib = None
+calls = None  # the extension module, once the library is loaded
 
 
 def load(path: str = LIB_PATH):
     """Load the HIP library (once).  Raises if it has not been built."""
-    global _lib
+    global _lib, calls
     if _lib is not None:
         return _lib
     import torch  # noqa: F401  (binds the process to torch's HIP runtime first)
@@ -208,8 +209,25 @@ def load(path: str = LIB_PATH):
     lib.moe_stage_times.restype = C.c_int
     lib.moe_stage_name.argtypes = [i32]
     lib.moe_stage_name.restype = C.c_char_p
+    calls = _bind_calls(lib)
     _lib = lib
     return lib
+
+
+_SHORT = ("moe_group_workspace_bytes", "moe_group", "moe_permute", "moe_permute_backward",
+          "moe_unpermute", "moe_unpermute_backward", "moe_int8_quantize_rows", "moe_int8_matmul")
+
+
+def _bind_calls(lib):
+    """The extension module with the short way to the small calls."""
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise RuntimeError("the binding's extension module is missing or was built for another "
+                           "torch: build it with `python -m sigmoid_top_routing_router_amd.build`"
+                           ) from e
+    _calls.bind(*(C.cast(getattr(lib, name), C.c_void_p).value for name in _SHORT))
+    return _calls
 
 
 def check(status: int):

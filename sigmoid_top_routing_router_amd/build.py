@@ -1,4 +1,5 @@
-"""Build the gfx950 shared library libmoe_mi355x.so in-tree with hipcc.
+"""Build the gfx950 shared library libmoe_mi355x.so, and the binding's extension
+module _calls.so, in-tree with hipcc.
 
     python -m sigmoid_top_routing_router_amd.build
 
@@ -48,6 +49,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_binding(verbose: bool = False) -> str:
+    """The extension module of the Python binding: host code against the installed
+    torch."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths, library_paths
+    out = os.path.join(HERE, "_calls.so")
+    cmd = [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", "/opt/rocm/include",
+           *(f for p in include_paths() for f in ("-isystem", p)),
+           "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding", "calls.cpp"), "-o", out + ".tmp",
+           *(f for p in library_paths() for f in ("-L", p)),
+           "-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    if verbose:
+        print(f"built {out}")
+    return out
+
+
 PROBES = os.path.join(HERE, "..", "tests", "probes")
 
 
@@ -74,8 +98,10 @@ def build_probes(verbose: bool = False):
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
-    with ThreadPoolExecutor(max(1, min(8, len(srcs)))) as ex:
+    with ThreadPoolExecutor(max(1, min(8, len(srcs) + 1))) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(_compile, srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
