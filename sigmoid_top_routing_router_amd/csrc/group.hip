@@ -7,21 +7,22 @@
 // the place  offsets[e] + #{p' < p : expert e};  pairs without an expert (on
 // another GPU, dropped) are a last bucket with no counts and no places.
 //
-// All integer work: the order does not depend on the launch.  Up to kSmall pairs
-// are one block's; more take two launches, kBlockWaves chunks of consecutive
-// pairs a block, one a wave:
+// All integer work: the order does not depend on the launch.  Lanes of one bucket
+// are found with nine ballots over the bits of its number, the rank among them is a
+// popcount, and the lowest such lane advances the bucket's running place.
+//
+// Up to kSmall pairs take one launch: a block to 1024 pairs, one a thread, and every
+// block counts all pairs, before its own, its own by wave, and behind.  More take
+// two launches, kBlockWaves chunks of consecutive pairs a block, one a wave:
 //  1. every block counts its pairs -> block_counts[b][bucket];
 //  2. every block reads the whole table (at most kMaxBlocks rows), which gives
 //     each bucket's total and its pairs in earlier blocks, scans the totals in
-//     expert order, counts its own chunks, and walks them in order: lanes of one
-//     bucket are found with nine ballots over the bits of its number, the rank
-//     among them is a popcount, and the lowest such lane advances the bucket's
-//     running place.
-// Latencies bound it: 98304 pairs (1.2 MB) take 11 us one call after the other, 6185
-// pairs in one block 9, six pairs 3.6.  Sixteen waves a block keep the table short and
-// the walks shorter: with four waves (the layer's form, which also makes the GEMMs'
-// tile table) 98304 pairs take 14.4 us.  In the one block the sorted pairs go straight
-// to their places; gathered in LDS first they took as long.
+//     expert order, counts its own chunks, and walks them in order.
+// Latencies bound it, one call after the other: six pairs 3.5 us, 6185 5.0 (8.5 in
+// one block, which has four waves a SIMD walk through them), 24000 8.5 (9.9 in two
+// launches), 32768 9.9 (10.1 in one), 98304 10.8 (1.2 MB).  Sixteen waves a block keep
+// the table short and the walks shorter: with four (the layer's form, which also makes
+// the GEMMs' tile table) 98304 pairs take 14.4 us.
 #include <algorithm>
 
 #include "common.h"
@@ -32,7 +33,8 @@ namespace {
 
 constexpr int kBlockWaves = 16;
 constexpr int kThreads = kBlockWaves * kWave;
-constexpr int64_t kSmall = 8192;   // pairs of the one-block form
+constexpr int64_t kSmall = 24576;  // pairs of the one-launch form
+constexpr int kAllAtOnce = 8;      // its loads of ids in flight
 constexpr int64_t kMaxBlocks = 64;
 constexpr int kAtOnce = 4;         // loads of ids in flight
 constexpr int64_t kChunk = kAtOnce * kWave;  // pairs a wave, at least
@@ -91,29 +93,38 @@ __device__ __forceinline__ void spread(uint32_t (*pos)[kBuckets], int e, uint32_
 }
 
 __global__ __launch_bounds__(kThreads) void group_small_kernel(
-    const int32_t* __restrict__ ids, int64_t pairs, int E, int32_t* __restrict__ counts,
+    const int32_t* __restrict__ ids, int pairs, int E, int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_src,
     int32_t* __restrict__ src_pos) {
-  constexpr int kSteps = (int)(kSmall / kThreads);
   __shared__ uint32_t pos[kBlockWaves][kBuckets];
-  __shared__ uint32_t tot[kBuckets], wave_sum[kBlockWaves];
-  const int tid = threadIdx.x, w = tid >> 6, lane = lane_id(), B = E + 1;
-  const int64_t len = (pairs + kBlockWaves - 1) / kBlockWaves;
-  const int64_t i0 = w * len, i1 = min(pairs, i0 + len);
-  uint32_t e[kSteps];
+  __shared__ uint32_t before[kBuckets], after[kBuckets], tot[kBuckets], wave_sum[kBlockWaves];
+  const int tid = threadIdx.x, w = tid >> 6, B = E + 1;
+  const int own = blockIdx.x * kThreads;  // the block's pairs, one a thread
+  uint32_t e[kAllAtOnce], mine = 0;
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t i = i0 + s * kWave + lane;
-    e[s] = i < i1 ? bucket_of(ids[i], E) : 0u;
-  }
+    for (int j = 0; j < kAllAtOnce; ++j) {
+      const int i = i0 + j * kThreads + tid;
+      e[j] = i < pairs ? bucket_of(ids[i], E) : 0u;
+    }
+  };
+  load(0);
   for (int i = tid; i < kBlockWaves * kBuckets; i += kThreads) (&pos[0][0])[i] = 0u;
+  if (tid < B) before[tid] = after[tid] = 0u;
   __syncthreads();
+  for (int i0 = 0; i0 < pairs; i0 += kAllAtOnce * kThreads) {
+    if (i0 > 0) load(i0);
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-    if (i0 + s * kWave + lane < i1) atomicAdd(&pos[w][e[s]], 1u);
+    for (int j = 0; j < kAllAtOnce; ++j) {
+      const int at = i0 + j * kThreads;
+      uint32_t* to = at < own ? before : at > own ? after : pos[w];
+      if (at == own) mine = e[j];
+      if (at + tid < pairs) atomicAdd(&to[e[j]], 1u);
+    }
+  }
   __syncthreads();
   if (tid < B) {
-    uint32_t sum = 0;
+    uint32_t sum = before[tid] + after[tid];
 #pragma unroll
     for (int q = 0; q < kBlockWaves; ++q) sum += pos[q][tid];
     tot[tid] = sum;
@@ -121,16 +132,14 @@ __global__ __launch_bounds__(kThreads) void group_small_kernel(
   __syncthreads();
   const uint32_t start = bucket_start(tot, B, wave_sum);
   if (tid < B) {
-    if (tid < E) counts[tid] = (int32_t)tot[tid];
-    offsets[tid] = (int32_t)start;
-    spread(pos, tid, start);
+    if (own == 0) {
+      if (tid < E) counts[tid] = (int32_t)tot[tid];
+      offsets[tid] = (int32_t)start;
+    }
+    spread(pos, tid, start + before[tid]);
   }
   __syncthreads();
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t i = i0 + s * kWave;
-    if (i < i1) place_wave(e[s], i + lane < i1, E, i + lane, pos[w], sorted_src, src_pos);
-  }
+  place_wave(mine, own + tid < pairs, E, own + tid, pos[w], sorted_src, src_pos);
 }
 
 __global__ __launch_bounds__(kThreads) void group_count_kernel(
@@ -247,8 +256,9 @@ hipError_t launch_group(const int32_t* ids, int64_t pairs, int E, int32_t* count
                         int32_t* offsets, int32_t* sorted_src, int32_t* src_pos,
                         uint32_t* block_counts, hipStream_t stream) {
   if (pairs <= kSmall) {
-    hipLaunchKernelGGL(group_small_kernel, dim3(1), dim3(kThreads), 0, stream, ids, pairs, E,
-                       counts, offsets, sorted_src, src_pos);
+    const int64_t blocks = std::max<int64_t>(1, (pairs + kThreads - 1) / kThreads);
+    hipLaunchKernelGGL(group_small_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, ids,
+                       (int)pairs, E, counts, offsets, sorted_src, src_pos);
     return hipGetLastError();
   }
   const int64_t cw = chunk_of(pairs), n = blocks_of(pairs);

@@ -64,7 +64,7 @@ def choice(rng, N, E, K, away):
 GROUPS = [  # N, E, K, away
     (0, 3, 2, "none"), (1, 1, 1, "none"), (1, 384, 6, "none"), (1, 2, 8, "some"),
     (64, 384, 6, "none"), (37, 5, 3, "some"), (50, 7, 2, "all"), (300, 384, 8, "one"),
-    (1365, 384, 6, "some"),      # 8190 pairs: the last size of the one-block form
+    (1365, 384, 6, "some"),      # 8190 pairs
     (1366, 384, 6, "none"),      # 8196 pairs
     (2731, 384, 6, "some"), (4097, 128, 8, "some"), (65537, 384, 8, "some"), (70001, 384, 1, "some"), (33000, 2, 4, "all"),
 ]
@@ -467,3 +467,25 @@ def test_refusals(M):
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("E", [1, 7, 384])
+@pytest.mark.parametrize("pairs", [1023, 1024, 1025, 2048, 8191, 8192, 8193, 16385, 24575, 24576,
+                                   24577, 30000])
+def test_group_around_the_blocks(M, pairs, E):
+    """Numbers of pairs around those of a block, of a thread's loads at once and of the
+    one launch; loads even, one expert's alone, and ids far out of range."""
+    import torch
+    rng = np.random.default_rng(pairs + E)
+    for kind in range(3):
+        ids = rng.integers(-1, E + 1, (pairs, 1))
+        if kind == 1:
+            ids[:] = E - 1
+        if kind == 2:
+            ids[rng.random((pairs, 1)) < 0.3] = rng.choice([2 ** 31 - 1, -2 ** 31, E])
+        t = torch.from_numpy(ids.astype(np.int32)).cuda()
+        g = M.group_tokens(t, E)
+        want = R.group(ids, E)
+        got = (g.counts, g.offsets, g.sorted_src, g.src_pos)
+        for a, b in zip(got, want):
+            assert np.array_equal(host(a).ravel(), np.asarray(b).ravel()), (pairs, E, kind)
