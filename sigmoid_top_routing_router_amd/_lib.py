@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_mi355x.so")
@@ -218,14 +219,22 @@ _SHORT = ("moe_group_workspace_bytes", "moe_group", "moe_permute", "moe_permute_
           "moe_unpermute", "moe_unpermute_backward", "moe_int8_quantize_rows", "moe_int8_matmul")
 
 
+class _LongWay:
+    """In the place of the extension module: no call is an ordinary one."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _bind_calls(lib):
     """The extension module with the short way to the small calls."""
     try:
         from . import _calls
     except ImportError as e:
-        raise RuntimeError("the binding's extension module is missing or was built for another "
-                           "torch: build it with `python -m sigmoid_top_routing_router_amd.build`"
-                           ) from e
+        warnings.warn(f"small calls take twice the time on the host: the binding's extension "
+                      f"module is missing or was built for another torch ({e}); build it with "
+                      f"`python -m sigmoid_top_routing_router_amd.build`")
+        return _LongWay()
     _calls.bind(*(C.cast(getattr(lib, name), C.c_void_p).value for name in _SHORT))
     return _calls
 

@@ -192,13 +192,6 @@ struct Segments {
   }
 };
 
-// The row of A behind output row r.
-__device__ __forceinline__ int64_t a_row_of(const Int8Args& a, int64_t r) {
-  if (!a.sorted_src) return r;
-  const int64_t t = (int64_t)a.sorted_src[r] / a.K;
-  return min(max(t, (int64_t)0), a.a_rows - 1);
-}
-
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
@@ -657,13 +650,11 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
                    : make_rsrc(a.a + tile.row0 * a.k, (uint32_t)tile.rows * (uint32_t)a.k);
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + w_row * a.k, w_bytes);
   const __amdgpu_buffer_rsrc_t ru = make_rsrc((UP ? a.w_up : a.w) + w_row * a.k, w_bytes);
-  uint32_t a_off[RG], b_off[CB];
+  uint32_t pair[RG], a_off[RG], b_off[CB];
 #pragma unroll
   for (int r = 0; r < RG; ++r) {
-    const int i = 16 * r + row;
-    a_off[r] = kNoRow;
-    if (i < tile.rows)
-      a_off[r] = (uint32_t)(a.sorted_src ? a_row_of(a, tile.row0 + i) : i) * (uint32_t)a.k;
+    const int i = min(16 * r + row, tile.rows - 1);
+    pair[r] = a.sorted_src ? (uint32_t)a.sorted_src[tile.row0 + i] : 0u;
   }
 #pragma unroll
   for (int c = 0; c < CB; ++c)
@@ -671,7 +662,7 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
 
   i32x4_t fa[kDepth][2][RG], fb[kDepth][2][NB], acc[RG][NB];
   // line i of this wave
-  auto load = [&](int buf, int i) {
+  auto load_b = [&](int buf, int i) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = (4 * i + wave) * 128 + 64 * h + piece;
@@ -684,6 +675,13 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
                          c < CB ? rw : ru, (int)(in && off != kNoRow ? off + (uint32_t)at : kNoRow),
                          0, 0));
       }
+    }
+  };
+  auto load_a = [&](int buf, int i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = (4 * i + wave) * 128 + 64 * h + piece;
+      const bool in = at < a.k;
 #pragma unroll
       for (int r = 0; r < RG; ++r)
         fa[buf][h][r] = __builtin_bit_cast(
@@ -697,8 +695,48 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
 #pragma unroll
     for (int c = 0; c < NB; ++c) acc[r][c] = i32x4_t{0, 0, 0, 0};
   const int lines = (a.k + 127) / 128, mine = (lines - wave + 3) / 4;  // of this wave
+  // all that is known by the expert first, then what waits for the rows' pairs
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) load(d, d);
+  for (int d = 0; d < kDepth; ++d) load_b(d, d);
+  // output block (r, c) of the columns: wave (r CB + c) % 4; lane l has row l & 15
+  // and columns 4 (l / 16) ..
+  constexpr int kMine = (RG * CB + 3) / 4;
+  float sr[kMine];
+  f32x4_t sc[kMine], su[kMine];
+  auto block_of = [&](int j, int& r, int& i, int& col) {
+    const int o = wave + 4 * j;
+    r = o / CB;
+    i = 16 * r + row;
+    col = 16 * (o % CB) + 4 * (lane >> 4);
+    return o < RG * CB && i < tile.rows && col < cols;
+  };
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    int r, i, col;
+    sc[j] = su[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (!block_of(j, r, i, col)) continue;
+    sc[j] = *reinterpret_cast<const f32x4_t*>(a.w_scales + w_row + col);
+    if (UP) su[j] = *reinterpret_cast<const f32x4_t*>(a.w_up_scales + w_row + col);
+  }
+  uint32_t a_row[RG];
+#pragma unroll
+  for (int r = 0; r < RG; ++r) {
+    a_row[r] = a.sorted_src ? min(max((int)pair[r], 0) / (uint32_t)a.K, (uint32_t)a.a_rows - 1u)
+                            : 16u * r + row;
+    a_off[r] = 16 * r + row < tile.rows ? a_row[r] * (uint32_t)a.k : kNoRow;
+  }
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load_a(d, d);
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    int r, i, col;
+    sr[j] = 0.0f;
+    if (!block_of(j, r, i, col)) continue;
+    uint32_t from = 0;
+#pragma unroll
+    for (int q = 0; q < RG; ++q) from = q == r ? a_row[q] : from;
+    sr[j] = a.a_scales[a.sorted_src ? (int64_t)from : tile.row0 + from];
+  }
   for (int i = 0; i < mine; i += kDepth) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
@@ -710,7 +748,9 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
           for (int r = 0; r < RG; ++r)
             acc[r][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[d][h][c], fa[d][h][r], acc[r][c],
                                                               0, 0, 0);
-      load(d, i + kDepth + d);  // past the wave's last line: zeros, without a memory access
+      // past the wave's last line: zeros, without a memory access
+      load_b(d, i + kDepth + d);
+      load_a(d, i + kDepth + d);
     }
   }
 #pragma unroll
@@ -718,29 +758,25 @@ __global__ __launch_bounds__(256, 2) void int8_few_kernel(Int8Args a, int col_ti
 #pragma unroll
     for (int c = 0; c < NB; ++c) sums[wave][r * NB + c][lane] = acc[r][c];
   __syncthreads();
-  // output block (r, c) of the columns: wave (r CB + c) % 4; lane l has row l & 15
-  // and columns 4 (l / 16) ..
-  for (int o = wave; o < RG * CB; o += 4) {
-    const int r = o / CB, c = o % CB;
-    const int i = 16 * r + row, col = 16 * c + 4 * (lane >> 4);
-    if (i >= tile.rows || col >= cols) continue;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    int r, i, col;
+    if (!block_of(j, r, i, col)) continue;
+    const int c = (wave + 4 * j) % CB;
     auto total = [&](int b) {
       i32x4_t t = sums[0][b][lane];
 #pragma unroll
       for (int w = 1; w < 4; ++w) t += sums[w][b][lane];
       return t;
     };
-    const float sr = a.a_scales[a_row_of(a, tile.row0 + i)];
-    const f32x4_t sc = *reinterpret_cast<const f32x4_t*>(a.w_scales + w_row + col);
     const i32x4_t g = total(r * NB + c);
     float y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = (float)g[j] * (sr * sc[j]);
+    for (int e = 0; e < 4; ++e) y[e] = (float)g[e] * (sr[j] * sc[j][e]);
     if constexpr (UP) {
-      const f32x4_t su = *reinterpret_cast<const f32x4_t*>(a.w_up_scales + w_row + col);
       const i32x4_t u = total(r * NB + CB + c);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = silu_mul(y[j], (float)u[j] * (sr * su[j]));
+      for (int e = 0; e < 4; ++e) y[e] = silu_mul(y[e], (float)u[e] * (sr[j] * su[j][e]));
     }
     *reinterpret_cast<u32x2_t*>(a.out + (tile.row0 + i) * a.cols + col0 + col) =
         u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};

@@ -44,3 +44,18 @@ def test_bind_refuses(M):
         _lib.calls.bind(*[0] * 8)
     with pytest.raises(TypeError):
         _lib.calls.bind(*["x"] * 8)
+
+
+def test_without_the_module(M, monkeypatch):
+    """A module that does not load leaves the way through Python, and says so."""
+    import sys
+    from sigmoid_top_routing_router_amd import _lib
+    monkeypatch.setitem(sys.modules, "sigmoid_top_routing_router_amd._calls", None)
+    monkeypatch.delattr(M, "_calls", raising=False)
+    with pytest.warns(UserWarning, match="twice the time"):
+        calls = _lib._bind_calls(M.load_library())
+    assert calls.permute(1, 2, 3, 4) is None
+    monkeypatch.setattr(_lib, "calls", calls)
+    pos = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="GPU torch tensor"):
+        M.group_tokens(pos, 3)
