@@ -913,6 +913,12 @@ def _kept(pair, name, shape):
     return codes, scales
 
 
+def _pair(rows):
+    """(codes, scales) as they are, rows with None in the place of scales."""
+    pair = isinstance(rows, (tuple, list)) and len(rows) == 2 and rows[1] is not None
+    return rows if pair else (rows, None)
+
+
 def _rows_flag(t):
     return _lib.MOE_ROWS_F32 if t.dtype == _torch().float32 else 0
 
@@ -926,8 +932,7 @@ def permute(x, grouping: Grouping, out=None, stream=None):
     torch = _torch()
     lib = _lib.load()
     if stream is None:
-        pair = x if isinstance(x, (tuple, list)) and len(x) == 2 else (x, None)
-        rows = _lib.calls.permute(*pair, grouping.src_pos, out)
+        rows = _lib.calls.permute(*_pair(x), grouping.src_pos, out)
         if rows is not None:
             return rows
     pos = _places(grouping)
@@ -1026,8 +1031,7 @@ def unpermute_backward(grad_y, grouping: Grouping, weights=None, rows=None, out=
     torch = _torch()
     lib = _lib.load()
     if stream is None:
-        pair = rows if isinstance(rows, (tuple, list)) and len(rows) == 2 else (rows, None)
-        r = _lib.calls.unpermute_backward(grad_y, grouping.src_pos, weights, *pair, out)
+        r = _lib.calls.unpermute_backward(grad_y, grouping.src_pos, weights, *_pair(rows), out)
         if r is not None:
             return r
     pos = _places(grouping)
@@ -1099,13 +1103,16 @@ def int8_matmul(x, w, w_up=None, grouping: Grouping = None, gather: bool = False
     are unspecified)."""
     torch = _torch()
     lib = _lib.load()
-    if stream is None and (grouping is not None or not gather):
-        up, by = (None, None) if w_up is None else w_up, grouping
-        r = _lib.calls.int8_matmul(
-            *x[:2], *w[:2], *up[:2], by and by.offsets, by.sorted_src if gather else None,
-            by and by.src_pos, out)
-        if r is not None:
-            return r
+    if stream is None:
+        # None in the place of a tensor that a given argument has to have: not ordinary
+        up = (None, None) if w_up is None else w_up if w_up[0] is not None else (x, x)
+        by = (None, None, None)
+        if grouping is not None:
+            by = grouping.offsets, grouping.sorted_src if gather else None, grouping.src_pos
+        if not gather or by[1] is not None:
+            r = _lib.calls.int8_matmul(*x, *w, *up, *by, out)
+            if r is not None:
+                return r
     a = _dev(x[0], "x codes", torch.int8)
     if a is None or a.dim() != 2:
         raise ValueError("x codes must be [n, k]")

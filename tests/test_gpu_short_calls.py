@@ -138,6 +138,13 @@ def test_what_is_not_ordinary_is_answered_by_python(M):
         (ValueError, lambda: M.int8_matmul((q[0], q[1][:-1]), (wq[0][0], wq[1][0]))),
         (ValueError, lambda: M.int8_matmul(q, wq)),
         (ValueError, lambda: M.int8_matmul(q, (wq[0][0], wq[1][0]), gather=True)),
+        (TypeError, lambda: M.permute((x, None), g)),
+        (TypeError, lambda: M.unpermute_backward(x, g, rows=(rows, None))),
+        (ValueError, lambda: M.int8_matmul(q, (wq[0][0], wq[1][0]), w_up=(None, None))),
+        (ValueError, lambda: M.int8_matmul(M.int8_quantize_rows(rows), wq, gather=True, grouping=(
+            M.Grouping(g.counts, g.offsets, None, g.src_pos.view(-1, 1))))),
+        (ValueError, lambda: M.int8_matmul(q, wq, grouping=M.Grouping(
+            g.counts, None, g.sorted_src, g.src_pos), gather=True)),
         (M.MoeError, lambda: M.int8_quantize_rows(x[:, :24].contiguous())),
         (M.MoeError, lambda: M.group_tokens(s["ids"].repeat(1, 3), 6)),
     ]
