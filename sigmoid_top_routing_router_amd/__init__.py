@@ -910,6 +910,11 @@ def _kept(pair, name, shape):
     scales = _dev(pair[1], f"{name} scales", torch.float32, (n, d // 128))
     if codes is None or scales is None:
         raise ValueError(f"{name}: codes and scales, both")
+    if d % 128:
+        # below 128 columns the scales are empty and have no address, by which the C
+        # entry would take the codes for rows of 16 bits and read past them
+        raise MoeError(_lib.MOE_ERR_UNSUPPORTED_SHAPE,
+                       f"d={d}: rows kept in 8 bits need a multiple of 128")
     return codes, scales
 
 
@@ -926,8 +931,8 @@ def _rows_flag(t):
 def permute(x, grouping: Grouping, out=None, stream=None):
     """Rows of tokens sorted by expert (moe_permute): rows[src_pos[t, k]] = x[t].
     x: [N, d] bf16 or fp32, or (codes, scales) of tokens kept in 8 bits
-    (``fp8_quantize_rows``, ``rms_norm(..., quantize=True)``), which gives bf16
-    rows.  Returns rows [N*K, d]; those from offsets[E] on keep what ``out``
+    (``fp8_quantize_rows``, ``rms_norm(..., quantize=True)``; d % 128 == 0),
+    which gives bf16 rows.  Returns rows [N*K, d]; those from offsets[E] on keep what ``out``
     held (without it they are unspecified)."""
     torch = _torch()
     lib = _lib.load()
@@ -1023,7 +1028,8 @@ def unpermute_backward(grad_y, grouping: Grouping, weights=None, rows=None, out=
                        stream=None):
     """Gradients of unpermute (moe_unpermute_backward).  grad_y: [N, d] bf16 or
     fp32 (it is base's gradient as it is); rows: the forward call's [N*K, d], or
-    the (codes, scales) that it kept; None: no gradient of the weights.
+    the (codes, scales) that it kept (d % 128 == 0); None: no gradient of the
+    weights.
 
     Returns (grad_rows [N*K, d] in the type of grad_y, grad_weights fp32 [N, K]
     or None); grad_rows from offsets[E] on keep what ``out`` held (without it

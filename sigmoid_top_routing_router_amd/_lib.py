@@ -14,6 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_mi355x.so")
 
 MOE_OK = 0
+MOE_ERR_UNSUPPORTED_SHAPE = 2
 MOE_RECOMPUTE_BIAS = 0x1
 MOE_KEY32 = 0x2
 MOE_PACKED_GATEUP = 0x4

@@ -122,6 +122,14 @@ PyObject* ordinary(Py_ssize_t have, Py_ssize_t n, F&& f) {
   Py_RETURN_NONE;
 }
 
+// The scales of n rows of d codes.  Below 128 columns they would be empty, and the C
+// entry tells codes from rows of 16 bits by the scales' address.
+void are_scales(const Arg& s, int64_t n, int64_t d, const Arg& first) {
+  if (!s) return;
+  need(d % 128 == 0);
+  s.is(at::kFloat, {n, d / 128}, first);
+}
+
 struct Places {
   Arg pos;
   int64_t N, K;
@@ -174,7 +182,7 @@ PyObject* permute(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::ScalarType type = x.type();
     if (xs) {
       need(type == at::kByte);
-      xs.is(at::kFloat, {at.N, d / 128}, x);
+      are_scales(xs, at.N, d, x);
       type = out ? out.type() : at::kBFloat16;
       need(bf16_bits(type));
     } else {
@@ -250,7 +258,7 @@ PyObject* unpermute_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t d = g->size(1), P = at.N * at.K;
     w.is(at::kFloat, {at.N, at.K}, g);
     rows.is(rs ? at::kByte : g.type(), {P, d}, g);
-    rs.is(at::kFloat, {P, d / 128}, g);
+    are_scales(rs, P, d, g);
     out.is(g.type(), {P, d}, g);
     void* stream = stream_of(g);
     const at::Tensor dr = out ? *out.t : empty(g, g.type(), {P, d});

@@ -1,0 +1,39 @@
+"""Calls that are refused before any launch, the short way (no stream given) and the
+way through Python (a stream given) alike."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def M():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import sigmoid_top_routing_router_amd as M
+    M.load_library()
+    return M
+
+
+def both_ways(call, kind, match):
+    import torch
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(kind, match=match):
+            call(stream)
+
+
+@pytest.mark.parametrize("d", [1, 64, 127, 192])
+def test_codes_of_rows_without_whole_groups(M, d):
+    import torch
+
+    def kept(n):
+        return (torch.zeros(n, d, dtype=torch.uint8, device="cuda"),
+                torch.zeros(n, d // 128, device="cuda"))
+    g = M.group_tokens(torch.tensor([[0, 1], [1, 2], [2, 0]], dtype=torch.int32, device="cuda"), 3)
+    dy = torch.zeros(3, d, dtype=torch.bfloat16, device="cuda")
+    both_ways(lambda s: M.permute(kept(3), g, stream=s), M.MoeError, "multiple of 128")
+    both_ways(lambda s: M.unpermute_backward(dy, g, rows=kept(6), stream=s), M.MoeError,
+              "multiple of 128")
+    rows = torch.zeros(6, d, dtype=torch.bfloat16, device="cuda")
+    both_ways(lambda s: M.unpermute(rows, g, checkpoint=True, stream=s), M.MoeError,
+              "multiple of 128")
