@@ -1115,7 +1115,7 @@ def int8_matmul(x, w, w_up=None, grouping: Grouping = None, gather: bool = False
         by = (None, None, None)
         if grouping is not None:
             by = grouping.offsets, grouping.sorted_src if gather else None, grouping.src_pos
-        if not gather or by[1] is not None:
+        if (grouping is None or by[0] is not None) and (not gather or by[1] is not None):
             r = _lib.calls.int8_matmul(*x, *w, *up, *by, out)
             if r is not None:
                 return r

@@ -37,3 +37,13 @@ def test_codes_of_rows_without_whole_groups(M, d):
     rows = torch.zeros(6, d, dtype=torch.bfloat16, device="cuda")
     both_ways(lambda s: M.unpermute(rows, g, checkpoint=True, stream=s), M.MoeError,
               "multiple of 128")
+
+
+def test_a_grouping_without_tensors_is_no_dense_product(M):
+    import torch
+    q = torch.zeros(4, 32, dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
+    w = torch.zeros(8, 32, dtype=torch.int8, device="cuda"), torch.zeros(8, device="cuda")
+    none = M.Grouping(None, None, None, None)
+    both_ways(lambda s: M.int8_matmul(q, w, grouping=none, stream=s), ValueError, "expected")
+    both_ways(lambda s: M.int8_matmul(q, (w[0][None], w[1][None]), grouping=none, stream=s),
+              ValueError, "src_pos must be")

@@ -43,3 +43,24 @@ def test_codes_of_rows_without_whole_groups(M, d):
         with pytest.raises(M.MoeError, match="multiple of 128") as e:
             call()
         assert e.value.status == 2
+
+
+def test_a_grouping_without_tensors_is_no_dense_product(M, monkeypatch):
+    """The extension module takes None in the place of offsets and places for a dense
+    product, so a grouping that holds neither may not reach it."""
+    from sigmoid_top_routing_router_amd import _lib
+
+    class Dense:
+        def int8_matmul(self, *args):
+            return "a dense product"
+    monkeypatch.setattr(_lib, "calls", Dense())
+    q, w = (torch.zeros(4, 32, dtype=torch.int8), torch.zeros(4)), \
+        (torch.zeros(8, 32, dtype=torch.int8), torch.zeros(8))
+    assert M.int8_matmul(q, w) == "a dense product"
+    for g in (M.Grouping(None, None, None, None),
+              M.Grouping(None, None, torch.zeros(4, dtype=torch.int32), None)):
+        with pytest.raises(ValueError, match=r"expected \(E, cols, 32\)"):
+            M.int8_matmul(q, w, grouping=g)
+    w3 = (w[0].view(1, 8, 32), w[1].view(1, 8))
+    with pytest.raises(ValueError, match=r"src_pos must be \[N, K\]"):
+        M.int8_matmul(q, w3, grouping=M.Grouping(None, None, None, None))
