@@ -777,6 +777,7 @@ const char* moe_status_string(moe_status_t s);
 /* Detail of the last failed call on this thread ("" if none). */
 const char* moe_last_error_message(void);
 /* Version of this ABI (incremented on any incompatible change). */
+#define MOE_ABI_VERSION 2
 int32_t moe_abi_version(void);
 
 #ifdef __cplusplus

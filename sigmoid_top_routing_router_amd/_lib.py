@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import warnings
+from importlib.machinery import EXTENSION_SUFFIXES
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_mi355x.so")
@@ -227,10 +228,23 @@ class _LongWay:
         return lambda *args: None
 
 
+def built_for():
+    """The torch and the Python whose headers an extension module is built with."""
+    import torch
+    return f"torch {torch.__version__} {torch.version.git_version}, {EXTENSION_SUFFIXES[0]}"
+
+
 def _bind_calls(lib):
-    """The extension module with the short way to the small calls."""
+    """The extension module with the short way to the small calls.  A module that was
+    built with another torch, Python or C ABI may load all the same and read other
+    members than it means: it is left out as a missing one is."""
     try:
         from . import _calls
+        for name, have, want in (
+                ("built for", getattr(_calls, "built_for", None), built_for()),
+                ("of ABI", getattr(_calls, "abi_version", None), lib.moe_abi_version())):
+            if have != want:
+                raise ImportError(f"it is {name} {have}, here is {want}")
     except ImportError as e:
         warnings.warn(f"small calls take twice the time on the host: the binding's extension "
                       f"module is missing or was built for another torch ({e}); build it with "

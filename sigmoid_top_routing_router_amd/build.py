@@ -1,5 +1,5 @@
 """Build the gfx950 shared library libmoe_mi355x.so, and the binding's extension
-module _calls.so, in-tree with hipcc.
+module _calls, in-tree with hipcc.
 
     python -m sigmoid_top_routing_router_amd.build
 
@@ -13,11 +13,13 @@ import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
+from importlib.machinery import EXTENSION_SUFFIXES
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
+BINDING = os.path.join(HERE, "_calls" + EXTENSION_SUFFIXES[0])
 ARCH = "gfx950"
 
 HIPFLAGS = [
@@ -55,9 +57,12 @@ def build_binding(verbose: bool = False) -> str:
     import sysconfig
 
     from torch.utils.cpp_extension import include_paths, library_paths
-    out = os.path.join(HERE, "_calls.so")
+
+    from ._lib import built_for
+    out = BINDING
     cmd = [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", "/opt/rocm/include",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f'-DMOE_BUILT_FOR="{built_for()}"',
+           "-I", "/opt/rocm/include",
            *(f for p in include_paths() for f in ("-isystem", p)),
            "-I", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "binding", "calls.cpp"), "-o", out + ".tmp",

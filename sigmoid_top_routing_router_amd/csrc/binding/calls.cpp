@@ -384,4 +384,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Short calls of the bindi
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+// built_for and abi_version: what the binding compares with its own before it uses the
+// module, whose inlined code knows torch's tensors and the C entries by their layout.
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && (PyModule_AddStringConstant(m, "built_for", MOE_BUILT_FOR) < 0 ||
+            PyModule_AddIntConstant(m, "abi_version", MOE_ABI_VERSION) < 0))
+    Py_CLEAR(m);
+  return m;
+}

@@ -648,7 +648,7 @@ static moe_status_t forward_impl(const moe_problem_t* p, const Experts& ex, cons
 
 extern "C" {
 
-int32_t moe_abi_version(void) { return 2; }
+int32_t moe_abi_version(void) { return MOE_ABI_VERSION; }
 
 moe_status_t moe_stage_timing(int32_t enable) {
   if (enable < 0 || enable > 2) return fail(MOE_ERR_INVALID_ARGUMENT, "enable=%d outside [0, 2]", enable);
