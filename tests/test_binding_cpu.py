@@ -53,3 +53,30 @@ def test_another_library_is_not_called(lib, monkeypatch):
             return lib.moe_abi_version() + 1
     with pytest.warns(UserWarning, match="of ABI"):
         assert not is_short(_lib._bind_calls(Other()))
+
+
+def test_library_without_the_module(tmp_path, monkeypatch):
+    """Where the module does not build, the library does, and no older module stays."""
+    import ctypes
+    import os
+    import shutil
+
+    from sigmoid_top_routing_router_amd import build as B
+    if not os.path.exists("/opt/rocm/bin/hipcc") and shutil.which("hipcc") is None:
+        pytest.skip("no hipcc")
+    src = tmp_path / "one.cpp"
+    src.write_text('extern "C" int one() { return 1; }\n')
+    older = tmp_path / "_calls.so"
+    older.write_text("")
+
+    def no_headers(verbose=False):
+        raise RuntimeError("Python.h: no such file")
+    monkeypatch.setattr(B, "sources", lambda: [str(src)])
+    monkeypatch.setattr(B, "OBJ", str(tmp_path / "objects"))
+    monkeypatch.setattr(B, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(B, "BINDING", str(older))
+    monkeypatch.setattr(B, "build_binding", no_headers)
+    monkeypatch.setattr(B, "build_probes", lambda verbose=False: [])
+    with pytest.warns(UserWarning, match="Python.h: no such file"):
+        lib = B.build()
+    assert ctypes.CDLL(lib).one() == 1 and not older.exists()
