@@ -120,6 +120,10 @@ constexpr int kQuarter = 64 * kStage;        // 64 weight rows of a stage
 constexpr int kXcds = 8, kCus = 256;
 constexpr int kListed = 64;                  // tiles that a block works on, at most
 constexpr uint32_t kNoRow = 0xFFFFFFFFu - 256u * 1024u;  // past any buffer: the load gives zeros
+// ... with a place in the row added too (which alone is less than any buffer's bytes)
+static_assert(kInt8MaxGathered <= kNoRow && (uint64_t)256 * kInt8MaxDepth <= kNoRow &&
+                  (uint64_t)kNoRow + kInt8MaxDepth <= 0xFFFFFFFFu,
+              "kNoRow lies past a gathered a and past a tile's rows and weights");
 
 template <int MB>
 struct TileShape {

@@ -200,6 +200,7 @@ struct Int8Args {
   int k, cols, E, K;         // k % 16 == 0, cols % 8 == 0
 };
 constexpr uint64_t kInt8MaxGathered = 0xFFF80000u;  // bytes of an a that rows are picked from
+constexpr int kInt8MaxDepth = 65536;                // k
 hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream);
 
 // ---------------------------------------------------------------- diagnostics

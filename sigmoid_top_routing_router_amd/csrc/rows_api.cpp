@@ -13,7 +13,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxRows = kMaxTokens * MOE_MAX_K;
-constexpr int kMaxD = 8192, kMaxDepth = 65536;
+constexpr int kMaxD = 8192, kMaxDepth = moe::kInt8MaxDepth;
 
 bool group_sizes_ok(int64_t N, int32_t E, int32_t K) {
   return N >= 0 && N <= kMaxTokens && E >= 1 && E <= MOE_MAX_E && K >= 1 && K <= MOE_MAX_K;
