@@ -644,8 +644,8 @@ moe_status_t moe_backward(const moe_problem_t* p, const moe_weights_t* w, const 
  * (x, rows, y, base and their gradients alike).  0 <= N <= 2^24, 1 <= d <= 8192,
  * 1 <= K <= 8.  Rows that no pair has (from offsets[E] on) are neither read
  * nor written.  Sums are fp32 and rounded once.  bf16 buffers 2-byte, fp32
- * buffers 4-byte aligned; 16-byte aligned buffers and rows of whole 16-byte
- * words take the fast path.
+ * buffers 4-byte aligned.  Rows of 16 bytes and more move in pieces of 16 at any
+ * alignment, shorter ones by elements.
  *
  * Rows kept in 8 bits are E4M3 codes [n,d] with fp32 scales [n,d/128], as
  * moe_fp8_quantize_rows and moe_rms_norm write them: d % 128 == 0, not with
@@ -708,8 +708,9 @@ moe_status_t moe_unpermute_backward(const void* grad_y, const void* rows, const 
  * codes 16-byte aligned.
  *
  * moe_int8_matmul - out[r,c] = a_scales[s] w_scales[e,c] sum_k a[s,k] w[e,c,k],
- * the two scales' product formed first, in fp32 (so it must not underflow), and
- * the result rounded to bf16; with w_up silu(out) times the same of w_up, formed
+ * the two scales' product formed first, in fp32 (so it must neither underflow nor
+ * overflow: an infinite one makes a sum of 0 a NaN), and the result rounded to
+ * bf16; with w_up silu(out) times the same of w_up, formed
  * in fp32.
  *  a            [a_rows,k] integers (-128 too), a_scales [a_rows] fp32.
  *  w            [E,cols,k] integers, w_scales [E,cols] fp32; w_up, w_up_scales

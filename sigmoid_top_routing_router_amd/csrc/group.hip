@@ -18,9 +18,13 @@
 //  2. every block reads the whole table (at most kMaxBlocks rows), which gives
 //     each bucket's total and its pairs in earlier blocks, scans the totals in
 //     expert order, counts its own chunks, and walks them in order.
-// Latencies bound it, one call after the other: six pairs 3.5 us, 6185 5.0 (8.5 in
-// one block, which has four waves a SIMD walk through them), 24000 8.5 (9.9 in two
-// launches), 32768 9.9 (10.1 in one), 98304 10.8 (1.2 MB).  Sixteen waves a block keep
+// Latencies bound it, one call after the other in a graph, loads nearly level: six
+// pairs 3.7 us, 6185 5.0 (8.5 in one block, which has four waves a SIMD walk through
+// them), 24000 8.6 (9.9 in two launches), 32768 9.9 (10.1 in one), 98304 11.1 (1.2 MB).
+// The counts are LDS atomics by bucket, so pairs of one bucket wait for each other:
+// 6185 pairs of which half have no expert here 6.8, all with one expert 9.2; 24576 with
+// one expert 25 (every block counts them all), 98304 17, 393216 24 (level 15.6).  Every
+// token with the same six or five experts costs 0.1 to 0.7 us.  Sixteen waves a block keep
 // the table short and the walks shorter: with four (the layer's form, which also makes
 // the GEMMs' tile table) 98304 pairs take 14.4 us.
 #include <algorithm>

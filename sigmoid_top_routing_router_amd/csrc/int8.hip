@@ -34,10 +34,12 @@ constexpr float kInt8Max = 127.0f;
 
 // Four integers.  The quotient v / s rounded to fp32 as q = v y, q + (v - s q) y
 // with y = 1 / s (three operations in the place of a division's; the residual is
-// exact, and the sum is the rounded quotient for each of the 2^14 pairs of
-// significands of v and of the largest value): half of the largest value is a tie
+// exact but for 9 of the 2^14 pairs of significands of v and of the largest value,
+// where it has 25 bits, and the sum is the rounded quotient for each of them, found
+// by trying all in exact arithmetic): half of the largest value is a tie
 // but for the rounding of s, and the product alone then misses the quotient's
-// integer.  divide: s is so small that the residual would not be exact.
+// integer.  divide: s is so small that the residual would lose bits below the
+// smallest subnormal.
 __device__ __forceinline__ uint32_t int8x4(const float (&v)[4], float s, float y, bool divide) {
   uint32_t c = 0;
 #pragma unroll
@@ -251,24 +253,33 @@ struct Buffer {
   }
 };
 
-// A block's tiles one after the other.  While a tile's results are scaled, rounded
-// and stored (straight from registers), the next tile's first stages are on their
-// way into LDS: a block to each tile spent 1.9 us on finding it, 4.4 until its first
-// products and 5.1 behind its last ones, next to 25 us of products.  98304 rows of
-// 384 experts, 2560 deep, 2 x 512 columns, tiles of 192 rows: 355 us that way, 344
-// this way; 2048 rows of 128 experts, 512 deep, 2560 columns: 41 and 32.
+// A block's tiles one after the other, found once: a block to each tile spent 1.9 us
+// on finding it, 4.4 until its first products and 5.1 behind its last ones, next to 25
+// us of products.  98304 rows of 384 experts, 2560 deep, 2 x 512 columns, tiles of 192
+// rows: 355 us that way, 344 this way; 2048 rows of 128 experts, 512 deep, 2560
+// columns: 41 and 32.
+//
+// The next tile's first stages are asked for in front of a tile's stores, but as
+// compiled they are not under way through them: the wait for the rows' scales takes
+// the strictest count of the paths that meet there, so the first store waits for
+// nearly all of these loads; the pairs of the results' rows, fetched behind the last
+// product, are waited for before the first of them; and MB 4 keeps 10 or 11 registers
+// in scratch, the weights' offsets among them, whose reloads between these loads wait
+// for the ones before.  About 9 tiles a block pay that in the product above.
 //
 // What bounds it: dense, the power of the matrix instructions (8192 x 8192 x 8192:
-// 405 us, 2.7 POP/s, in use 71% of the time at 1.7 GHz); few rows an expert, the
-// weights' way from HBM (64 tokens of six among 384 experts: 0.64 GB in 97 us, 6.6
-// TB/s); many rows of many experts, both in part.  The 98304 rows above, 22 to 1243 an
-// expert: 339 us in tiles of 256, the same loads without products 304, from L2 with
-// products 265, products alone 210; 256 rows an expert: 298, 266, 233 and 186.  Tiles
-// in descending size, dealt so that all blocks end together, were no faster: a block
-// that ends early leaves its share of both to the others.
+// 405 to 422 us, 2.6 to 2.7 POP/s, in use 71% of the time at 1.7 GHz); few rows an
+// expert, the weights' way from HBM (64 tokens of six among 384 experts: 0.64 GB in 97
+// to 101 us, 6.4 to 6.6 TB/s); many rows of many experts, both in part, and what the
+// change of tiles above costs, which is in all of these figures.  The 98304 rows above,
+// 22 to 1243 an expert: 339 us in tiles of 256 (355 to 395 in a long row, as the clock
+// falls), the same loads without products 304, from L2 with products 265, products
+// alone 210; 256 rows an expert: 298, 266, 233 and 186.  Tiles in descending size,
+// dealt so that all blocks end together, were no faster.
 //
 // The results go past the caches (98304 rows, 512 deep, 2560 columns: 287 us without,
-// 281 so).  ONCE: so do the weights.
+// 281 so, of 206 that its bytes would take at a copy's rate: a tile is four stages of
+// products, and a block changes tiles about 23 times).  ONCE: so do the weights.
 template <int MB, bool UP, bool ONCE>
 __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, char* lds) {
   typedef TileShape<MB> S;
@@ -304,8 +315,8 @@ __device__ __forceinline__ void int8_tiles(const Int8Args& a, const List& list, 
   Tile tile;
   int col0, cols;
   // The pairs of the rows of A that the wave loads (a_pair) and of those whose
-  // results it holds (r_pair), all loads at once and none waited for here; a row
-  // past the tile gives its last one's.
+  // results it holds (r_pair), all loads at once; a row past the tile gives its last
+  // one's.
   auto pairs_of = [&](const Tile& t, auto row, uint32_t(&pair)[MB]) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
@@ -923,11 +934,15 @@ double expected_tiles(const Int8Args& a, int bm) {
   const double experts = (double)std::min<int64_t>(a.E, a.rows), share = (double)a.rows / experts;
   return experts * std::max(1.0, share / bm + 0.5);
 }
-// Microseconds of a launch, by a fit to what shapes from 1 to 16384 rows, 512 to
-// 8192 deep, took dense and with 16 to 384 experts (within a fifth of most).
+// A launch's cost, to rank the forms: a fit to the microseconds of shapes from 1 to
+// 16384 rows, 512 to 8192 deep, dense and with 16 to 384 experts.  The shortest launches
+// are within a fifth of it, those of 30 us take up to half as much again (4096 rows of
+// 2560 x 2560 22 for 30; 2048 of 128 experts 21 for 31), long ones twice, as neither memory's share nor the falling clock is in it (98304
+// rows of 2560, 2 x 512 columns: 243 for 339; of 512, 2560 columns: 144 for 282; 64 rows
+// an expert: 110 for 214; 8192 x 8192 x 8192: 289 for 417), so that between MB 3 and 4 it
+// ranks by less than it is off.  Rows are all N K, pairs without an expert here too.
 // Tiles: 0.22 (MB + 1) a stage and 1 a tile, 256 at a time; experts' weights that no
-// more than a tile or two share slow a stage by 0.18 where memory is busy for more
-// than one round.
+// more than a tile or two share slow a stage by 0.18 where there is more than one round.
 double tile_cost(const Int8Args& a, int mb) {
   const double rounds = std::ceil(expected_tiles(a, 64 * mb) * column_tiles(a) / kCus);
   const double stage = 0.22 * (mb + 1) + (a.offsets && rounds > 1 ? 0.18 : 0.0);
@@ -950,7 +965,7 @@ double few_cost(const Int8Args& a, int rg, int cb) {
 // The cheapest form by the fits above.  2560 x 2560 weights, us: 1 row 4.8 (few,
 // 1 x 1; tiles of MB 1 11.7), 64 rows 8.5 (few, 2 x 2; 11.7), 512 rows 12.7 (MB 1;
 // MB 4 27, few-row blocks of 64 x 64 25), 4096 rows 29 (MB 3; MB 1 42); 8192 x 8192 x
-// 8192 405 (MB 4; MB 2 449).
+// 8192 405 to 422 (MB 4; MB 2 449).
 hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream) {
   typedef hipError_t (*Launch)(const Int8Args&, hipStream_t);
   struct Form {

@@ -110,10 +110,11 @@ __device__ __forceinline__ void open_codes(u32x2_t c, float s, float (&f)[8]) {
 }
 
 // quant8 of fp8_codes.h, with the quotients v / s as q = v y, q + (v - s q) y, y =
-// 1 / s: three operations for the division's ten.  The residual is exact, and the sum
-// is the rounded quotient for each of the 2^14 pairs of significands of v and of the
-// group's maximum.  divide: s is infinite, or so small that the residual would not be
-// exact.  16384 tokens of 2560, six each, with codes: 187 us with divisions, 155 so.
+// 1 / s: three operations for the division's ten.  The residual is exact but for 35 of
+// the 2^14 pairs of significands of v and of the group's maximum, where it has 25 bits;
+// the sum is the rounded quotient for each of them (all tried in exact arithmetic).
+// divide: s is infinite, or so small that the residual would lose bits below the
+// smallest subnormal.  16384 tokens of 2560, six each, with codes: 187 us with divisions, 155 so.
 __device__ __forceinline__ uint2 quant8_by(uint4 v, float s, float y, bool divide) {
   if (divide) return quant8(v, s);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
