@@ -123,6 +123,15 @@ def _one_device(first, **others):
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
+def _given_workspace(first, workspace):
+    """A given workspace lies on first's device, and the bytes that its size says
+    follow each other from its address on."""
+    if workspace is not None:
+        _one_device(first, workspace=workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+
+
 @functools.lru_cache(maxsize=None)
 def _bf16():
     torch = _torch()
@@ -221,6 +230,7 @@ def eqb_bias(logits, K: int, beta_in=None, alpha=None, key_bits: int = 16,
     N, E = logits.shape
     beta_in = _dev(beta_in, "beta_in", torch.float32, (E,))
     alpha = _dev(alpha, "alpha", torch.float32, (N,))
+    _given_workspace(logits, workspace)
     with _on(stream):
         need = int(lib.moe_eqb_workspace_bytes(N, E, key_bits))
         if workspace is None:
@@ -451,6 +461,7 @@ def _run_forward(fp8, x, wstruct, N, d, E, K, h, n_shared, h_shared, beta_in, re
     beta_in = _dev(beta_in, "beta_in", torch.float32, (E,))
     logit_offset = _dev(logit_offset, "logit_offset", torch.float32, (E,))
     logits_in = _dev(logits_in, "logits_in", torch.float32, (N, E))
+    _given_workspace(x, workspace)
     flags = (MOE_RECOMPUTE_BIAS if recompute_bias else 0) | (MOE_KEY32 if key_bits == 32 else 0)
     p = _problem(N, d, E, K, h, n_shared, h_shared, flags | extra_flags, logit_offset, logits_in)
     ws_fn = lib.moe_forward_fp8_workspace_bytes if fp8 else lib.moe_forward_workspace_bytes
@@ -627,7 +638,8 @@ def backward(grad_y, x, weights: ExpertWeights, logits, topk_ids, grad_logits=No
         raise ValueError("inplace needs grad_logits")
     names = [f for f, _ in MoeWeights._fields_ if getattr(weights, f) is not None]
     _one_device(x, grad_y=grad_y, logits=logits, topk_ids=topk_ids, grad_logits=grad_logits,
-                workspace=workspace, **{f: getattr(weights, f) for f in names})
+                **{f: getattr(weights, f) for f in names})
+    _given_workspace(x, workspace)
     p = _problem(N, d, E, K, h, n_shared, h_shared, 0, None, None)
     with _on_device(x, stream):
         dev = x.device
@@ -722,7 +734,8 @@ def rms_norm_backward(grad_y, r, weight, eps: float = 1e-6, grad_residual=None, 
     if (x is None) != (post_weight is None):
         raise ValueError("x belongs to post_weight: both or neither")
     _one_device(grad_y, weight=weight, post_weight=post_weight, r=r, grad_residual=grad_residual,
-                x=x, workspace=workspace)
+                x=x)
+    _given_workspace(grad_y, workspace)
     f32 = r.dtype == torch.float32
     if f32:
         flags |= _lib.MOE_NORM_STREAM_F32
@@ -795,7 +808,8 @@ def balance_loss(logits, topk_ids=None, coef: float = 1e-2, score: str = "sigmoi
     counts = _dev(counts, "counts", torch.int32, (n_seg, E))
     if topk_ids is None and counts is None:
         raise ValueError("topk_ids or counts is required")
-    _one_device(logits, topk_ids=topk_ids, counts=counts, workspace=workspace)
+    _one_device(logits, topk_ids=topk_ids, counts=counts)
+    _given_workspace(logits, workspace)
     which = _score(score)
     with _on_device(logits, stream):
         dev = logits.device
@@ -873,7 +887,7 @@ def group_tokens(topk_ids, E: int, workspace=None, stream=None) -> Grouping:
     if topk_ids is None or topk_ids.dim() != 2:
         raise ValueError("topk_ids must be [N, K]")
     N, K = topk_ids.shape
-    _one_device(topk_ids, workspace=workspace)
+    _given_workspace(topk_ids, workspace)
     need = _group_workspace(N, E, K) if workspace is None else 0
     with _on_device(topk_ids, stream):
         # one allocation for the four outputs and the workspace: 3 us less a call on

@@ -47,3 +47,22 @@ def test_a_grouping_without_tensors_is_no_dense_product(M):
     both_ways(lambda s: M.int8_matmul(q, w, grouping=none, stream=s), ValueError, "expected")
     both_ways(lambda s: M.int8_matmul(q, (w[0][None], w[1][None]), grouping=none, stream=s),
               ValueError, "src_pos must be")
+
+
+def test_a_workspace_elsewhere_or_expanded(M):
+    import torch
+    N, d, E, K, h = 4, 64, 3, 2, 32
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device="cuda")
+    x, logits, ids = z(N, d), z(N, E, t=torch.float32), z(N, K, t=torch.int32)
+    W = M.ExpertWeights(w_router=z(E, d), w_gate=z(E, h, d), w_up=z(E, h, d), w_down=z(E, d, h))
+    calls = (lambda ws, s: M.eqb_bias(logits, K, workspace=ws, stream=s),
+             lambda ws, s: M.forward(x, W, K, workspace=ws, stream=s),
+             lambda ws, s: M.backward(x, x, W, logits, ids, workspace=ws, stream=s),
+             lambda ws, s: M.rms_norm_backward(x, x, z(d), workspace=ws, stream=s),
+             lambda ws, s: M.balance_loss(logits, ids, workspace=ws, stream=s),
+             lambda ws, s: M.group_tokens(ids, E, workspace=ws, stream=s))
+    for call in calls:
+        both_ways(lambda s: call(torch.zeros(1 << 20, dtype=torch.uint8), s), ValueError,
+                  "workspace is on cpu")
+        both_ways(lambda s: call(z(256, t=torch.uint8)[:1].expand(1 << 20), s), ValueError,
+                  "workspace must be contiguous")

@@ -64,3 +64,25 @@ def test_a_grouping_without_tensors_is_no_dense_product(M, monkeypatch):
     w3 = (w[0].view(1, 8, 32), w[1].view(1, 8))
     with pytest.raises(ValueError, match=r"src_pos must be \[N, K\]"):
         M.int8_matmul(q, w3, grouping=M.Grouping(None, None, None, None))
+
+
+def test_a_workspace_has_the_bytes_that_it_says(M):
+    """An expanded tensor's size is not the memory behind its address."""
+    N, d, E, K, h = 4, 64, 3, 2, 32
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)
+    x, logits, ids = z(N, d), z(N, E, t=torch.float32), z(N, K, t=torch.int32)
+    W = M.ExpertWeights(w_router=z(E, d), w_gate=z(E, h, d), w_up=z(E, h, d), w_down=z(E, d, h))
+    calls = {
+        "eqb_bias": lambda ws: M.eqb_bias(logits, K, workspace=ws),
+        "forward": lambda ws: M.forward(x, W, K, workspace=ws),
+        "backward": lambda ws: M.backward(x, x, W, logits, ids, workspace=ws),
+        "rms_norm_backward": lambda ws: M.rms_norm_backward(x, x, z(d), workspace=ws),
+        "balance_loss": lambda ws: M.balance_loss(logits, ids, workspace=ws),
+        "group_tokens": lambda ws: M.group_tokens(ids, E, workspace=ws),
+    }
+    small = torch.zeros(256, dtype=torch.uint8)
+    for name, call in calls.items():
+        for ws in (small[:1].expand(1 << 20), torch.zeros(1 << 16, 2, dtype=torch.uint8)[:, 0]):
+            with pytest.raises(ValueError, match="workspace must be contiguous"):
+                call(ws)
+                pytest.fail(name)
